@@ -29,6 +29,9 @@ TG_OP_LORA_DOWN, TG_OP_LORA_UP, TG_OP_LORA_GRAD, TG_OP_BMM_ATTN = 3, 4, 5, 6
 TG_OP_LORA_DOWN_F32W, TG_OP_LORA_UP_F32W, TG_OP_LORA_GRAD_F32W = 7, 8, 9
 TG_OP_ATTN_BWD = 10
 TG_OP_GEMM_FWD_LORA, TG_OP_GEMM_DGRAD_LORA = 11, 12
+TG_OP_GROUPED_FWD, TG_OP_GROUPED_DGRAD, TG_OP_GROUPED_WGRAD, TG_OP_GROUPED_UNALIGNED = 13, 14, 15, 16
+TG_OP_NORM_RESIDUAL_BWD, TG_OP_GRAD_CLIP = 17, 18
+TG_GATE_NONE, TG_GATE_CHANNEL, TG_GATE_TOKEN, TG_GATE_FULL = 0, 1, 2, 3
 ATTN_OPS = {"qk": 0, "pv": 1, "do_vt": 2, "pt_do": 3, "ds_k": 4, "dst_q": 5}
 SIZE_MAX = (1 << 64) - 1
 
@@ -57,6 +60,15 @@ SIGNATURES = {
     "tg_lora_grad_add": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, ctypes.c_float,
                               _i, _i, _vp, _sz, _vp]),
     "tg_bmm_attn": (_i, [_i, _vp, _vp, _vp, _i64, _i64, _i64, _i, _i, _vp, _sz, _vp]),
+    "tg_grouped_fwd": (_i, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i, _i, _vp, _sz, _vp]),
+    "tg_grouped_dgrad": (_i, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i, _i, _vp, _sz, _vp]),
+    "tg_grouped_wgrad": (_i, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i, _i, _vp, _sz, _vp]),
+    "tg_norm_residual_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i64, _i64, ctypes.c_float,
+                                  ctypes.c_float, _i, _i, _vp]),
+    "tg_norm_residual_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
+                                  ctypes.c_float, _i, _i, _i, _vp, _sz, _vp]),
+    "tg_grad_norm": (_i, [_vp, _vp, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "tg_grad_clip": (_i, [_vp, _vp, _vp, _vp, _i64, ctypes.c_float, _vp, _vp, _sz, _vp]),
     "tg_workspace_size": (_sz, [_i, _i64, _i64, _i64, _i64, _i, _i]),
     "tg_stream_status": (_i, [_vp]),
     "tg_status_string": (ctypes.c_char_p, [_i]),
@@ -473,6 +485,213 @@ def tg_bmm_attn(op, A, B, C=None, out_dtype=None, ws=None, stream=None):
                              _stream(stream)), "tg_bmm_attn")
     _keep(keep, stream)
     return C
+
+
+def _grouped(name, op, A, B, W_shape, offsets, rows, out_arg, out_shape, out_name, out_dtype, ws, stream):
+    """A, B: the two operands as the C entry point takes them; W_shape: (E, d_out, d_in)."""
+    E, d_out, d_in = W_shape
+    if not isinstance(offsets, torch.Tensor) or offsets.device != A.device or offsets.dtype != torch.int32 \
+            or tuple(offsets.shape) != (E + 1,) or not offsets.is_contiguous():
+        raise ValueError(f"offsets must be a contiguous int32 tensor of {E + 1} values on the operands' device")
+    if B.device != A.device:
+        raise ValueError("the operands must be on one device")
+    C = _out(out_arg, out_shape, out_dtype or getattr(out_arg, "dtype", A.dtype), A.device, out_name)
+    if C.device != A.device:
+        raise ValueError(f"{out_name} must be on the operands' device")
+    din, dout = _DT.get(A.dtype, -1), _DT.get(C.dtype, -1)
+    wp, wn, keep = ctypes.c_void_p(0), 0, None
+    # rows of whole 16-byte words at 16-byte aligned bases need no workspace
+    aligned = (A.data_ptr() | B.data_ptr()) % 16 == 0
+    if not aligned or d_in % 8 or d_out % 8:
+        wp, wn, keep = _workspace(op if aligned else TG_OP_GROUPED_UNALIGNED, (rows, E, d_out, d_in), din, dout, ws,
+                                  A.device)
+    _check(getattr(lib(), name)(_ptr(A), _ptr(B), ctypes.c_void_p(offsets.data_ptr()), _ptr(C), rows, E, d_out, d_in,
+                                din, dout, wp, wn, _stream(stream)), name)
+    if keep is not ws:
+        _keep(keep, stream)
+    return C
+
+
+def tg_grouped_fwd(X, W, offsets, Y=None, out_dtype=None, ws=None, stream=None):
+    """Y[t] = X[t] W[e]^T for the rows offsets[e] <= t < offsets[e + 1] of expert e, zeros in rows of no
+    expert: X [T, d_in], W [E, d_out, d_in], offsets [E + 1] int32 on the device."""
+    _need(X, "X", 2), _need(W, "W", 3)
+    T, d_in = X.shape
+    if W.shape[2] != d_in or W.dtype != X.dtype:
+        raise ValueError("W must be [E, d_out, d_in] with X's dtype")
+    return _grouped("tg_grouped_fwd", TG_OP_GROUPED_FWD, X, W, W.shape, offsets, T, Y, (T, W.shape[1]), "Y", out_dtype,
+                    ws, stream)
+
+
+def tg_grouped_dgrad(dY, W, offsets, dX=None, out_dtype=None, ws=None, stream=None):
+    """dX[t] = dY[t] W[e] for the rows of expert e, zeros in rows of no expert: dY [T, d_out],
+    W [E, d_out, d_in], offsets [E + 1] int32 on the device."""
+    _need(dY, "dY", 2), _need(W, "W", 3)
+    T, d_out = dY.shape
+    if W.shape[1] != d_out or W.dtype != dY.dtype:
+        raise ValueError("W must be [E, d_out, d_in] with dY's dtype")
+    return _grouped("tg_grouped_dgrad", TG_OP_GROUPED_DGRAD, dY, W, W.shape, offsets, T, dX, (T, W.shape[2]), "dX",
+                    out_dtype, ws, stream)
+
+
+def tg_grouped_wgrad(dY, X, offsets, dW=None, out_dtype=None, ws=None, stream=None):
+    """dW[e] = sum over the rows t of expert e of dY[t]^T X[t] (zeros for an expert without rows):
+    dY [T, d_out], X [T, d_in], offsets [E + 1] int32 on the device; dW [E, d_out, d_in]."""
+    _need(dY, "dY", 2), _need(X, "X", 2)
+    T, d_out = dY.shape
+    if X.shape[0] != T or X.dtype != dY.dtype:
+        raise ValueError("X must be [T, d_in] with dY's dtype")
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be a 1-d tensor of E + 1 values")
+    shape = (offsets.shape[0] - 1, d_out, X.shape[1])
+    return _grouped("tg_grouped_wgrad", TG_OP_GROUPED_WGRAD, dY, X, shape, offsets, T, dW, shape, "dW", out_dtype, ws,
+                    stream)
+
+
+def _gate_kind(gate, T, d, dtype, device):
+    if gate is None:
+        return TG_GATE_NONE
+    kind = {(d,): TG_GATE_CHANNEL, (T, 1): TG_GATE_TOKEN, (T, d): TG_GATE_FULL}.get(tuple(gate.shape))
+    if kind is None or gate.dtype != dtype or gate.device != device or not gate.is_contiguous():
+        raise ValueError("gate must be a contiguous [d], [T, 1] or [T, d] tensor with B's dtype on B's device")
+    return kind
+
+
+def _need_like(t, name, shape, dtype, device):
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape) \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on {device}")
+    return t
+
+
+def _out_like(t, name, shape, dtype, device):
+    return torch.empty(shape, dtype=dtype, device=device) if t is None else _need_like(t, name, shape, dtype, device)
+
+
+def tg_norm_residual_fwd(B, H, w_post, w_pre, gate=None, res_scale=1.0, eps=1e-6, outs=None, stream=None):
+    """u = B rstd_b w_post, H_out = res_scale H + gate u, N = H_out rstd_h w_pre with rstd = (mean square + eps)^-1/2
+    over the row: B, H [T, d], w_post, w_pre [d], gate None, [d], [T, 1] or [T, d].  H may be FP32 beside 16-bit B.
+    Returns {"H", "N", "rstd_b", "rstd_h"} (outs may give any of them; outs["H"] may be H)."""
+    _need(B, "B", 2)
+    T, d = B.shape
+    dev, dt = B.device, B.dtype
+    if not isinstance(H, torch.Tensor) or H.dtype not in (dt, torch.float32):
+        raise ValueError("H must have B's dtype or FP32")
+    _need_like(H, "H", (T, d), H.dtype, dev)
+    _need_like(w_post, "w_post", (d,), dt, dev)
+    _need_like(w_pre, "w_pre", (d,), dt, dev)
+    kind = _gate_kind(gate, T, d, dt, dev)
+    outs = outs or {}
+    res = {"H": _out_like(outs.get("H"), "H", (T, d), H.dtype, dev), "N": _out_like(outs.get("N"), "N", (T, d), dt, dev),
+           "rstd_b": _out_like(outs.get("rstd_b"), "rstd_b", (T,), torch.float32, dev),
+           "rstd_h": _out_like(outs.get("rstd_h"), "rstd_h", (T,), torch.float32, dev)}
+    _check(lib().tg_norm_residual_fwd(_ptr(B), _ptr(H), _ptr(w_post), _ptr(w_pre), _ptr(gate), kind, _ptr(res["H"]),
+                                      _ptr(res["N"]), _ptr(res["rstd_b"]), _ptr(res["rstd_h"]), T, d, float(res_scale),
+                                      float(eps), _DT.get(dt, -1), _DT.get(H.dtype, -1), _stream(stream)),
+           "tg_norm_residual_fwd")
+    return res
+
+
+def tg_norm_residual_bwd(dH_out, dN, B, H_out, w_post, w_pre, rstd_b, rstd_h, gate=None, res_scale=1.0, out_dtype=None,
+                         outs=None, ws=None, stream=None):
+    """Gradients of <dH_out, H_out> + <dN, N> for the forward of tg_norm_residual_fwd: {"dB", "dH", "dw_post",
+    "dw_pre"} and "dgate" when there is a gate.  out_dtype (B's dtype or FP32): dw_post, dw_pre and the gradient
+    of a broadcast gate.  outs may give any of them."""
+    _need(B, "B", 2)
+    T, d = B.shape
+    dev, dt = B.device, B.dtype
+    if not isinstance(H_out, torch.Tensor) or H_out.dtype not in (dt, torch.float32):
+        raise ValueError("H_out must have B's dtype or FP32")
+    rt = H_out.dtype
+    _need_like(H_out, "H_out", (T, d), rt, dev)
+    _need_like(dH_out, "dH_out", (T, d), rt, dev)
+    _need_like(dN, "dN", (T, d), dt, dev)
+    _need_like(w_post, "w_post", (d,), dt, dev)
+    _need_like(w_pre, "w_pre", (d,), dt, dev)
+    _need_like(rstd_b, "rstd_b", (T,), torch.float32, dev)
+    _need_like(rstd_h, "rstd_h", (T,), torch.float32, dev)
+    kind = _gate_kind(gate, T, d, dt, dev)
+    outs = outs or {}
+    ot = out_dtype or (outs["dw_post"].dtype if "dw_post" in outs else dt)
+    res = {"dB": _out_like(outs.get("dB"), "dB", (T, d), dt, dev), "dH": _out_like(outs.get("dH"), "dH", (T, d), rt, dev),
+           "dw_post": _out_like(outs.get("dw_post"), "dw_post", (d,), ot, dev),
+           "dw_pre": _out_like(outs.get("dw_pre"), "dw_pre", (d,), ot, dev)}
+    dgate = None
+    if kind != TG_GATE_NONE:
+        dgate = res["dgate"] = _out_like(outs.get("dgate"), "dgate", gate.shape, dt if kind == TG_GATE_FULL else ot, dev)
+    din, dout = _DT.get(dt, -1), _DT.get(ot, -1)
+    wp, wn, keep = _workspace(TG_OP_NORM_RESIDUAL_BWD, (T, d, 0, 0), din, dout, ws, dev)
+    _check(lib().tg_norm_residual_bwd(_ptr(dH_out), _ptr(dN), _ptr(B), _ptr(H_out), _ptr(w_post), _ptr(w_pre), _ptr(gate),
+                                      kind, _ptr(rstd_b), _ptr(rstd_h), _ptr(res["dB"]), _ptr(res["dH"]),
+                                      _ptr(res["dw_post"]), _ptr(res["dw_pre"]), _ptr(dgate), T, d, float(res_scale), din,
+                                      _DT.get(rt, -1), dout, wp, wn, _stream(stream)), "tg_norm_residual_bwd")
+    if keep is not ws:
+        _keep(keep, stream)
+    return res
+
+
+class TGTensorList:
+    """Addresses, sizes and types of tensors, laid out once for tg_grad_norm and tg_grad_clip.  Keeps the
+    tensors alive; they must not be resized while it is used."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        for k, t in enumerate(self.tensors):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous() or t.dtype not in _DT:
+                raise ValueError(f"tensor {k} must be a contiguous bf16, fp16 or FP32 CUDA tensor")
+            if t.device != self.tensors[0].device:
+                raise ValueError("the tensors must be on one device")
+        n = len(self.tensors)
+        self.shape_key = [(t.numel(), t.dtype) for t in self.tensors]
+        self.pointers = (ctypes.c_void_p * n)(*[t.data_ptr() if t.numel() else 0 for t in self.tensors])
+        self.numels = (ctypes.c_int64 * n)(*[t.numel() for t in self.tensors])
+        self.dtypes = (ctypes.c_int32 * n)(*[_DT[t.dtype] for t in self.tensors])
+
+    def __len__(self):
+        return len(self.tensors)
+
+    def __iter__(self):
+        return iter(self.tensors)
+
+
+def tg_tensor_list(tensors) -> TGTensorList:
+    """A list of gradient tensors to hand to tg_grad_norm and tg_grad_clip step after step."""
+    return tensors if isinstance(tensors, TGTensorList) else TGTensorList(tensors)
+
+
+def _grad_args(grads, norm, ws):
+    g = tg_tensor_list(grads)
+    dev = g.tensors[0].device if len(g) else (norm.device if norm is not None else torch.device("cuda"))
+    norm = _out_like(norm, "norm", (1,), torch.float32, dev)
+    wp, wn, keep = _workspace(TG_OP_GRAD_CLIP, (len(g), 0, 0, 0), TG_F32, TG_F32, ws, dev)
+    return g, norm, wp, wn, keep
+
+
+def tg_grad_norm(grads, norm=None, ws=None, stream=None):
+    """The L2 norm of all the tensors' elements together, as one FP32 value on the device ([1])."""
+    g, norm, wp, wn, keep = _grad_args(grads, norm, ws)
+    _check(lib().tg_grad_norm(g.pointers, g.numels, g.dtypes, len(g), _ptr(norm), wp, wn, _stream(stream)),
+           "tg_grad_norm")
+    if keep is not ws:
+        _keep(keep, stream)
+    return norm
+
+
+def tg_grad_clip(grads, max_norm, outs=None, norm=None, ws=None, stream=None):
+    """Scale every tensor by min(1, max_norm / (norm + 1e-6)), norm the L2 norm of all their elements together:
+    in place, or into outs (tensors of the same types and sizes).  grads and outs: tensors, or lists laid out
+    once with tg_tensor_list.  Returns the norm (before scaling), one FP32 value on the device ([1])."""
+    g, norm, wp, wn, keep = _grad_args(grads, norm, ws)
+    o = g if outs is None else tg_tensor_list(outs)
+    if o is not g and o.shape_key != g.shape_key:
+        raise ValueError("outs must match the gradients' sizes and dtypes one by one")
+    if o is not g and len(o) and o.tensors[0].device != g.tensors[0].device:
+        raise ValueError("outs must be on the gradients' device")
+    _check(lib().tg_grad_clip(g.pointers, o.pointers, g.numels, g.dtypes, len(g), float(max_norm), _ptr(norm), wp, wn,
+                              _stream(stream)), "tg_grad_clip")
+    if keep is not ws:
+        _keep(keep, stream)
+    return norm
 
 
 def tg_workspace_size(op, d0, d1, d2, d3, din, dout) -> int:

@@ -7,6 +7,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <chrono>
 #include <cmath>
@@ -18,6 +19,9 @@
 #include <unordered_map>
 
 #include "attn.h"
+#include "grad_clip.h"
+#include "grouped.h"
+#include "norm_residual.h"
 #include "ptx.cuh"
 #include "tg.h"
 #include "tg_internal.h"
@@ -1623,8 +1627,260 @@ tg_status tg_attn_bwd(const void* Q, const void* K, const void* V, const void* d
   return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
 }
 
+// ------------------------------------------------- products grouped by expert
+// rows stay below 2^31 with the kernels' tiles added
+static const int64_t kMaxRows = (int64_t(1) << 31) - 1024;
+
+static tg_status run_grouped(int op, const char* name, const void* A, const void* B, const int32_t* offsets, void* C,
+                             int64_t T, int64_t E, int64_t d_out, int64_t d_in, tg_dtype in, tg_dtype out, void* ws,
+                             size_t ws_bytes, void* stream) {
+  TG_TRY(check_common(in, out, {T, E, d_out, d_in}));
+  if (T > kMaxRows) return TG_ERR_INVALID_ARG;
+  const bool wgrad = op == 2;
+  TG_TRY(check_ptr(A, wgrad ? T * d_out : E * d_out * d_in, 2));
+  TG_TRY(check_ptr(B, T * (op == 1 ? d_out : d_in), 2));
+  TG_TRY(check_ptr(offsets, 1, 4));
+  const int64_t elems = wgrad ? E * d_out * d_in : T * (op == 1 ? d_in : d_out);
+  TG_TRY(check_ptr(C, elems, dt_bytes(out)));
+  DevCtx* ctx = nullptr;
+  TG_TRY(device_ctx(&ctx));
+  if (elems == 0) {
+    record(std::string(name) + " empty output: nothing to do");
+    return TG_OK;
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0 || E == 0 || d_out == 0 || d_in == 0) {  // an empty sum everywhere
+    record(std::string(name) + " empty reduction: zero fill");
+    return cudaMemsetAsync(C, 0, static_cast<size_t>(elems) * dt_bytes(out), st) == cudaSuccess ? TG_OK : TG_ERR_CUDA;
+  }
+  GroupedCall g{};
+  g.op = op;
+  g.A = A;
+  g.B = B;
+  g.offsets = offsets;
+  g.C = C;
+  g.T = T;
+  g.E = E;
+  g.d_out = d_out;
+  g.d_in = d_in;
+  g.in_kind = in == TG_BF16 ? EK_BF16 : EK_F16;
+  g.out_kind = out == TG_F32 ? EK_F32 : g.in_kind;
+  g.ws = ws;
+  g.ws_bytes = ws_bytes;
+  g.num_sms = ctx->sms;
+  g.status = ctx->status;
+  g.timeout_ns = ctx->timeout_ns;
+  g.stream = st;
+  size_t need = 0;
+  const cudaError_t e = grouped_launch(g, &need);
+  if (need > 0) {
+    record(std::string(name) + ": workspace " + std::to_string(need) + " bytes needed (16-byte aligned), " +
+           std::to_string(ws ? ws_bytes : 0) + " given");
+    return TG_ERR_WORKSPACE_TOO_SMALL;
+  }
+  record(std::string(name) + " tc T=" + std::to_string(T) + " E=" + std::to_string(E) + " d_out=" +
+         std::to_string(d_out) + " d_in=" + std::to_string(d_in) + " " +
+         (e == cudaSuccess ? "ok" : cudaGetErrorString(e)));
+  return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
+}
+
+tg_status tg_grouped_fwd(const void* X, const void* W, const int32_t* offsets, void* Y, int64_t T, int64_t E,
+                         int64_t d_out, int64_t d_in, tg_dtype in, tg_dtype out, void* ws, size_t ws_bytes,
+                         void* stream) {
+  return run_grouped(0, "grouped_fwd", W, X, offsets, Y, T, E, d_out, d_in, in, out, ws, ws_bytes, stream);
+}
+
+tg_status tg_grouped_dgrad(const void* dY, const void* W, const int32_t* offsets, void* dX, int64_t T, int64_t E,
+                           int64_t d_out, int64_t d_in, tg_dtype in, tg_dtype out, void* ws, size_t ws_bytes,
+                           void* stream) {
+  return run_grouped(1, "grouped_dgrad", W, dY, offsets, dX, T, E, d_out, d_in, in, out, ws, ws_bytes, stream);
+}
+
+tg_status tg_grouped_wgrad(const void* dY, const void* X, const int32_t* offsets, void* dW, int64_t T, int64_t E,
+                           int64_t d_out, int64_t d_in, tg_dtype in, tg_dtype out, void* ws, size_t ws_bytes,
+                           void* stream) {
+  return run_grouped(2, "grouped_wgrad", dY, X, offsets, dW, T, E, d_out, d_in, in, out, ws, ws_bytes, stream);
+}
+
+// ------------------------------------------------------ norms around a block
+static int ek_of(tg_dtype d) { return d == TG_BF16 ? EK_BF16 : d == TG_F16 ? EK_F16 : EK_F32; }
+
+static tg_status check_norm(int64_t T, int64_t d, float res_scale, tg_gate gate_kind, tg_dtype in, tg_dtype res,
+                            tg_dtype out) {
+  if (!dtype_in_ok_layer(in) || !dtype_out_ok(in, res) || !dtype_out_ok(in, out)) return TG_ERR_UNSUPPORTED_DTYPE;
+  if (T < 0 || T > kMaxDim || d < 0 || d > NORM_MAX_D || !std::isfinite(res_scale)) return TG_ERR_INVALID_ARG;
+  if (gate_kind < TG_GATE_NONE || gate_kind > TG_GATE_FULL) return TG_ERR_INVALID_ARG;
+  return TG_OK;
+}
+static int64_t gate_elems(tg_gate k, int64_t T, int64_t d) {
+  return k == TG_GATE_CHANNEL ? d : k == TG_GATE_TOKEN ? T : k == TG_GATE_FULL ? T * d : 0;
+}
+
+tg_status tg_norm_residual_fwd(const void* B, const void* H, const void* w_post, const void* w_pre, const void* gate,
+                               tg_gate gate_kind, void* H_out, void* N, float* rstd_b, float* rstd_h, int64_t T,
+                               int64_t d, float res_scale, float eps, tg_dtype in, tg_dtype res, void* stream) {
+  TG_TRY(check_norm(T, d, res_scale, gate_kind, in, res, in));
+  if (!std::isfinite(eps) || eps < 0.f) return TG_ERR_INVALID_ARG;
+  const int64_t n = T * d;
+  TG_TRY(check_ptr(B, n, dt_bytes(in)));
+  TG_TRY(check_ptr(H, n, dt_bytes(res)));
+  TG_TRY(check_ptr(w_post, n > 0 ? d : 0, dt_bytes(in)));
+  TG_TRY(check_ptr(w_pre, n > 0 ? d : 0, dt_bytes(in)));
+  TG_TRY(check_ptr(gate, n > 0 ? gate_elems(gate_kind, T, d) : 0, dt_bytes(in)));
+  TG_TRY(check_ptr(H_out, n, dt_bytes(res)));
+  TG_TRY(check_ptr(N, n, dt_bytes(in)));
+  if (!aligned(rstd_b, 4) || !aligned(rstd_h, 4)) return TG_ERR_MISALIGNED;
+  DevCtx* ctx = nullptr;
+  TG_TRY(device_ctx(&ctx));
+  if (n == 0) {
+    record("norm_residual_fwd empty: nothing to do");
+    return TG_OK;
+  }
+  NormResidual a{};
+  a.B = B;
+  a.H = H;
+  a.w_post = w_post;
+  a.w_pre = w_pre;
+  a.gate = gate;
+  a.H_out = H_out;
+  a.N = N;
+  a.rstd_b = rstd_b;
+  a.rstd_h = rstd_h;
+  a.T = T;
+  a.d = d;
+  a.res_scale = res_scale;
+  a.eps = eps;
+  a.gate_kind = gate_kind;
+  a.in_kind = ek_of(in);
+  a.res_kind = ek_of(res);
+  a.num_sms = ctx->sms;
+  a.stream = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = norm_residual_fwd_launch(a);
+  record("norm_residual_fwd T=" + std::to_string(T) + " d=" + std::to_string(d) + " " +
+         (e == cudaSuccess ? "ok" : cudaGetErrorString(e)));
+  return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
+}
+
+tg_status tg_norm_residual_bwd(const void* dH_out, const void* dN, const void* B, const void* H_out, const void* w_post,
+                               const void* w_pre, const void* gate, tg_gate gate_kind, const float* rstd_b,
+                               const float* rstd_h, void* dB, void* dH, void* dw_post, void* dw_pre, void* dgate,
+                               int64_t T, int64_t d, float res_scale, tg_dtype in, tg_dtype res, tg_dtype out, void* ws,
+                               size_t ws_bytes, void* stream) {
+  TG_TRY(check_norm(T, d, res_scale, gate_kind, in, res, out));
+  const int64_t n = T * d;
+  TG_TRY(check_ptr(dH_out, n, dt_bytes(res)));
+  TG_TRY(check_ptr(dN, n, dt_bytes(in)));
+  TG_TRY(check_ptr(B, n, dt_bytes(in)));
+  TG_TRY(check_ptr(H_out, n, dt_bytes(res)));
+  TG_TRY(check_ptr(w_post, n > 0 ? d : 0, dt_bytes(in)));
+  TG_TRY(check_ptr(w_pre, n > 0 ? d : 0, dt_bytes(in)));
+  TG_TRY(check_ptr(gate, n > 0 ? gate_elems(gate_kind, T, d) : 0, dt_bytes(in)));
+  TG_TRY(check_ptr(rstd_b, T, 4));
+  TG_TRY(check_ptr(rstd_h, T, 4));
+  TG_TRY(check_ptr(dB, n, dt_bytes(in)));
+  TG_TRY(check_ptr(dH, n, dt_bytes(res)));
+  TG_TRY(check_ptr(dw_post, d, dt_bytes(out)));
+  TG_TRY(check_ptr(dw_pre, d, dt_bytes(out)));
+  const size_t gb = dt_bytes(gate_kind == TG_GATE_FULL ? in : out);
+  TG_TRY(check_ptr(dgate, gate_elems(gate_kind, T, d), gb));
+  DevCtx* ctx = nullptr;
+  TG_TRY(device_ctx(&ctx));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (n == 0) {  // sums over nothing
+    record("norm_residual_bwd empty: zero fill");
+    const int64_t ng = gate_elems(gate_kind, T, d);
+    if ((d > 0 && (cudaMemsetAsync(dw_post, 0, d * dt_bytes(out), st) != cudaSuccess ||
+                   cudaMemsetAsync(dw_pre, 0, d * dt_bytes(out), st) != cudaSuccess)) ||
+        (ng > 0 && cudaMemsetAsync(dgate, 0, ng * gb, st) != cudaSuccess))
+      return TG_ERR_CUDA;
+    return TG_OK;
+  }
+  const size_t need = norm_residual_bwd_ws_bytes(T, d, ctx->sms);
+  if (ws == nullptr || ws_bytes < need) return TG_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(ws, 16)) return TG_ERR_MISALIGNED;
+  NormResidual a{};
+  a.dH_out = dH_out;
+  a.dN = dN;
+  a.B = B;
+  a.H = H_out;
+  a.w_post = w_post;
+  a.w_pre = w_pre;
+  a.gate = gate;
+  a.rstd_b = const_cast<float*>(rstd_b);
+  a.rstd_h = const_cast<float*>(rstd_h);
+  a.dB = dB;
+  a.dH = dH;
+  a.dw_post = dw_post;
+  a.dw_pre = dw_pre;
+  a.dgate = dgate;
+  a.T = T;
+  a.d = d;
+  a.res_scale = res_scale;
+  a.gate_kind = gate_kind;
+  a.in_kind = ek_of(in);
+  a.res_kind = ek_of(res);
+  a.out_kind = ek_of(out);
+  a.ws = static_cast<float*>(ws);
+  a.num_sms = ctx->sms;
+  a.stream = st;
+  const cudaError_t e = norm_residual_bwd_launch(a);
+  record("norm_residual_bwd T=" + std::to_string(T) + " d=" + std::to_string(d) + " " +
+         (e == cudaSuccess ? "ok" : cudaGetErrorString(e)));
+  return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
+}
+
+// ------------------------------------------- global gradient norm and clipping
+static tg_status run_grad(const char* name, const void* const* grads, void* const* outs, const int64_t* numels,
+                          const int32_t* dtypes, int64_t n, float max_norm, float* norm, void* ws, size_t ws_bytes,
+                          void* stream) {
+  if (n < 0 || n > (1 << 20) || std::isnan(max_norm) || max_norm < 0.f) return TG_ERR_INVALID_ARG;
+  if (n > 0 && (grads == nullptr || numels == nullptr || dtypes == nullptr)) return TG_ERR_INVALID_ARG;
+  TG_TRY(check_ptr(norm, 1, 4));
+  for (int64_t i = 0; i < n; ++i) {
+    if (dtypes[i] != TG_BF16 && dtypes[i] != TG_F16 && dtypes[i] != TG_F32) return TG_ERR_UNSUPPORTED_DTYPE;
+    if (numels[i] < 0 || numels[i] > (int64_t(1) << 40)) return TG_ERR_INVALID_ARG;
+    const size_t esz = dt_bytes(static_cast<tg_dtype>(dtypes[i]));
+    TG_TRY(check_ptr(grads[i], numels[i], esz));
+    if (outs) TG_TRY(check_ptr(outs[i], numels[i], esz));
+  }
+  DevCtx* ctx = nullptr;
+  TG_TRY(device_ctx(&ctx));
+  const size_t need = grad_norm_ws_bytes(n, ctx->sms);
+  if (ws == nullptr || ws_bytes < need) return TG_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(ws, 16)) return TG_ERR_MISALIGNED;
+  GradList g{};
+  g.grads = grads;
+  g.outs = outs;
+  g.numels = numels;
+  g.kinds = dtypes;  // tg_dtype and the kernels' kinds number the types alike
+  static_assert(TG_BF16 == static_cast<int>(EK_BF16) && TG_F16 == static_cast<int>(EK_F16) &&
+                    TG_F32 == static_cast<int>(EK_F32),
+                "types");
+  g.n = n;
+  g.max_norm = max_norm;
+  g.norm = norm;
+  g.ws = ws;
+  g.num_sms = ctx->sms;
+  g.stream = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = grad_clip_launch(g);
+  record(std::string(name) + " tensors=" + std::to_string(n) + " " + (e == cudaSuccess ? "ok" : cudaGetErrorString(e)));
+  return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
+}
+
+tg_status tg_grad_norm(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int64_t n, float* norm,
+                       void* ws, size_t ws_bytes, void* stream) {
+  return run_grad("grad_norm", grads, nullptr, numels, dtypes, n, 0.f, norm, ws, ws_bytes, stream);
+}
+
+tg_status tg_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels, const int32_t* dtypes,
+                       int64_t n, float max_norm, float* norm, void* ws, size_t ws_bytes, void* stream) {
+  if (n > 0 && outs == nullptr) return TG_ERR_INVALID_ARG;
+  return run_grad("grad_clip", grads, outs, numels, dtypes, n, max_norm, norm, ws, ws_bytes, stream);
+}
+
 size_t tg_workspace_size(tg_op op, int64_t d0, int64_t d1, int64_t d2, int64_t d3, tg_dtype in, tg_dtype out) {
-  const bool layer = op == TG_OP_GEMM_FWD || op == TG_OP_GEMM_DGRAD || op == TG_OP_GEMM_WGRAD;
+  const bool layer = op == TG_OP_GEMM_FWD || op == TG_OP_GEMM_DGRAD || op == TG_OP_GEMM_WGRAD ||
+                     op == TG_OP_NORM_RESIDUAL_BWD || op == TG_OP_GRAD_CLIP;  // these take FP32 too
   if (!(layer ? dtype_in_ok_layer(in) : dtype_in_ok(in)) || !dtype_out_ok(in, out)) return SIZE_MAX;
   if (d0 < 0 || d1 < 0 || d2 < 0 || d3 < 0) return SIZE_MAX;
   DevCtx* ctx = nullptr;
@@ -1648,6 +1904,16 @@ size_t tg_workspace_size(tg_op op, int64_t d0, int64_t d1, int64_t d2, int64_t d
     case TG_OP_ATTN_BWD: return d2 == 64 ? attn_bwd_ws_bytes(d0, d1) : SIZE_MAX;
     case TG_OP_GEMM_FWD_LORA: return layer_lora_ws(LAYOUT_NT, d0, d1, d2, d3, in, out, ctx->sms);
     case TG_OP_GEMM_DGRAD_LORA: return layer_lora_ws(LAYOUT_NN, d0, d2, d1, d3, in, out, ctx->sms);
+    case TG_OP_GROUPED_FWD: return grouped_ws_bytes(0, d0, d1, d2, d3, false);
+    case TG_OP_GROUPED_DGRAD: return grouped_ws_bytes(1, d0, d1, d2, d3, false);
+    case TG_OP_GROUPED_WGRAD: return grouped_ws_bytes(2, d0, d1, d2, d3, false);
+    case TG_OP_GROUPED_UNALIGNED: {
+      size_t most = 0;
+      for (int k = 0; k < 3; ++k) most = std::max(most, grouped_ws_bytes(k, d0, d1, d2, d3, true));
+      return most;
+    }
+    case TG_OP_NORM_RESIDUAL_BWD: return norm_residual_bwd_ws_bytes(d0, d1, ctx->sms);
+    case TG_OP_GRAD_CLIP: return grad_norm_ws_bytes(d0, ctx->sms);
     case TG_OP_BMM_ATTN: {
       GemmCall g;
       if (!attn_call(static_cast<tg_attn_op>(d0), nullptr, nullptr, nullptr, d1, d2, d3, in, out, nullptr, 0,

@@ -1,0 +1,761 @@
+// grouped_tc.cu -- the three products of a linear layer whose rows are
+// grouped by expert, on tcgen05 CTA pairs.
+//
+// Rows [offsets[e], offsets[e+1]) of the activations belong to expert e:
+//   forward          Y[t]  = X[t] W[e]^T
+//   input gradient   dX[t] = dY[t] W[e]
+//   weight gradient  dW[e] = sum over the rows t of e of dY[t]^T X[t]
+// The offsets are read on the device, so no call waits for the host and a
+// captured call follows new offsets.
+//
+// Which operand is the 256-row side of the MMA.  tcgen05.mma takes M = 256
+// for a pair whatever the data, but N is any multiple of 32 up to 256.  A
+// group's row count is the ragged size, so in the forward and input-gradient
+// products the WEIGHT rows (or columns) are M and the group's rows are N:
+// the kernel computes Y^T tiles of 256 features x up to 256 rows, a group of n
+// rows costs ceil(n / 32) * 32 columns of MMA instead of ceil(n / 256) * 256,
+// and each expert's weight is streamed once when its rows fit one tile.  A
+// group of more rows is cut into tiles of nearly equal width.  Rows of a
+// neighbouring group that a load box takes in end in accumulator columns that
+// are never stored, so whatever they hold (NaN too) stays with them.
+//
+// In the weight gradient the ragged size is the reduction.  The last 64-row
+// block of a group takes in rows of the next group, which must not reach the
+// sums: the MMAs of that block stop at the last 16-row slice with a row of
+// the group, and the rest of that slice is overwritten with zeros in both
+// operands in shared memory before the MMA may read it (zeroing one operand
+// only would leave 0 * NaN).  A "mender" warp of each CTA does this; the
+// block's copies complete on a barrier of its own CTA, and the mender's
+// arrival stands for them on rank 0's "stage full" barrier.
+//
+// Roles of a CTA (7 warps): 0 producer (TMA), 1 MMA issuer (rank 0 of the
+// pair), 2-5 epilogue, 6 mender (weight gradient).  Every wait is bounded.
+#include <cuda.h>
+#include <stdio.h>
+
+#include "grouped.h"
+#include "ptx.cuh"
+#include "smem_attr.h"
+
+namespace tg {
+namespace {
+
+constexpr int G_FWD = 0, G_DGRAD = 1, G_WGRAD = 2;
+
+constexpr int GT_THREADS = 224;
+constexpr int GT_BM = 256;        // rows of the pair's tile
+constexpr int GT_BN = 256;        // largest tile width
+constexpr int GT_BK = 64;
+constexpr int GT_STAGES = 6;
+constexpr int GT_A_BYTES = 128 * GT_BK * 2;  // one CTA's operand halves of a stage
+constexpr int GT_B_BYTES = 128 * GT_BK * 2;
+constexpr int GT_EPI_BUF = 32 * 128;
+constexpr int GT_EPI_BYTES = 4 * 2 * GT_EPI_BUF;  // weight gradient only
+constexpr int GT_MAXG = GROUPED_PER_LAUNCH + 2;   // experts of a launch, rows before and after them
+constexpr int GT_BAR_BYTES = 256;
+
+template <int OP>
+struct GtCfg {
+  static constexpr int EPI = OP == G_WGRAD ? GT_EPI_BYTES : 0;
+  static constexpr int TAB = (GT_MAXG + 1) * 4 * (OP == G_WGRAD ? 1 : 2);
+  static constexpr int SMEM = 1024 + GT_STAGES * (GT_A_BYTES + GT_B_BYTES) + EPI + GT_BAR_BYTES + TAB;
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert((3 * GT_STAGES + 5) * 8 + 8 <= GT_BAR_BYTES, "barrier area");
+};
+
+struct GtArgs {
+  const int* offsets;  // [E + 1]
+  void* out;
+  long long T;
+  int E;           // experts of this launch
+  int M;           // forward: d_out; input gradient: d_in; weight gradient: d_out
+  int N;           // weight gradient: d_in
+  int K;           // forward: d_in; input gradient: d_out
+  int m_tiles;     // of 256
+  int n_tiles;     // weight gradient: column tiles
+  int n_width;     // weight gradient: width of a column tile (a multiple of 64)
+  int first, last; // this launch holds the first / last experts: it zeroes the rows outside every group
+  int out_kind;
+  int wide;        // forward, input gradient: two 16-bit features in one store; weight gradient: TMA stores
+  uint32_t idesc;  // without N
+  unsigned long long timeout_ns;
+  unsigned int* status;
+};
+
+struct GtMaps {
+  CUtensorMap A;     // forward: W (box 64 x 128 rows); input gradient: W (64 x 64); weight gradient: dY (64 x 64)
+  CUtensorMap B[4];  // forward, input gradient: rows in boxes of 128, 64, 32, 16; weight gradient: [0] = X (64 x 64)
+  CUtensorMap C;     // weight gradient: dW store
+};
+
+// One unit of work: a tile of one group.
+struct GtUnit {
+  int m0;    // first feature row of the pair's tile
+  int n0;    // first column: row of the activations, or (weight gradient) column of dW
+  int n;     // columns that are stored
+  int nmma;  // columns the MMA computes (a multiple of 32)
+  int e;     // expert (index of this launch)
+  int r0;    // weight gradient: first row of the reduction
+  int kb;    // 64-deep blocks of the reduction; 0: the tile is zeros
+  int tail;  // rows (or columns) of the last block, 1..64
+};
+
+__device__ __forceinline__ int pairs_in_grid() { return static_cast<int>(gridDim.x >> 1); }
+
+// Group tables in shared memory.  off[0 .. E]: the launch's offsets, made
+// non-decreasing and confined to [0, T] (so that offsets that break the rules
+// still address nothing outside the tensors).  Forward and input gradient:
+// group 0 holds the rows before the first expert, 1..E the experts, E + 1 the
+// rows after the last; start[g] = first row, cum[g] = units before group g.
+template <int OP>
+struct GtTab {
+  int* off;  // weight gradient: off[0..E]; otherwise start[0..E+2]
+  int* cum;  // forward, input gradient
+  int units;
+};
+
+__device__ __forceinline__ int tiles_of(int rows) { return (rows + GT_BN - 1) / GT_BN; }
+
+template <int OP>
+__device__ void gt_build(const GtArgs& a, GtTab<OP>& t, int* s_units) {
+  // one warp: running maximum of the clamped offsets, then (forward, input
+  // gradient) running sum of the groups' unit counts
+  const int lane = threadIdx.x & 31;
+  const int T = static_cast<int>(a.T);
+  const int shift = OP == G_WGRAD ? 0 : 1;
+  int run = 0;
+  for (int b = 0; b <= a.E; b += 32) {
+    const int i = b + lane;
+    int v = i <= a.E ? min(max(a.offsets[i], 0), T) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int w = __shfl_up_sync(~0u, v, o);
+      if (lane >= o) v = max(v, w);
+    }
+    v = max(v, run);
+    if (i <= a.E) t.off[i + shift] = v;
+    run = __shfl_sync(~0u, v, 31);
+  }
+  __syncwarp();
+  if (OP == G_WGRAD) {
+    if (lane == 0) *s_units = a.E * a.m_tiles * a.n_tiles;
+    return;
+  }
+  if (lane == 0) {
+    // rows outside every group: only the launches with the first and last experts own them
+    t.off[0] = a.first ? 0 : t.off[1];
+    t.off[a.E + 2] = a.last ? T : t.off[a.E + 1];
+  }
+  __syncwarp();
+  int sum = 0;
+  const int G = a.E + 2;
+  for (int b = 0; b < G; b += 32) {
+    const int g = b + lane;
+    const int u = g < G ? tiles_of(t.off[g + 1] - t.off[g]) * a.m_tiles : 0;
+    int v = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int w = __shfl_up_sync(~0u, v, o);
+      if (lane >= o) v += w;
+    }
+    if (g < G) t.cum[g] = sum + v - u;
+    sum += __shfl_sync(~0u, v, 31);
+  }
+  if (lane == 0) {
+    t.cum[G] = sum;
+    *s_units = sum;
+  }
+}
+
+template <int OP>
+__device__ __forceinline__ GtUnit gt_unit(const GtArgs& a, const GtTab<OP>& t, int u) {
+  GtUnit c;
+  if (OP == G_WGRAD) {
+    const int per = a.m_tiles * a.n_tiles;
+    c.e = u / per;
+    const int r = u - c.e * per;
+    const int nt = r / a.m_tiles;
+    c.m0 = (r - nt * a.m_tiles) * GT_BM;
+    c.n0 = nt * a.n_width;
+    c.n = min(a.n_width, a.N - c.n0);
+    c.nmma = (c.n + 63) / 64 * 64;
+    c.r0 = t.off[c.e];
+    const int rows = t.off[c.e + 1] - c.r0;
+    c.kb = (rows + GT_BK - 1) / GT_BK;
+    c.tail = rows - (c.kb - 1) * GT_BK;
+  } else {
+    int lo = 0, hi = a.E + 1;  // the last group whose units start at or before u
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (t.cum[mid] <= u) lo = mid;
+      else hi = mid - 1;
+    }
+    const int start = t.off[lo], rows = t.off[lo + 1] - start;
+    const int r = u - t.cum[lo];
+    const int nt = r / a.m_tiles;
+    const int tiles = tiles_of(rows);
+    const int width = ((rows + tiles - 1) / tiles + 31) / 32 * 32;
+    c.m0 = (r - nt * a.m_tiles) * GT_BM;
+    c.n0 = start + nt * width;
+    c.n = min(width, rows - nt * width);
+    c.nmma = (c.n + 31) / 32 * 32;
+    c.e = lo - 1;
+    const bool expert = lo >= 1 && lo <= a.E;
+    c.r0 = 0;
+    c.kb = expert ? (a.K + GT_BK - 1) / GT_BK : 0;
+    c.tail = a.K - (c.kb - 1) * GT_BK;
+  }
+  return c;
+}
+
+// arrivals on rank 0's barriers
+__device__ __forceinline__ void arrive_expect_tx_cluster(uint32_t cluster_addr, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void arrive_release_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+__device__ __forceinline__ uint16_t to_16(float v, int kind) {
+  return kind == EK_F16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+__device__ __forceinline__ uint32_t pack_16(float lo, float hi, int kind) {
+  return kind == EK_F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+}
+
+template <int OP>
+__global__ void __launch_bounds__(GT_THREADS, 1)
+    grouped_kernel(const __grid_constant__ GtMaps maps, const GtArgs args) {
+  using Cfg = GtCfg<OP>;
+  constexpr int S = GT_STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + S * GT_A_BYTES;
+  uint8_t* sE = sB + S * GT_B_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sE + Cfg::EPI);
+  uint64_t* empty = full + S;
+  uint64_t* landed = empty + S;  // weight gradient: a group's last block has landed in this CTA
+  uint64_t* tfull = landed + S;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* s_units = reinterpret_cast<int*>(sE + Cfg::EPI + GT_BAR_BYTES - 4);
+  GtTab<OP> tab;
+  tab.off = reinterpret_cast<int*>(sE + Cfg::EPI + GT_BAR_BYTES);
+  tab.cum = tab.off + GT_MAXG + 1;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&full[s]), 2);    // rank 0's: an arrival from each CTA, and both CTAs' bytes
+      mbar_init(smem_u32(&empty[s]), 1);   // one multicast commit
+      mbar_init(smem_u32(&landed[s]), 1);  // this CTA's producer
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&tfull[i]), 1);
+      mbar_init(smem_u32(&tempty[i]), 8);  // the epilogue warps of both CTAs
+    }
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&maps.A);
+    prefetch_tmap(&maps.B[0]);
+    if (OP == G_WGRAD) prefetch_tmap(&maps.C);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
+    tc_fence_before();
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 2) gt_build<OP>(args, tab, s_units);
+  __syncthreads();
+  // both CTAs' barriers are initialised before either signals the other's
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const unsigned long long tmo = args.timeout_ns;
+  tab.units = *s_units;
+  const int pair = static_cast<int>(blockIdx.x >> 1);
+
+  if (warp == 0) {
+    // ------------------------------------------------ producer (both CTAs)
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued[S];
+#pragma unroll
+      for (int s = 0; s < S; ++s) issued[s] = -1;
+      bool ok = true;
+      for (int u = pair; ok && u < tab.units; u += pairs_in_grid()) {
+        const GtUnit c = gt_unit<OP>(args, tab, u);
+        const int m = c.m0 + static_cast<int>(rank) * 128;
+        const int half = c.nmma / 2;  // this CTA's columns
+        const int n = c.n0 + static_cast<int>(rank) * half;
+        const int chunks = (half + 63) / 64;
+        const uint32_t bytes = GT_A_BYTES + (OP == G_WGRAD ? chunks * 64 * GT_BK * 2 : half * GT_BK * 2);
+        for (int kb = 0; kb < c.kb; ++kb) {
+          if (!mbar_wait<true>(smem_u32(&empty[stage]), phase ^ 1u, tmo, abort_flag, args.status, 0x41)) {
+            ok = false;
+            break;
+          }
+          // the last block of a group whose rows end inside a 16-row slice goes through the mender
+          const bool mend = OP == G_WGRAD && kb == c.kb - 1 && (c.tail & 15) != 0;
+          uint32_t bar;
+          if (mend) {
+            bar = smem_u32(&landed[stage]);
+            mbar_arrive_expect_tx(bar, bytes);
+          } else {
+            bar = mapa_shared(smem_u32(&full[stage]), 0);
+            arrive_expect_tx_cluster(bar, bytes);
+          }
+          const uint32_t a_dst = smem_u32(sA + stage * GT_A_BYTES);
+          const uint32_t b_dst = smem_u32(sB + stage * GT_B_BYTES);
+          const int k0 = kb * GT_BK;
+          if (OP == G_FWD) {
+            tma_load_3d_pair(a_dst, &maps.A, bar, k0, m, c.e);
+          } else if (OP == G_DGRAD) {
+            tma_load_3d_pair(a_dst, &maps.A, bar, m, k0, c.e);
+            tma_load_3d_pair(a_dst + 8192, &maps.A, bar, m + 64, k0, c.e);
+          } else {
+            tma_load_3d_pair(a_dst, &maps.A, bar, m, c.r0 + k0, 0);
+            tma_load_3d_pair(a_dst + 8192, &maps.A, bar, m + 64, c.r0 + k0, 0);
+          }
+          if (OP == G_WGRAD) {
+            for (int j = 0; j < chunks; ++j)
+              tma_load_3d_pair(b_dst + j * 8192, &maps.B[0], bar, n + 64 * j, c.r0 + k0, 0);
+          } else {
+            // half rows (a multiple of 16) in boxes of 128, 64, 32 and 16 rows
+            int done = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int h = 128 >> i;
+              if (half & h) {
+                tma_load_3d_pair(b_dst + done * 128, &maps.B[i], bar, k0, n + done, 0);
+                done += h;
+              }
+            }
+          }
+          issued[stage] = static_cast<int>(phase);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (ok) {
+        // the last commits of rank 0's MMAs arrive on these barriers: see
+        // them all before this CTA can leave
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+          if (issued[s] >= 0 && !mbar_wait<true>(smem_u32(&empty[s]), static_cast<uint32_t>(issued[s]), tmo, abort_flag,
+                                                 args.status, 0x42))
+            break;
+      }
+      if (!ok || *abort_flag) {
+        // a wait ran out: give the copies in flight (they complete on barriers
+        // of either CTA) time to land before the CTAs leave
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------- MMA issuer (rank 0 only)
+    if (lane == 0 && rank == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < tab.units; u += pairs_in_grid()) {
+        const GtUnit c = gt_unit<OP>(args, tab, u);
+        if (c.kb == 0) continue;
+        if (!mbar_wait<true>(smem_u32(&tempty[acc]), acc_phase ^ 1u, tmo, abort_flag, args.status, 0x43)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
+        const uint32_t idesc = args.idesc | (static_cast<uint32_t>(c.nmma >> 3) << 17);
+        for (int kb = 0; kb < c.kb; ++kb) {
+          if (!mbar_wait<true>(smem_u32(&full[stage]), phase, tmo, abort_flag, args.status, 0x44)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_base = smem_u32(sA + stage * GT_A_BYTES);
+          const uint32_t b_base = smem_u32(sB + stage * GT_B_BYTES);
+          const int slices = kb == c.kb - 1 ? (c.tail + 15) / 16 : GT_BK / 16;
+#pragma unroll
+          for (int kk = 0; kk < GT_BK / 16; ++kk) {
+            if (kk < slices) {
+              const uint64_t ad = OP == G_FWD ? sdesc_sw128(a_base + kk * 32, 16, 1024)
+                                              : sdesc_sw128(a_base + kk * 2048, 8192, 1024);
+              const uint64_t bd = OP == G_WGRAD ? sdesc_sw128(b_base + kk * 2048, 8192, 1024)
+                                                : sdesc_sw128(b_base + kk * 32, 16, 1024);
+              umma_f16_pair(d_tmem, ad, bd, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+            }
+          }
+          umma_commit_pair(smem_u32(&empty[stage]), 0x3);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit_pair(smem_u32(&tfull[acc]), 0x3);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      // every MMA issued must finish before either CTA frees tensor memory
+      umma_commit_pair(smem_u32(drain), 0x1);
+      mbar_wait<true>(smem_u32(drain), 0, ok ? tmo : 200000000ull, nullptr, args.status, 0x45);
+    }
+  } else if (warp == 6) {
+    // ------------------------------------------------- mender (both CTAs)
+    if (OP == G_WGRAD) {
+      int at = 0;                // stage of the unit's first block
+      uint32_t phases = 0;       // parity of each stage's `landed`
+      for (int u = pair; u < tab.units; u += pairs_in_grid()) {
+        const GtUnit c = gt_unit<OP>(args, tab, u);
+        if (c.kb == 0) continue;
+        const int stage = (at + c.kb - 1) % S;
+        at = (at + c.kb) % S;
+        if ((c.tail & 15) == 0) continue;
+        if (!mbar_wait(smem_u32(&landed[stage]), (phases >> stage) & 1u, tmo, abort_flag, args.status, 0x46)) break;
+        phases ^= 1u << stage;
+        // 16-row slices are 2,048 bytes of each 64-column chunk, a row 128 bytes
+        const int words = (16 - (c.tail & 15)) * 8;  // 16-byte words of one chunk
+        const int chunks = (c.nmma / 2 + 63) / 64;
+        for (int j = 0; j < 2 + chunks; ++j) {
+          uint8_t* chunk = j < 2 ? sA + stage * GT_A_BYTES + j * 8192 : sB + stage * GT_B_BYTES + (j - 2) * 8192;
+          uint4* z = reinterpret_cast<uint4*>(chunk + c.tail * 128);
+          for (int i = lane; i < words; i += 32) z[i] = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_release_cluster(mapa_shared(smem_u32(&full[stage]), 0));
+      }
+    }
+  } else {
+    // ------------------------------------------------- epilogue (both CTAs)
+    const int q = warp & 3;  // tensor-memory lane quadrant this warp may access
+    const uint32_t tempty_cl = mapa_shared(smem_u32(&tempty[0]), 0);
+    const int kind = args.out_kind;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    int nstore = 0;
+    for (int u = pair; u < tab.units; u += pairs_in_grid()) {
+      const GtUnit c = gt_unit<OP>(args, tab, u);
+      if (c.kb > 0 &&
+          !mbar_wait<true>(smem_u32(&tfull[acc]), acc_phase, tmo, abort_flag, args.status, 0x47))
+        break;
+      tc_fence_after();
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256);
+      const int row = c.m0 + static_cast<int>(rank) * 128 + q * 32;  // of the accumulator's first lane
+      const int nch = (c.n + 31) / 32;
+      if (OP != G_WGRAD) {
+        // Y^T: lane = feature, column = row of the activations
+        const int f = row + lane;
+        const bool live = f < args.M;
+#pragma unroll 1
+        for (int ch = 0; ch < nch; ++ch) {
+          uint32_t r[32];
+          if (c.kb > 0) {
+            tmem_ld_32x32b_x32(t_row + ch * 32, r);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = 0;
+          }
+          const int left = c.n - ch * 32;  // columns of this chunk that are stored
+          const long long base = static_cast<long long>(c.n0 + ch * 32) * args.M + f;
+          if (kind == EK_F32) {
+            float* p = static_cast<float*>(args.out) + base;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (live && j < left) p[static_cast<long long>(j) * args.M] = __uint_as_float(r[j]);
+          } else if (args.wide) {
+            // lanes 2i and 2i + 1 exchange a value: the even one stores features
+            // (f, f + 1) of row j, the odd one features (f - 1, f) of row j + 1
+            const bool odd = lane & 1;
+            uint16_t* p = static_cast<uint16_t*>(args.out) + base + (odd ? args.M - 1 : 0);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const uint32_t got = __shfl_xor_sync(~0u, odd ? r[j] : r[j + 1], 1);
+              const uint32_t v = odd ? pack_16(__uint_as_float(got), __uint_as_float(r[j + 1]), kind)
+                                     : pack_16(__uint_as_float(r[j]), __uint_as_float(got), kind);
+              if (live && j + (odd ? 1 : 0) < left) *reinterpret_cast<uint32_t*>(p + static_cast<long long>(j) * args.M) = v;
+            }
+          } else {
+            uint16_t* p = static_cast<uint16_t*>(args.out) + base;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (live && j < left) p[static_cast<long long>(j) * args.M] = to_16(__uint_as_float(r[j]), kind);
+          }
+        }
+        if (c.kb > 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty_cl + static_cast<uint32_t>(acc * 8));
+        }
+      } else {
+        // dW: lane = row of dW, column = column of dW; 128-byte rows of columns staged in shared memory
+        const bool f32 = kind == EK_F32;
+        const int per = f32 ? 32 : 64;  // columns of a staged row
+        const int nst = (c.n + per - 1) / per;
+        const int esz = f32 ? 4 : 2;
+#pragma unroll 1
+        for (int ch = 0; ch < nst; ++ch) {
+          uint32_t r[64];
+          if (c.kb > 0) {
+            tmem_ld_32x32b_x32(t_row + ch * per, r);
+            if (!f32) tmem_ld_32x32b_x32(t_row + ch * per + 32, r + 32);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 64; ++j) r[j] = 0;
+          }
+          if (ch == nst - 1 && c.kb > 0) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty_cl + static_cast<uint32_t>(acc * 8));
+          }
+          uint8_t* buf = sE + (q * 2 + (nstore & 1)) * GT_EPI_BUF;
+          if (args.wide) {
+            if (lane == 0 && nstore >= 2) bulk_wait_read<1>();
+          }
+          __syncwarp();
+          uint8_t* rowp = buf + lane * 128;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint4 v;
+            if (f32) {
+              v = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+            } else {
+              const uint32_t* x = r + 8 * j;
+              v.x = pack_16(__uint_as_float(x[0]), __uint_as_float(x[1]), kind);
+              v.y = pack_16(__uint_as_float(x[2]), __uint_as_float(x[3]), kind);
+              v.z = pack_16(__uint_as_float(x[4]), __uint_as_float(x[5]), kind);
+              v.w = pack_16(__uint_as_float(x[6]), __uint_as_float(x[7]), kind);
+            }
+            // 128-byte swizzle: 16-byte word j of row `lane` sits at word j ^ (lane % 8)
+            *reinterpret_cast<uint4*>(rowp + ((j ^ (lane & 7)) << 4)) = v;
+          }
+          if (args.wide) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&maps.C, smem_u32(buf), c.n0 + ch * per, row, c.e);
+              bulk_commit();
+            }
+          } else {
+            // rows of dW that are no multiple of 16 bytes: element by element, along the rows
+            __syncwarp();
+            const int left = min(per, c.n - ch * per);
+            for (int i = 0; i < 32 && row + i < args.M; ++i) {
+              const long long at = (static_cast<long long>(c.e) * args.M + row + i) * args.N + c.n0 + ch * per;
+              for (int j = lane; j < left; j += 32) {
+                const int byte = j * esz;
+                const uint8_t* src = buf + i * 128 + (((byte >> 4) ^ (i & 7)) << 4) + (byte & 15);
+                if (f32) static_cast<uint32_t*>(args.out)[at + j] = *reinterpret_cast<const uint32_t*>(src);
+                else static_cast<uint16_t*>(args.out)[at + j] = *reinterpret_cast<const uint16_t*>(src);
+              }
+            }
+            __syncwarp();
+          }
+          ++nstore;
+        }
+      }
+      if (c.kb > 0 && ++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    if (OP == G_WGRAD && lane == 0) bulk_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // neither CTA leaves (or frees tensor memory) while the other may still
+  // read its shared memory, write its tensor memory or arrive on its barriers
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// Rows of `cols` 16-bit elements copied to rows of `pitch` (a multiple of 8)
+// elements, the rest zero: what TMA needs of an operand whose rows are no
+// multiple of 16 bytes or whose base is not 16-byte aligned.
+__global__ void grouped_pitch_kernel(const uint16_t* src, uint16_t* dst, long long rows, int cols, int pitch) {
+  pdl_wait();
+  pdl_trigger();
+  const int per = pitch / 8;
+  const long long n = rows * per;
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+       i += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const long long r = i / per;
+    const int c = static_cast<int>(i - r * per) * 8;
+    const uint16_t* s = src + r * cols + c;
+    uint16_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? s[j] : static_cast<uint16_t>(0);
+    uint4 o;
+    o.x = v[0] | static_cast<uint32_t>(v[1]) << 16;
+    o.y = v[2] | static_cast<uint32_t>(v[3]) << 16;
+    o.z = v[4] | static_cast<uint32_t>(v[5]) << 16;
+    o.w = v[6] | static_cast<uint32_t>(v[7]) << 16;
+    *reinterpret_cast<uint4*>(dst + r * pitch + c) = o;
+  }
+}
+
+int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+template <int OP>
+cudaError_t launch_op(const GroupedCall& g, const void* A, int64_t lda, const void* B, int64_t ldb) {
+  using Cfg = GtCfg<OP>;
+  auto kern = grouped_kernel<OP>;
+  cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), Cfg::SMEM);
+  if (e != cudaSuccess) return e;
+
+  GtArgs a = {};
+  a.out = g.C;
+  a.T = g.T;
+  a.M = static_cast<int>(OP == G_DGRAD ? g.d_in : g.d_out);
+  a.N = static_cast<int>(g.d_in);
+  a.K = static_cast<int>(OP == G_FWD ? g.d_in : g.d_out);
+  a.m_tiles = (a.M + GT_BM - 1) / GT_BM;
+  a.n_tiles = (a.N + GT_BN - 1) / GT_BN;
+  a.n_width = ((a.N + a.n_tiles - 1) / a.n_tiles + 63) / 64 * 64;
+  a.n_tiles = (a.N + a.n_width - 1) / a.n_width;
+  a.out_kind = g.out_kind;
+  a.idesc = idesc_f16(g.in_kind == EK_BF16, OP != G_FWD, OP == G_WGRAD, GT_BM, 0);
+  a.timeout_ns = g.timeout_ns;
+  a.status = g.status;
+  const int esz = elem_bytes(g.out_kind);
+  const uintptr_t out = reinterpret_cast<uintptr_t>(g.C);
+  a.wide = OP == G_WGRAD ? (a.N * esz) % 16 == 0 && out % 16 == 0 : a.M % 2 == 0 && out % 4 == 0;
+
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(GT_THREADS);
+  cfg.dynamicSmemBytes = Cfg::SMEM;
+  cfg.stream = g.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+
+  for (int64_t e0 = 0; e0 < g.E; e0 += GROUPED_PER_LAUNCH) {
+    const int64_t ne = g.E - e0 < GROUPED_PER_LAUNCH ? g.E - e0 : GROUPED_PER_LAUNCH;
+    GtMaps m;
+    bool ok = true;
+    const uint64_t T = g.T, di = g.d_in, dn = g.d_out;
+    const uint64_t pa = static_cast<uint64_t>(lda) * 2, pb = static_cast<uint64_t>(ldb) * 2;
+    if (OP == G_WGRAD) {
+      ok = encode_tmap_3d(&m.A, A, g.in_kind, dn, T, 1, pa, 0, 64, 64, 128) &&
+           encode_tmap_3d(&m.B[0], B, g.in_kind, di, T, 1, pb, 0, 64, 64, 128);
+      m.B[1] = m.B[2] = m.B[3] = m.C = m.B[0];
+      a.out = static_cast<char*>(g.C) + e0 * g.d_out * g.d_in * esz;
+      if (ok && a.wide)
+        ok = encode_tmap_3d(&m.C, a.out, g.out_kind, di, dn, ne, di * esz, dn * di * esz, esz == 4 ? 32 : 64, 32, 128);
+    } else {
+      // A: the weights [E][d_out][pitch]; B: the rows
+      const char* W = static_cast<const char*>(A) + e0 * dn * pa;
+      ok = encode_tmap_3d(&m.A, W, g.in_kind, di, dn, ne, pa, dn * pa, 64, OP == G_FWD ? 128 : 64, 128);
+      for (int i = 0; i < 4 && ok; ++i)
+        ok = encode_tmap_3d(&m.B[i], B, g.in_kind, OP == G_FWD ? di : dn, T, 1, pb, 0, 64, 128 >> i, 128);
+      m.C = m.A;
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    a.offsets = g.offsets + e0;
+    a.E = static_cast<int>(ne);
+    a.first = e0 == 0;
+    a.last = e0 + ne == g.E;
+    // no more pairs than there can be units
+    int64_t most = OP == G_WGRAD ? ne * a.m_tiles * static_cast<int64_t>(a.n_tiles)
+                                 : a.m_tiles * ((ne + 2 < g.T ? ne + 2 : g.T) + g.T / GT_BN);
+    int64_t pairs = g.num_sms / 2;
+    if (pairs > most) pairs = most;
+    if (pairs < 1) pairs = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+    e = cudaLaunchKernelEx(&cfg, kern, m, a);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+struct Operand {
+  const void* p;
+  int64_t rows, cols;
+};
+
+}  // namespace
+
+// Staged copies: an operand whose rows are no multiple of 8 elements (or
+// whose base is not 16-byte aligned, when `any_base`).
+size_t grouped_ws_bytes(int op, int64_t T, int64_t E, int64_t d_out, int64_t d_in, bool any_base) {
+  const int64_t rows[2] = {op == G_WGRAD ? T : E * d_out, T};
+  const int64_t cols[2] = {op == G_WGRAD ? d_out : d_in, op == G_DGRAD ? d_out : d_in};
+  size_t n = 0;
+  for (int i = 0; i < 2; ++i)
+    if (any_base || cols[i] % 8) n += up256(static_cast<size_t>(rows[i]) * up8(cols[i]) * 2);
+  return n;
+}
+
+cudaError_t grouped_launch(const GroupedCall& g, size_t* need) {
+  const Operand ops[2] = {{g.A, g.op == G_WGRAD ? g.T : g.E * g.d_out, g.op == G_WGRAD ? g.d_out : g.d_in},
+                          {g.B, g.T, g.op == G_DGRAD ? g.d_out : g.d_in}};
+  const void* p[2];
+  int64_t pitch[2];
+  size_t used = 0;
+  bool staged[2];
+  for (int i = 0; i < 2; ++i) {
+    pitch[i] = up8(ops[i].cols);
+    p[i] = ops[i].p;
+    staged[i] = ops[i].cols % 8 != 0 || reinterpret_cast<uintptr_t>(ops[i].p) % 16 != 0;
+    if (staged[i]) {
+      p[i] = static_cast<char*>(g.ws) + used;
+      used += up256(static_cast<size_t>(ops[i].rows) * pitch[i] * 2);
+    }
+  }
+  *need = used;
+  if (used > 0 && (g.ws == nullptr || g.ws_bytes < used || reinterpret_cast<uintptr_t>(g.ws) % 16)) return cudaSuccess;
+  *need = 0;
+  for (int i = 0; i < 2; ++i) {
+    if (!staged[i]) continue;
+    const int64_t words = ops[i].rows * (pitch[i] / 8);
+    int64_t grid = (words + 255) / 256;
+    if (grid > 8 * g.num_sms) grid = 8 * g.num_sms;
+    const cudaError_t e = launch_k(grouped_pitch_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, g.stream,
+                                   static_cast<const uint16_t*>(ops[i].p), static_cast<uint16_t*>(const_cast<void*>(p[i])),
+                                   static_cast<long long>(ops[i].rows), static_cast<int>(ops[i].cols),
+                                   static_cast<int>(pitch[i]));
+    if (e != cudaSuccess) return e;
+  }
+  switch (g.op) {
+    case G_FWD: return launch_op<G_FWD>(g, p[0], pitch[0], p[1], pitch[1]);
+    case G_DGRAD: return launch_op<G_DGRAD>(g, p[0], pitch[0], p[1], pitch[1]);
+    default: return launch_op<G_WGRAD>(g, p[0], pitch[0], p[1], pitch[1]);
+  }
+}
+
+}  // namespace tg

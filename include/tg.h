@@ -88,6 +88,14 @@ typedef enum {
   TG_ATTN_DST_Q = 5  /* dK = dS^T Q : A=dS [b,s,s], B=Q [b,s,d]  -> C [b,s,d] */
 } tg_attn_op;
 
+/* What the gate of tg_norm_residual_* is broadcast along. */
+typedef enum {
+  TG_GATE_NONE = 0,    /* no gate */
+  TG_GATE_CHANNEL = 1, /* [d] */
+  TG_GATE_TOKEN = 2,   /* [T], one value a row (a router's probability) */
+  TG_GATE_FULL = 3     /* [T, d] */
+} tg_gate;
+
 /* Operation ids for tg_workspace_size. */
 typedef enum {
   TG_OP_GEMM_FWD = 0,   /* d0=T, d1=d_out, d2=d_in */
@@ -102,7 +110,13 @@ typedef enum {
   TG_OP_LORA_GRAD_F32W = 9,  /* d0=T, d1=d_in, d2=d_out, d3=r */
   TG_OP_ATTN_BWD = 10,       /* d0=heads, d1=s, d2=d */
   TG_OP_GEMM_FWD_LORA = 11,  /* d0=T, d1=d_out, d2=d_in, d3=r */
-  TG_OP_GEMM_DGRAD_LORA = 12 /* d0=T, d1=d_out, d2=d_in, d3=r */
+  TG_OP_GEMM_DGRAD_LORA = 12, /* d0=T, d1=d_out, d2=d_in, d3=r */
+  TG_OP_GROUPED_FWD = 13,     /* d0=T, d1=E, d2=d_out, d3=d_in */
+  TG_OP_GROUPED_DGRAD = 14,   /* d0=T, d1=E, d2=d_out, d3=d_in */
+  TG_OP_GROUPED_WGRAD = 15,   /* d0=T, d1=E, d2=d_out, d3=d_in */
+  TG_OP_GROUPED_UNALIGNED = 16, /* the same, when an operand's base is not 16-byte aligned */
+  TG_OP_NORM_RESIDUAL_BWD = 17, /* d0=T, d1=d */
+  TG_OP_GRAD_CLIP = 18        /* d0=number of tensors (tg_grad_norm too) */
 } tg_op;
 
 /* Forward product of a linear layer ("Where the time went"):
@@ -312,6 +326,89 @@ tg_status tg_attn_bwd(const void* Q, const void* K, const void* V, const void* d
 tg_status tg_bmm_attn(tg_attn_op op, const void* A, const void* B, void* C, int64_t batch,
                       int64_t s, int64_t d, tg_dtype in, tg_dtype out, void* ws, size_t ws_bytes,
                       void* stream);
+
+/* The three products of a linear layer whose rows are grouped by expert (a
+ * mixture-of-experts layer after its tokens were sorted by expert): rows
+ * offsets[e] <= t < offsets[e + 1] belong to expert e of E,
+ *   tg_grouped_fwd:    Y[t, d_out]  = X[t, d_in] . W[e, d_out, d_in]^T
+ *   tg_grouped_dgrad:  dX[t, d_in]  = dY[t, d_out] . W[e, d_out, d_in]
+ *   tg_grouped_wgrad:  dW[e, d_out, d_in] = sum over the rows t of e of
+ *                                           dY[t, d_out]^T . X[t, d_in]
+ * offsets: E + 1 32-bit integers in DEVICE memory, non-decreasing, within
+ * [0, T].  They are read by the kernels (no call waits for the host; a
+ * captured call follows new offsets).  Rows of no expert (before offsets[0],
+ * from offsets[E] on) get zeros; an expert without rows gets dW[e] = 0;
+ * what rows of other experts hold never reaches an expert's results.
+ * Offsets that break the rules give unspecified results, but nothing outside
+ * the tensors is read or written.
+ * T < 2^31 - 1024.  Any widths and alignments run on the tensor cores: an
+ * operand whose rows are no multiple of 8 elements, or whose base is not
+ * 16-byte aligned, is first copied to rows that are, in `ws`: the size is
+ * tg_workspace_size(TG_OP_GROUPED_FWD / _DGRAD / _WGRAD, T, E, d_out, d_in),
+ * or of TG_OP_GROUPED_UNALIGNED when a base is not 16-byte aligned (`ws`
+ * 16-byte aligned).  Results are bitwise reproducible, and a row's result
+ * does not depend on the other rows' values. */
+tg_status tg_grouped_fwd(const void* X, const void* W, const int32_t* offsets, void* Y, int64_t T, int64_t E,
+                         int64_t d_out, int64_t d_in, tg_dtype in, tg_dtype out, void* ws, size_t ws_bytes,
+                         void* stream);
+tg_status tg_grouped_dgrad(const void* dY, const void* W, const int32_t* offsets, void* dX, int64_t T, int64_t E,
+                           int64_t d_out, int64_t d_in, tg_dtype in, tg_dtype out, void* ws, size_t ws_bytes,
+                           void* stream);
+tg_status tg_grouped_wgrad(const void* dY, const void* X, const int32_t* offsets, void* dW, int64_t T, int64_t E,
+                           int64_t d_out, int64_t d_in, tg_dtype in, tg_dtype out, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/* The norm after a block, its gate, the residual sum and the norm before the
+ * next block, in one pass over the rows of B (the block's output, [T, d]) and
+ * H (the residual stream, [T, d]):
+ *   u     = B . rstd_b . w_post            rstd_b[t] = (mean_c B[t,c]^2 + eps)^-1/2
+ *   H_out = res_scale . H + gate . u
+ *   N     = H_out . rstd_h . w_pre         rstd_h[t] = (mean_c H_out[t,c]^2 + eps)^-1/2
+ * w_post, w_pre are [d]; gate_kind says what the gate is broadcast along
+ * (gate NULL with TG_GATE_NONE).  B, w_post, w_pre, gate and N have type `in`
+ * (bf16, fp16 or FP32); H and H_out have type `res` (FP32 or `in`); N and
+ * rstd_h are taken from H_out before its rounding.  H_out may be H.  rstd_b
+ * and rstd_h ([T], FP32; what the backward takes) may be NULL.
+ * FP32 arithmetic, each output rounded once.  d <= 16384.  res_scale finite,
+ * eps finite and >= 0 (a zero row with eps = 0 gives NaN). */
+tg_status tg_norm_residual_fwd(const void* B, const void* H, const void* w_post, const void* w_pre, const void* gate,
+                               tg_gate gate_kind, void* H_out, void* N, float* rstd_b, float* rstd_h, int64_t T,
+                               int64_t d, float res_scale, float eps, tg_dtype in, tg_dtype res, void* stream);
+
+/* Backward of tg_norm_residual_fwd: the gradients of <dH_out, H_out> +
+ * <dN, N> for B, H, w_post, w_pre and the gate, given the forward's inputs
+ * (H_out in H's place) and its rstd_b, rstd_h.  dB has type `in`, dH type
+ * `res`; dw_post, dw_pre ([d]) and the gradient of a broadcast gate ([d] or
+ * [T]) have type `out` (FP32 or `in`); the gradient of a full gate has type
+ * `in`.  dgate NULL with TG_GATE_NONE.  dH may be dH_out, dB may be dN.
+ * Sums over rows are FP32 partials added in a fixed order.  Workspace:
+ * tg_workspace_size(TG_OP_NORM_RESIDUAL_BWD, T, d, 0, 0, in, out), 16-byte
+ * aligned; its content on entry does not matter. */
+tg_status tg_norm_residual_bwd(const void* dH_out, const void* dN, const void* B, const void* H_out, const void* w_post,
+                               const void* w_pre, const void* gate, tg_gate gate_kind, const float* rstd_b,
+                               const float* rstd_h, void* dB, void* dH, void* dw_post, void* dw_pre, void* dgate,
+                               int64_t T, int64_t d, float res_scale, tg_dtype in, tg_dtype res, tg_dtype out, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/* The norm of n gradient tensors taken as one vector, and their scaling to a
+ * largest norm (global-norm gradient clipping):
+ *   norm = sqrt(sum over all elements g^2),  c = min(1, max_norm / (norm + 1e-6))
+ *   outs[i] = round(c . grads[i])
+ * grads, outs, numels, dtypes (tg_dtype values) are HOST arrays of n entries,
+ * read before the call returns; the tensors they point to are device memory,
+ * contiguous, any alignment to their elements, types may be mixed and sizes
+ * zero; outs[i] has grads[i]'s type and may be grads[i].  norm: one FP32
+ * value on the device.  Squares are summed in FP32 groups of at most 32 and
+ * FP64 beyond; magnitudes whose square leaves FP32's range are handled.  A
+ * norm that is infinite gives c = 0, one that is not a number stays so.  When
+ * every output is in place and c = 1 nothing is written to them.  max_norm >=
+ * 0 (may be infinite).  n <= 2^20.  Workspace: tg_workspace_size(
+ * TG_OP_GRAD_CLIP, n, 0, 0, 0, TG_F32, TG_F32), 16-byte aligned.  Results are
+ * bitwise reproducible. */
+tg_status tg_grad_norm(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int64_t n, float* norm,
+                       void* ws, size_t ws_bytes, void* stream);
+tg_status tg_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels, const int32_t* dtypes,
+                       int64_t n, float max_norm, float* norm, void* ws, size_t ws_bytes, void* stream);
 
 /* Bytes of `ws` the call with these sizes needs on the current device
  * (0 when none).  Returns SIZE_MAX for invalid arguments. */

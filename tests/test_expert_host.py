@@ -1,0 +1,96 @@
+"""Host-side checks of the expert-block operators (no GPU): arguments that the C entry points refuse before any
+device work, and the binding's own checks."""
+import ctypes
+
+import pytest
+import torch
+
+import gemms_linear_layers_gb300 as tg
+from gemms_linear_layers_gb300 import _binding as B
+from gemms_linear_layers_gb300 import build
+
+NULL, EVEN, ODD, HALF = (ctypes.c_void_p(x) for x in (0, 0x1000, 0x1001, 0x1002))
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return B.lib()
+
+
+@pytest.mark.parametrize("fn", ["tg_grouped_fwd", "tg_grouped_dgrad", "tg_grouped_wgrad"])
+def test_grouped_products_refuse(lib, fn):
+    f = getattr(lib, fn)
+
+    def call(a=EVEN, b=EVEN, off=EVEN, c=EVEN, T=8, E=2, o=8, i=8, din=B.TG_BF16, dout=B.TG_BF16):
+        return f(a, b, off, c, T, E, o, i, din, dout, NULL, 0, NULL)
+
+    for bad in ({"T": -1}, {"E": -1}, {"o": -8}, {"i": 1 << 31}, {"T": (1 << 31) - 1}):
+        assert call(**bad) == 1, bad
+    for bad in ({"a": NULL}, {"b": NULL}, {"off": NULL}, {"c": NULL}):
+        assert call(**bad) == 1, bad
+    for bad in ({"din": B.TG_F32, "dout": B.TG_F32}, {"din": 7}, {"dout": B.TG_F16}):
+        assert call(**bad) == 2, bad
+    for bad in ({"a": ODD}, {"b": ODD}, {"c": ODD}, {"off": HALF}, {"c": HALF, "dout": B.TG_F32}):
+        assert call(**bad) == 3, bad
+
+
+def test_norms_refuse(lib):
+    def fwd(B_=EVEN, H=EVEN, w=EVEN, gate=NULL, kind=0, out=EVEN, rstd=EVEN, T=4, d=8, scale=1.0, eps=1e-6,
+            din=B.TG_BF16, res=B.TG_BF16):
+        return lib.tg_norm_residual_fwd(B_, H, w, w, gate, kind, out, out, rstd, rstd, T, d, scale, eps, din, res, NULL)
+
+    for bad in ({"T": -1}, {"d": -8}, {"d": 16385}, {"scale": float("nan")}, {"scale": float("inf")}, {"eps": -1e-6},
+                {"eps": float("nan")}, {"kind": 4}, {"kind": -1}, {"kind": 1}, {"B_": NULL}, {"H": NULL}, {"w": NULL},
+                {"out": NULL}):
+        assert fwd(**bad) == 1, bad
+    for bad in ({"din": 5}, {"res": B.TG_F16}, {"din": B.TG_F32, "res": B.TG_BF16}):
+        assert fwd(**bad) == 2, bad
+    for bad in ({"B_": ODD}, {"H": HALF, "res": B.TG_F32}, {"rstd": HALF}, {"kind": 2, "gate": ODD}):
+        assert fwd(**bad) == 3, bad
+
+    def bwd(g=EVEN, w=EVEN, gate=NULL, kind=0, rstd=EVEN, dx=EVEN, dw=EVEN, dgate=NULL, T=4, d=8, scale=1.0,
+            din=B.TG_BF16, res=B.TG_BF16, out=B.TG_BF16):
+        return lib.tg_norm_residual_bwd(g, g, g, g, w, w, gate, kind, rstd, rstd, dx, dx, dw, dw, dgate, T, d, scale, din,
+                                        res, out, NULL, 0, NULL)
+
+    for bad in ({"T": -1}, {"d": 16385}, {"scale": float("inf")}, {"kind": 9}, {"g": NULL}, {"rstd": NULL}, {"dx": NULL},
+                {"dw": NULL}, {"kind": 3, "gate": EVEN}, {"kind": 3, "dgate": EVEN}):
+        assert bwd(**bad) == 1, bad
+    for bad in ({"din": 9}, {"res": B.TG_F16}, {"out": B.TG_F16}):
+        assert bwd(**bad) == 2, bad
+    for bad in ({"g": ODD}, {"rstd": HALF}, {"dw": HALF, "out": B.TG_F32}, {"kind": 1, "gate": EVEN, "dgate": ODD}):
+        assert bwd(**bad) == 3, bad
+
+
+def test_clipping_refuses(lib):
+    def call(p=0x1000, o=0x1000, n=5, dt=B.TG_F32, count=1, max_norm=1.0, norm=EVEN, outs=True):
+        ps, os, ns, ds = (ctypes.c_void_p * 1)(p), (ctypes.c_void_p * 1)(o), (ctypes.c_int64 * 1)(n), (ctypes.c_int32 * 1)(dt)
+        return lib.tg_grad_clip(ps, os if outs else NULL, ns, ds, count, max_norm, norm, NULL, 0, NULL)
+
+    for bad in ({"count": -1}, {"count": (1 << 20) + 1}, {"max_norm": -1.0}, {"max_norm": float("nan")}, {"norm": NULL},
+                {"p": 0}, {"o": 0}, {"n": -1}, {"n": 1 << 41}, {"outs": False}):
+        assert call(**bad) == 1, bad
+    assert call(dt=3) == 2 and call(dt=-1) == 2
+    for bad in ({"p": 0x1002}, {"o": 0x1001, "dt": B.TG_BF16, "p": 0x1000}, {"norm": HALF}):
+        assert call(**bad) == 3, bad
+    assert lib.tg_grad_norm(NULL, NULL, NULL, 1, EVEN, NULL, 0, NULL) == 1
+
+
+def test_the_binding_takes_cuda_tensors_only():
+    x, w, o = torch.zeros(4, 8), torch.zeros(2, 8, 8), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        tg.tg_grouped_fwd(x, w, o)
+    with pytest.raises(ValueError):
+        tg.tg_grouped_wgrad(x, x, o)
+    with pytest.raises(ValueError):
+        tg.tg_norm_residual_fwd(x, x, x[0], x[0])
+    with pytest.raises(ValueError):
+        tg.tg_tensor_list([x])
+
+
+def test_exported():
+    import gemms_linear_layers_gb300 as pkg
+    for n in B.SIGNATURES:
+        if n.startswith(("tg_grouped", "tg_norm", "tg_grad")):
+            assert n in pkg.__all__, n
