@@ -208,9 +208,12 @@ __device__ __forceinline__ GtUnit gt_unit(const GtArgs& a, const GtTab<OP>& t, i
   return c;
 }
 
-// arrivals on rank 0's barriers
+// Arrivals on rank 0's barriers.  The producer's publishes nothing of its own
+// (the copies' bytes complete the phase), so it is relaxed: a cluster-scope
+// release in its place made 16,384 rows of 2,304 -> 5,760 over 64 experts take
+// 905 us instead of 402.  The mender's publishes its zeros.
 __device__ __forceinline__ void arrive_expect_tx_cluster(uint32_t cluster_addr, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
                "r"(bytes)
                : "memory");
 }

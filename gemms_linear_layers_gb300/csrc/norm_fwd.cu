@@ -1,0 +1,164 @@
+// norm_fwd.cu -- the norm after a block, its gate, the residual sum and the
+// norm before the next block, in one pass over the rows.
+//
+//   u  = B rstd_b w_post             rstd_b = (mean_c B^2 + eps)^-1/2
+//   H' = res_scale H + gate u
+//   N  = H' rstd_h w_pre             rstd_h = (mean_c H'^2 + eps)^-1/2
+// FP32 arithmetic, every output rounded once; N is taken from the unrounded
+// H'.  Bound by HBM: 2 values (3 with an element-wise gate) read and 2 written
+// an element.
+#include "norm_residual.cuh"
+
+namespace tg {
+namespace {
+using namespace nr;
+
+constexpr int FWD_THREADS = 512;  // of a CTA
+constexpr int FWD_PER_SM = 4;
+constexpr int FWD_DEPTH = 2;      // rows in the ring
+
+template <typename IN, typename RES, int VPT, int FEED>
+__global__ void __launch_bounds__(FWD_THREADS) norm_fwd_kernel(const Args a) {
+  constexpr bool VEC = FEED != FEED_SCALAR;
+  constexpr int D = FWD_DEPTH;
+  extern __shared__ __align__(16) uint8_t ring_smem[];
+  __shared__ float2 slots[MAX_TEAMS][32];
+  const int team_id = threadIdx.x / a.team, t = threadIdx.x - team_id * a.team;
+  float2* slot = slots[team_id];
+  const int d = a.d;
+  const float inv_d = 1.f / static_cast<float>(d);
+  const bool full = a.gate_kind == GATE_FULL, channel = a.gate_kind == GATE_CHANNEL;
+  const Ring ring = ring_of(ring_smem, VPT * (Pack<RES>::WORDS + (full ? 2 : 1) * Pack<IN>::WORDS));
+  pdl_wait();
+  pdl_trigger();
+  const long long step = static_cast<long long>(gridDim.x) * a.teams;
+  const long long row0 = static_cast<long long>(blockIdx.x) * a.teams + team_id;
+  auto fetch = [&](long long row, int stage) {
+    if (row < a.T) {
+      int w = 0;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int c = (v * a.team + t) * 8;
+        ring_copy<IN>(ring, stage, w, a.B, row, c, d);
+        ring_copy<RES>(ring, stage, w, a.H, row, c, d);
+        if (full) ring_copy<IN>(ring, stage, w, a.gate, row, c, d);
+      }
+    }
+    ring_commit();
+  };
+  if (FEED == FEED_RING) {
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) fetch(row0 + i * step, i);
+  }
+  Pack<IN> wpost[VPT], wpre[VPT], g[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int c = (v * a.team + t) * 8;
+    wpost[v] = load8<IN, VEC>(a.w_post, 0, c, d);
+    wpre[v] = load8<IN, VEC>(a.w_pre, 0, c, d);
+    if (channel) g[v] = load8<IN, VEC>(a.gate, 0, c, d);
+  }
+  int which = 0, stage = 0;
+  for (long long row = row0; row < a.T; row += step) {
+    Pack<IN> b[VPT];
+    Pack<RES> h[VPT];
+    const float gt = a.gate_kind == GATE_TOKEN ? to_f(static_cast<const IN*>(a.gate)[row]) : 1.f;
+    if (FEED == FEED_RING) {
+      fetch(row + (D - 1) * step, stage + D - 1 < D ? stage + D - 1 : stage - 1);
+      ring_wait<D - 1>();
+      int w = 0;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int c = (v * a.team + t) * 8;
+        b[v] = ring_read<IN>(ring, stage, w, c, d);
+        h[v] = ring_read<RES>(ring, stage, w, c, d);
+        if (full) g[v] = ring_read<IN>(ring, stage, w, c, d);
+      }
+      stage = stage + 1 < D ? stage + 1 : 0;
+    } else {
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int c = (v * a.team + t) * 8;
+        b[v] = load8<IN, VEC>(a.B, row, c, d);
+        h[v] = load8<RES, VEC>(a.H, row, c, d);
+        if (full) g[v] = load8<IN, VEC>(a.gate, row, c, d);
+      }
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x = to_f(b[v].v[j]);
+        s = fmaf(x, x, s);
+      }
+    s = team_sum(make_float2(s, 0.f), slot, which, team_id, a.team, t).x;
+    which ^= 1;
+    const float rb = rsqrtf(s * inv_d + a.eps);
+    float x[VPT][8];
+    s = 0.f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float u = to_f(b[v].v[j]) * rb * to_f(wpost[v].v[j]) * (full || channel ? to_f(g[v].v[j]) : gt);
+        x[v][j] = fmaf(a.res_scale, to_f(h[v].v[j]), u);
+        s = fmaf(x[v][j], x[v][j], s);
+      }
+      store8<RES, VEC>(a.H_out, row, (v * a.team + t) * 8, d, x[v]);
+    }
+    s = team_sum(make_float2(s, 0.f), slot, which, team_id, a.team, t).x;
+    which ^= 1;
+    const float rh = rsqrtf(s * inv_d + a.eps);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[v][j] *= rh * to_f(wpre[v].v[j]);
+      store8<IN, VEC>(a.N, row, (v * a.team + t) * 8, d, x[v]);
+    }
+    if (t == 0) {
+      if (a.rstd_b) a.rstd_b[row] = rb;
+      if (a.rstd_h) a.rstd_h[row] = rh;
+    }
+  }
+  if (FEED == FEED_RING) ring_wait<0>();
+}
+
+template <typename IN, typename RES, int VPT, int FEED>
+cudaError_t fwd_one(const NormResidual& n, const Geo& g) {
+  const Args a = to_args(n, g);
+  auto kern = norm_fwd_kernel<IN, RES, VPT, FEED>;
+  const int words = VPT * (Pack<RES>::WORDS + (n.gate_kind == GATE_FULL ? 2 : 1) * Pack<IN>::WORDS);
+  const int smem = FEED == FEED_RING ? FWD_DEPTH * words * g.team * g.teams * 16 : 0;
+  if (smem > 0) {
+    const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_k(kern, dim3(g.ctas), dim3(g.team * g.teams), smem, n.stream, a);
+}
+template <typename IN, typename RES>
+cudaError_t fwd_types(const NormResidual& n) {
+  const Geo g = geometry(n.T, n.d, n.num_sms, FWD_THREADS, FWD_PER_SM);
+  // a gate of one value a row needs no alignment
+  const bool wide_gate = n.gate_kind == GATE_FULL || n.gate_kind == GATE_CHANNEL;
+  const bool vec = vec_ok({n.B, n.H, n.w_post, n.w_pre, n.H_out, n.N, wide_gate ? n.gate : nullptr}, n.d);
+  // the ring: up to 8,192 columns (64 KB of FP32 stream and 32 KB of 16-bit values a row at most)
+  switch (g.vpt) {
+    case 1: return vec ? fwd_one<IN, RES, 1, FEED_RING>(n, g) : fwd_one<IN, RES, 1, FEED_SCALAR>(n, g);
+    case 2: return vec ? fwd_one<IN, RES, 2, FEED_RING>(n, g) : fwd_one<IN, RES, 2, FEED_SCALAR>(n, g);
+    default: return vec ? fwd_one<IN, RES, 4, FEED_VEC>(n, g) : fwd_one<IN, RES, 4, FEED_SCALAR>(n, g);
+  }
+}
+
+}  // namespace
+
+cudaError_t norm_residual_fwd_launch(const NormResidual& n) {
+  const bool r32 = n.res_kind == EK_F32;
+  switch (n.in_kind) {
+    case EK_BF16: return r32 ? fwd_types<__nv_bfloat16, float>(n) : fwd_types<__nv_bfloat16, __nv_bfloat16>(n);
+    case EK_F16: return r32 ? fwd_types<__half, float>(n) : fwd_types<__half, __half>(n);
+    default: return fwd_types<float, float>(n);
+  }
+}
+
+}  // namespace tg

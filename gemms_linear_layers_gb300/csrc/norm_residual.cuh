@@ -1,0 +1,239 @@
+// norm_residual.cuh -- what the forward and backward kernels of the norms
+// around a block share: eight-element loads and stores, the ring of rows in
+// flight, sums over the threads of a row, the launch geometry.
+//
+// A team of 32..512 threads owns a row, thread t the 8-element groups t,
+// t + team, ..; a CTA holds several teams when rows are short.  Columns stay
+// with their thread from row to row.
+//
+// The kernels are bound by HBM, and what feeds it is bytes in flight: about
+// 50 KB an SM at its latency.  Each thread copies its own groups of the team's
+// next row into shared memory with cp.async while it works on the present one
+// (a thread reads only what it copied itself, so the ring needs no barrier).
+// Rows in registers alone left the loads waiting behind each row's two sums:
+// 16,384 x 2,304 forward ran at 2.7 TB/s that way.
+#pragma once
+#include <initializer_list>
+
+#include "norm_residual.h"
+#include "ptx.cuh"
+#include "smem_attr.h"
+
+namespace tg {
+namespace nr {
+
+constexpr int MAX_TEAM = 512;
+constexpr int CTA_THREADS = 576;  // most threads of a CTA
+constexpr int MAX_TEAMS = 15;     // named barriers 1..15
+constexpr int SMEM_BYTES = 220 * 1024;  // dynamic, beside 4 KB of the teams' slots
+
+struct Args {
+  const void *B, *H, *w_post, *w_pre, *gate, *dH_out, *dN;
+  float *rstd_b, *rstd_h;
+  void *H_out, *N, *dB, *dH, *dgate;
+  float* part;  // backward: [CTA][3][d]
+  long long T;
+  int d;
+  int team, teams;  // threads of a team, teams of a CTA
+  float res_scale, eps;
+  int gate_kind, out_kind;
+};
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
+
+// Eight consecutive elements as they lie in memory.
+template <typename T>
+struct alignas(16) Pack {
+  T v[8];
+  static constexpr int WORDS = sizeof(T) / 2;  // of 16 bytes
+};
+template <typename T>
+__device__ __forceinline__ Pack<T> zeros() {
+  Pack<T> r;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) r.v[j] = from_f<T>(0.f);
+  return r;
+}
+
+// c: first column; VEC: rows start at multiples of 16 bytes and d is a
+// multiple of 8 (checked on the host); otherwise element by element
+template <typename T, bool VEC>
+__device__ __forceinline__ Pack<T> load8(const void* base, long long row, int c, int d) {
+  Pack<T> r = zeros<T>();
+  const T* p = static_cast<const T*>(base) + row * d + c;
+  if (VEC) {
+    if (c < d) {
+#pragma unroll
+      for (int i = 0; i < Pack<T>::WORDS; ++i) reinterpret_cast<uint4*>(&r)[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < d) r.v[j] = p[j];
+  }
+  return r;
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(void* base, long long row, int c, int d, const float* f) {
+  T* p = static_cast<T*>(base) + row * d + c;
+  Pack<T> r;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) r.v[j] = from_f<T>(f[j]);
+  if (VEC) {
+    if (c < d) {
+#pragma unroll
+      for (int i = 0; i < Pack<T>::WORDS; ++i) reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<uint4*>(&r)[i];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < d) p[j] = r.v[j];
+  }
+}
+
+// ------------------------------------------------------------ ring of rows
+// Word w of stage s of this thread sits at ((s * words + w) * threads + tid) * 16.
+struct Ring {
+  uint32_t base;  // shared address of this thread's word 0 of stage 0
+  uint32_t word, stage;  // bytes from one word to the next, one stage to the next
+};
+__device__ __forceinline__ Ring ring_of(const void* smem, int words) {
+  Ring r;
+  r.base = smem_u32(smem) + threadIdx.x * 16;
+  r.word = blockDim.x * 16;
+  r.stage = r.word * words;
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void ring_copy(const Ring& r, int stage, int& w, const void* base, long long row, int c, int d) {
+  const T* p = static_cast<const T*>(base) + row * d + c;
+#pragma unroll
+  for (int i = 0; i < Pack<T>::WORDS; ++i, ++w)
+    if (c < d)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(r.base + stage * r.stage + w * r.word),
+                   "l"(reinterpret_cast<const char*>(p) + 16 * i)
+                   : "memory");
+}
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void ring_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ Pack<T> ring_read(const Ring& r, int stage, int& w, int c, int d) {
+  Pack<T> v = zeros<T>();
+#pragma unroll
+  for (int i = 0; i < Pack<T>::WORDS; ++i, ++w)
+    if (c < d) {
+      uint4& x = reinterpret_cast<uint4*>(&v)[i];
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                   : "r"(r.base + stage * r.stage + w * r.word)
+                   : "memory");
+    }
+  return v;
+}
+
+// -------------------------------------------------------- sums over a team
+__device__ __forceinline__ void team_sync(int team_id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(team_id + 1), "r"(threads) : "memory");
+}
+
+// Sums of (x, y) over the team; every thread gets them, added in the same
+// order.  `slot`: shared space for 2 x 16 pairs of this team; `which` alternates
+// between its halves, so one barrier a call is enough.
+__device__ __forceinline__ float2 team_sum(float2 v, float2* slot, int which, int team_id, int team, int t) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(~0u, v.x, o);
+    v.y += __shfl_xor_sync(~0u, v.y, o);
+  }
+  const int warps = team >> 5;
+  if (warps == 1) return v;
+  float2* s = slot + which * 16;
+  if ((t & 31) == 0) s[t >> 5] = v;
+  team_sync(team_id, team);
+  float2 r = s[0];
+  for (int i = 1; i < warps; ++i) {
+    r.x += s[i].x;
+    r.y += s[i].y;
+  }
+  return r;
+}
+
+// ----------------------------------------------------------------- host side
+struct Geo {
+  int vpt, team, teams, ctas;
+};
+// Threads of a team: one per 8-element group up to 512, then 2 or 4 groups a
+// thread; teams to fill a CTA.
+inline Geo geometry(int64_t T, int64_t d, int sms, int threads, int ctas_per_sm) {
+  Geo g;
+  const int groups = static_cast<int>((d + 7) / 8);
+  g.vpt = groups <= MAX_TEAM ? 1 : groups <= 2 * MAX_TEAM ? 2 : 4;
+  g.team = ((groups + g.vpt - 1) / g.vpt + 31) / 32 * 32;
+  g.teams = threads / g.team;
+  if (g.teams < 1) g.teams = 1;
+  if (g.teams > MAX_TEAMS) g.teams = MAX_TEAMS;
+  const int64_t rows = (T + sms - 1) / sms;  // rows of an SM
+  if (g.teams > rows) g.teams = static_cast<int>(rows);
+  const int64_t most = (T + g.teams - 1) / g.teams, want = static_cast<int64_t>(sms) * ctas_per_sm;
+  g.ctas = static_cast<int>(most < want ? most : want);
+  return g;
+}
+
+inline bool vec_ok(std::initializer_list<const void*> ps, int64_t d) {
+  if (d % 8) return false;
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) % 16) return false;
+  return true;
+}
+
+inline Args to_args(const NormResidual& n, const Geo& g) {
+  Args a = {};
+  a.B = n.B;
+  a.H = n.H;
+  a.w_post = n.w_post;
+  a.w_pre = n.w_pre;
+  a.gate = n.gate;
+  a.dH_out = n.dH_out;
+  a.dN = n.dN;
+  a.rstd_b = n.rstd_b;
+  a.rstd_h = n.rstd_h;
+  a.H_out = n.H_out;
+  a.N = n.N;
+  a.dB = n.dB;
+  a.dH = n.dH;
+  a.dgate = n.dgate;
+  a.part = n.ws;
+  a.T = n.T;
+  a.d = static_cast<int>(n.d);
+  a.team = g.team;
+  a.teams = g.teams;
+  a.res_scale = n.res_scale;
+  a.eps = n.eps;
+  a.gate_kind = n.gate_kind;
+  a.out_kind = n.out_kind;
+  return a;
+}
+
+// How a kernel takes its rows.
+enum Feed : int { FEED_SCALAR = 0, FEED_VEC = 1, FEED_RING = 2 };
+
+}  // namespace nr
+}  // namespace tg

@@ -1,4 +1,4 @@
-// norm_residual.h -- launchers of the norms around a block (norm_residual.cu).
+// norm_residual.h -- launchers of the norms around a block (norm_fwd.cu, norm_bwd.cu).
 #pragma once
 #include "tg_internal.h"
 
