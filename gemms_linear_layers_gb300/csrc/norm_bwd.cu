@@ -9,14 +9,18 @@
 // gate) read and 2 (3) written an element, in one pass: the column sums build
 // up in registers (rows of up to 4,096 columns; in shared memory beyond, where
 // 16 or 32 columns a thread would spill); the teams of a CTA are added in
-// shared memory, the CTAs by a second launch, all in a fixed order.
+// shared memory, the CTAs by a second launch, all in a fixed order.  The
+// second mean is taken from sums that do not wait for the first (q and e
+// below), so a row costs one exchange between its threads, not two.
 #include "norm_residual.cuh"
 
 namespace tg {
 namespace {
 using namespace nr;
 
-constexpr int BWD_THREADS = 576;  // of a CTA: one CTA an SM (few partial sums), 18 warps
+// Threads of a CTA; one CTA an SM (few partial sums).  27 warps at 72 registers;
+// an element-wise gate needs more registers (18 warps at 112).
+constexpr int bwd_threads(bool el) { return el ? 576 : 864; }
 constexpr int BWD_DEPTH = 2;      // rows in the ring
 
 __device__ __forceinline__ void put_kind(void* p, long long i, float v, int kind) {
@@ -25,18 +29,19 @@ __device__ __forceinline__ void put_kind(void* p, long long i, float v, int kind
   else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
-template <typename IN, typename RES, int VPT, int FEED>
-__global__ void __launch_bounds__(VPT > 1 ? MAX_TEAM : BWD_THREADS, 1) norm_bwd_kernel(const Args a) {
+// EL: the gate differs from element to element (full or channel); otherwise
+// it is one value a row, or 1
+template <typename IN, typename RES, int VPT, int FEED, bool EL>
+__global__ void __launch_bounds__(VPT > 1 ? MAX_TEAM : bwd_threads(EL), 1) norm_bwd_kernel(const Args a) {
   constexpr bool VEC = FEED != FEED_SCALAR;
   constexpr int D = BWD_DEPTH;
   extern __shared__ __align__(16) uint8_t ring_smem[];  // the ring, then the column sums [3][d]
-  __shared__ float2 slots[MAX_TEAMS][32];
+  __shared__ float4 slots[MAX_TEAMS][32];
   const int team_id = threadIdx.x / a.team, t = threadIdx.x - team_id * a.team;
-  float2* slot = slots[team_id];
+  float4* slot = slots[team_id];
   const int d = a.d;
   const float inv_d = 1.f / static_cast<float>(d);
-  const bool full = a.gate_kind == GATE_FULL, channel = a.gate_kind == GATE_CHANNEL;
-  const bool per_element = full || channel;
+  const bool full = EL && a.gate_kind == GATE_FULL, channel = EL && a.gate_kind == GATE_CHANNEL;
   const Ring ring = ring_of(ring_smem, VPT * (2 * Pack<RES>::WORDS + (full ? 3 : 2) * Pack<IN>::WORDS));
   pdl_wait();
   pdl_trigger();
@@ -49,10 +54,10 @@ __global__ void __launch_bounds__(VPT > 1 ? MAX_TEAM : BWD_THREADS, 1) norm_bwd_
       for (int v = 0; v < VPT; ++v) {
         const int c = (v * a.team + t) * 8;
         ring_copy<RES>(ring, stage, w, a.H, row, c, d);
-        ring_copy<IN>(ring, stage, w, a.dN, row, c, d);
-        ring_copy<RES>(ring, stage, w, a.dH_out, row, c, d);
         ring_copy<IN>(ring, stage, w, a.B, row, c, d);
         if (full) ring_copy<IN>(ring, stage, w, a.gate, row, c, d);
+        ring_copy<IN>(ring, stage, w, a.dN, row, c, d);
+        ring_copy<RES>(ring, stage, w, a.dH_out, row, c, d);
       }
     }
     ring_commit();
@@ -61,19 +66,19 @@ __global__ void __launch_bounds__(VPT > 1 ? MAX_TEAM : BWD_THREADS, 1) norm_bwd_
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) fetch(row0 + i * step, i);
   }
-  // VPT > 1 (one team a CTA): sum k of the thread's group v, half i at (((k * VPT + v) * 2 + i) * team + t)
+  // VPT > 1 (one team a CTA): column sum k of the thread's group v, half i at (((k * VPT + v) * 2 + i) * team + t)
   constexpr bool IN_SMEM = VPT > 1;
   const int ring_bytes = FEED == FEED_RING ? D * static_cast<int>(ring.stage) : 0;
   float4* accs = reinterpret_cast<float4*>(ring_smem + ring_bytes) + t;
   auto at = [&](int k, int v, int i) -> float4& { return accs[((k * VPT + v) * 2 + i) * a.team]; };
-  auto add8 = [&](int k, int v, const float* x) {
+  auto add8 = [&](int k, int v, const float2* x, float by) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float4 f = at(k, v, i);
-      f.x += x[4 * i];
-      f.y += x[4 * i + 1];
-      f.z += x[4 * i + 2];
-      f.w += x[4 * i + 3];
+      f.x = fmaf(x[2 * i].x, by, f.x);
+      f.y = fmaf(x[2 * i].y, by, f.y);
+      f.z = fmaf(x[2 * i + 1].x, by, f.z);
+      f.w = fmaf(x[2 * i + 1].y, by, f.w);
       at(k, v, i) = f;
     }
   };
@@ -82,109 +87,113 @@ __global__ void __launch_bounds__(VPT > 1 ? MAX_TEAM : BWD_THREADS, 1) norm_bwd_
 #pragma unroll
       for (int v = 0; v < VPT; ++v) at(k, v, 0) = at(k, v, 1) = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  float acc_post[8] = {}, acc_pre[8] = {}, acc_gate[8] = {};
+  float2 acc_post[4] = {}, acc_pre[4] = {}, acc_gate[4] = {};
   int which = 0, stage = 0;
+  // a row's scalars are loaded a row ahead too
+  const bool token = !EL && a.gate_kind == GATE_TOKEN;
+  float rb_next = 0.f, rh_next = 0.f, gt_next = 1.f;
+  auto scalars = [&](long long row) {
+    if (row < a.T) {
+      rb_next = a.rstd_b[row];
+      rh_next = a.rstd_h[row];
+      if (token) gt_next = to_f(static_cast<const IN*>(a.gate)[row]);
+    }
+  };
+  scalars(row0);
   for (long long row = row0; row < a.T; row += step) {
-    Pack<IN> b[VPT], dn[VPT], g[VPT];
-    Pack<RES> h[VPT], dho[VPT];
-    const float gt = a.gate_kind == GATE_TOKEN ? to_f(static_cast<const IN*>(a.gate)[row]) : 1.f;
-    const float rb = a.rstd_b[row], rh = a.rstd_h[row];
+    const float rb = rb_next, rh = rh_next, gt = gt_next;
+    scalars(row + step);
     if (FEED == FEED_RING) {
       fetch(row + (D - 1) * step, stage + D - 1 < D ? stage + D - 1 : stage - 1);
       ring_wait<D - 1>();
-      int w = 0;
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int c = (v * a.team + t) * 8;
-        h[v] = ring_read<RES>(ring, stage, w, c, d);
-        dn[v] = ring_read<IN>(ring, stage, w, c, d);
-        dho[v] = ring_read<RES>(ring, stage, w, c, d);
-        b[v] = ring_read<IN>(ring, stage, w, c, d);
-        if (full) g[v] = ring_read<IN>(ring, stage, w, c, d);
-      }
-      stage = stage + 1 < D ? stage + 1 : 0;
-    } else {
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int c = (v * a.team + t) * 8;
-        h[v] = load8<RES, VEC>(a.H, row, c, d);
-        dn[v] = load8<IN, VEC>(a.dN, row, c, d);
-        dho[v] = load8<RES, VEC>(a.dH_out, row, c, d);
-        b[v] = load8<IN, VEC>(a.B, row, c, d);
-        if (full) g[v] = load8<IN, VEC>(a.gate, row, c, d);
-      }
     }
-    float s = 0.f;
+    // Group v of the thread: everything for the sums; for the results H', B
+    // and the gate are taken again (all of it kept between the two would spill).
+    Pack<IN> b, dn, g, wpre, wpost;
+    Pack<RES> h, dho;
+    auto take = [&](int v, bool sums) {
+      const int c = (v * a.team + t) * 8;
+      if (FEED == FEED_RING) {
+        int w = v * (2 * Pack<RES>::WORDS + (full ? 3 : 2) * Pack<IN>::WORDS);
+        h = ring_read<RES>(ring, stage, w, c, d);
+        b = ring_read<IN>(ring, stage, w, c, d);
+        if (full) g = ring_read<IN>(ring, stage, w, c, d);
+        if (sums) dn = ring_read<IN>(ring, stage, w, c, d);
+        if (sums) dho = ring_read<RES>(ring, stage, w, c, d);
+      } else {
+        h = load8<RES, VEC>(a.H, row, c, d);
+        b = load8<IN, VEC>(a.B, row, c, d);
+        if (full) g = load8<IN, VEC>(a.gate, row, c, d);
+        if (sums) dn = load8<IN, VEC>(a.dN, row, c, d);
+        if (sums) dho = load8<RES, VEC>(a.dH_out, row, c, d);
+      }
+      if (channel) g = load8<IN, VEC>(a.gate, 0, c, d);
+      if (sums) wpre = load8<IN, VEC>(a.w_pre, 0, c, d);
+      wpost = load8<IN, VEC>(a.w_post, 0, c, d);
+    };
+    // With g1 = dN w_pre, q = B w_post (times an element-wise gate) and
+    // e = dH' + rstd_h g1:  sum of g2 bn = rstd_b (sum of q e - rstd_h^2 mean(g1 H') (sum of q H'))
+    float2 s1 = both(0.f), sa = both(0.f), sb = both(0.f);
+    const float2 rh2 = both(rh);
+    float2 e[VPT][4];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      const int c = (v * a.team + t) * 8;
-      const Pack<IN> wpre = load8<IN, VEC>(a.w_pre, 0, c, d);
-      if (channel) g[v] = load8<IN, VEC>(a.gate, 0, c, d);
-      float p[8];
+      float2 p[4];
+      take(v, true);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        p[j] = to_f(dn[v].v[j]) * (to_f(h[v].v[j]) * rh);
-        if (!IN_SMEM) acc_pre[j] += p[j];
-        s = fmaf(p[j], to_f(wpre.v[j]), s);
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = two(h, j), n = two(dn, j), g1 = mul2(n, two(wpre, j));
+        s1 = fma2(g1, x, s1);
+        p[j] = mul2(n, x);  // dw_pre's term, without rstd_h
+        if (!IN_SMEM) acc_pre[j] = fma2(p[j], rh2, acc_pre[j]);
+        float2 q = mul2(two(b, j), two(wpost, j));
+        if (EL) q = mul2(q, two(g, j));
+        e[v][j] = fma2(rh2, g1, two(dho, j));
+        sa = fma2(q, e[v][j], sa);
+        sb = fma2(q, x, sb);
       }
-      if (IN_SMEM) add8(1, v, p);
+      if (IN_SMEM) add8(1, v, p, rh);
     }
-    s = team_sum(make_float2(s, 0.f), slot, which, team_id, a.team, t).x;
+    const float3 sum =
+        team_sum3(make_float3(s1.x + s1.y, sa.x + sa.y, sb.x + sb.y), slot, which, team_id, a.team, t);
     which ^= 1;
-    const float m1 = s * inv_d;
-    float dh[VPT][8];
-    float2 s2 = make_float2(0.f, 0.f);  // (sum of g2 bn, sum of dgate)
+    const float k1 = rh * (rh * (rh * sum.x * inv_d));  // rstd_h times rstd_h times mean(g1 hn)
+    const float s2 = rb * (sum.y - k1 * sum.z);
+    if (token && t == 0) put_kind(a.dgate, row, s2, a.out_kind);
+    // dB = (rstd_b gate) dh w_post - (rstd_b^2 mean(g2 bn)) B
+    const float2 mk1 = both(-k1), c1 = both(rb * gt), c2 = both(-rb * (rb * (gt * s2 * inv_d))), sc = both(a.res_scale);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = (v * a.team + t) * 8;
-      const Pack<IN> wpre = load8<IN, VEC>(a.w_pre, 0, c, d);
-      const Pack<IN> wpost = load8<IN, VEC>(a.w_post, 0, c, d);
-      float o[8];
+      float2 dh[4], o[4];
+      take(v, false);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float hn = to_f(h[v].v[j]) * rh;
-        const float x = to_f(dho[v].v[j]) + rh * (to_f(dn[v].v[j]) * to_f(wpre.v[j]) - hn * m1);
-        o[j] = a.res_scale * x;
-        dh[v][j] = x;
+      for (int j = 0; j < 4; ++j) {
+        dh[j] = fma2(mk1, two(h, j), e[v][j]);
+        o[j] = mul2(sc, dh[j]);
       }
       store8<RES, VEC>(a.dH, row, c, d, o);
-      float q[8];
+      float2 q[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float bn = to_f(b[v].v[j]) * rb;
-        const float e = dh[v][j] * bn;          // dw_post's term before the gate
-        const float dg = e * to_f(wpost.v[j]);  // the gate's gradient, element by element
-        const float gg = per_element ? to_f(g[v].v[j]) : gt;
-        q[j] = gg * e;
-        if (!IN_SMEM) acc_post[j] += q[j];
-        s2.x = fmaf(gg, dg, s2.x);
-        s2.y += dg;
-        if (!IN_SMEM && channel) acc_gate[j] += dg;
-        o[j] = dg;
-      }
-      if (IN_SMEM) {
-        add8(0, v, q);
-        if (channel) add8(2, v, o);
-      }
-      if (full) store8<IN, VEC>(a.dgate, row, c, d, o);
-    }
-    s2 = team_sum(s2, slot, which, team_id, a.team, t);
-    which ^= 1;
-    if (a.gate_kind == GATE_TOKEN && t == 0) put_kind(a.dgate, row, s2.y, a.out_kind);
-    const float m2 = s2.x * inv_d;
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int c = (v * a.team + t) * 8;
-      const Pack<IN> wpost = load8<IN, VEC>(a.w_post, 0, c, d);
-      float o[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float gg = per_element ? to_f(g[v].v[j]) : gt;
-        const float bn = to_f(b[v].v[j]) * rb;
-        o[j] = rb * (gg * dh[v][j] * to_f(wpost.v[j]) - bn * m2);
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = two(b, j), w = two(wpost, j);
+        const float2 du = EL ? mul2(dh[j], two(g, j)) : dh[j];  // without a gate of one value a row: c1 holds it
+        q[j] = mul2(du, x);
+        if (!IN_SMEM) acc_post[j] = fma2(q[j], c1, acc_post[j]);
+        o[j] = fma2(mul2(du, w), c1, mul2(c2, x));
+        if (EL) {
+          dh[j] = mul2(mul2(dh[j], x), mul2(w, c1));  // the gate's gradient, element by element
+          if (!IN_SMEM && channel) acc_gate[j] = add2(acc_gate[j], dh[j]);
+        }
       }
       store8<IN, VEC>(a.dB, row, c, d, o);
+      if (EL && full) store8<IN, VEC>(a.dgate, row, c, d, dh);
+      if (IN_SMEM) {
+        add8(0, v, q, rb * gt);
+        if (EL && channel) add8(2, v, dh, 1.f);
+      }
     }
+    stage = stage + 1 < D ? stage + 1 : 0;
   }
   if (FEED == FEED_RING) ring_wait<0>();
   const int sums = channel ? 3 : 2;
@@ -215,9 +224,9 @@ __global__ void __launch_bounds__(VPT > 1 ? MAX_TEAM : BWD_THREADS, 1) norm_bwd_
       for (int j = 0; j < 8; ++j)
         if (t * 8 + j < d) {
           float* p = col + t * 8 + j;
-          p[0] = (k ? p[0] : 0.f) + acc_post[j];
-          p[d] = (k ? p[d] : 0.f) + acc_pre[j];
-          if (channel) p[2 * d] = (k ? p[2 * d] : 0.f) + acc_gate[j];
+          p[0] = (k ? p[0] : 0.f) + (j & 1 ? acc_post[j / 2].y : acc_post[j / 2].x);
+          p[d] = (k ? p[d] : 0.f) + (j & 1 ? acc_pre[j / 2].y : acc_pre[j / 2].x);
+          if (EL && channel) p[2 * d] = (k ? p[2 * d] : 0.f) + (j & 1 ? acc_gate[j / 2].y : acc_gate[j / 2].x);
         }
     }
   }
@@ -248,8 +257,8 @@ __global__ void __launch_bounds__(256) norm_cols_kernel(const float* part, int c
   }
 }
 
-Geo bwd_geometry(int64_t T, int64_t d, int sms) {
-  Geo g = geometry(T, d, sms, BWD_THREADS, 1);
+Geo bwd_geometry(int64_t T, int64_t d, int sms, bool el) {
+  Geo g = geometry(T, d, sms, bwd_threads(el), 1);
   if (g.vpt > 1) {  // one row at a time
     g.teams = 1;
     g.ctas = static_cast<int>(T < sms ? T : sms);
@@ -263,7 +272,8 @@ int sum_bytes(const Geo& g, int64_t d) { return static_cast<int>(g.vpt > 1 ? 3 *
 template <typename IN, typename RES, int VPT, int FEED>
 cudaError_t bwd_one(const NormResidual& n, const Geo& g) {
   const Args a = to_args(n, g);
-  auto kern = norm_bwd_kernel<IN, RES, VPT, FEED>;
+  const bool el = n.gate_kind == GATE_FULL || n.gate_kind == GATE_CHANNEL;
+  auto kern = el ? norm_bwd_kernel<IN, RES, VPT, FEED, true> : norm_bwd_kernel<IN, RES, VPT, FEED, false>;
   const int words = VPT * (2 * Pack<RES>::WORDS + (n.gate_kind == GATE_FULL ? 3 : 2) * Pack<IN>::WORDS);
   const int ring = FEED == FEED_RING ? ring_bytes(g, words) : 0, sums_at = sum_bytes(g, n.d);
   const int smem = VPT > 1 ? ring + sums_at : ring > sums_at ? ring : sums_at;
@@ -278,13 +288,13 @@ cudaError_t bwd_one(const NormResidual& n, const Geo& g) {
 }
 template <typename IN, typename RES>
 cudaError_t bwd_types(const NormResidual& n) {
-  Geo g = bwd_geometry(n.T, n.d, n.num_sms);
   const bool full = n.gate_kind == GATE_FULL, wide_gate = full || n.gate_kind == GATE_CHANNEL;
+  Geo g = bwd_geometry(n.T, n.d, n.num_sms, wide_gate);
   const bool vec = vec_ok({n.B, n.H, n.w_post, n.w_pre, n.dH_out, n.dN, n.dB, n.dH, wide_gate ? n.gate : nullptr,
                            full ? n.dgate : nullptr},
                           n.d);
   const int words = g.vpt * (2 * Pack<RES>::WORDS + (full ? 3 : 2) * Pack<IN>::WORDS);
-  while (g.teams > 1 && ring_bytes(g, words) > SMEM_BYTES) --g.teams;  // fewer rows at once
+  while (g.teams > 1 && ring_bytes(g, words) > SMEM_BYTES) --g.teams;  // fewer rows at once, no fewer CTAs
   const bool ring = vec && ring_bytes(g, words) + (g.vpt > 1 ? sum_bytes(g, n.d) : 0) <= SMEM_BYTES;
   switch (g.vpt) {
     case 1: return ring ? bwd_one<IN, RES, 1, FEED_RING>(n, g) : bwd_one<IN, RES, 1, FEED_SCALAR>(n, g);
@@ -300,7 +310,7 @@ cudaError_t bwd_types(const NormResidual& n) {
 
 size_t norm_residual_bwd_ws_bytes(int64_t T, int64_t d, int num_sms) {
   if (T <= 0 || d <= 0) return 0;
-  return static_cast<size_t>(bwd_geometry(T, d, num_sms).ctas) * 3 * d * 4;
+  return static_cast<size_t>(T < num_sms ? T : num_sms) * 3 * d * 4;  // of each CTA
 }
 
 cudaError_t norm_residual_bwd_launch(const NormResidual& n) {

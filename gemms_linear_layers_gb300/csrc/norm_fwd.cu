@@ -14,7 +14,7 @@ namespace {
 using namespace nr;
 
 constexpr int FWD_THREADS = 512;  // of a CTA
-constexpr int FWD_PER_SM = 4;
+constexpr int FWD_PER_SM = 3;     // CTAs (registers hold three of 288 threads: a fourth ran as a second wave, 81 us for 73)
 constexpr int FWD_DEPTH = 2;      // rows in the ring
 
 template <typename IN, typename RES, int VPT, int FEED>
@@ -22,9 +22,9 @@ __global__ void __launch_bounds__(FWD_THREADS) norm_fwd_kernel(const Args a) {
   constexpr bool VEC = FEED != FEED_SCALAR;
   constexpr int D = FWD_DEPTH;
   extern __shared__ __align__(16) uint8_t ring_smem[];
-  __shared__ float2 slots[MAX_TEAMS][32];
+  __shared__ float slots[MAX_TEAMS][32];
   const int team_id = threadIdx.x / a.team, t = threadIdx.x - team_id * a.team;
-  float2* slot = slots[team_id];
+  float* slot = slots[team_id];
   const int d = a.d;
   const float inv_d = 1.f / static_cast<float>(d);
   const bool full = a.gate_kind == GATE_FULL, channel = a.gate_kind == GATE_CHANNEL;
@@ -59,10 +59,13 @@ __global__ void __launch_bounds__(FWD_THREADS) norm_fwd_kernel(const Args a) {
     if (channel) g[v] = load8<IN, VEC>(a.gate, 0, c, d);
   }
   int which = 0, stage = 0;
+  const bool token = a.gate_kind == GATE_TOKEN;
+  float gt_next = token && row0 < a.T ? to_f(static_cast<const IN*>(a.gate)[row0]) : 1.f;
   for (long long row = row0; row < a.T; row += step) {
     Pack<IN> b[VPT];
     Pack<RES> h[VPT];
-    const float gt = a.gate_kind == GATE_TOKEN ? to_f(static_cast<const IN*>(a.gate)[row]) : 1.f;
+    const float gt = gt_next;  // loaded a row ahead
+    if (token && row + step < a.T) gt_next = to_f(static_cast<const IN*>(a.gate)[row + step]);
     if (FEED == FEED_RING) {
       fetch(row + (D - 1) * step, stage + D - 1 < D ? stage + D - 1 : stage - 1);
       ring_wait<D - 1>();
@@ -84,36 +87,37 @@ __global__ void __launch_bounds__(FWD_THREADS) norm_fwd_kernel(const Args a) {
         if (full) g[v] = load8<IN, VEC>(a.gate, row, c, d);
       }
     }
-    float s = 0.f;
+    float2 s = both(0.f);
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x = to_f(b[v].v[j]);
-        s = fmaf(x, x, s);
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = two(b[v], j);
+        s = fma2(x, x, s);
       }
-    s = team_sum(make_float2(s, 0.f), slot, which, team_id, a.team, t).x;
+    const float rb = rsqrtf(team_sum(s.x + s.y, slot, which, team_id, a.team, t) * inv_d + a.eps);
     which ^= 1;
-    const float rb = rsqrtf(s * inv_d + a.eps);
-    float x[VPT][8];
-    s = 0.f;
+    const float2 k = both(rb * gt), sc = both(a.res_scale);
+    float2 x[VPT][4];
+    s = both(0.f);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float u = to_f(b[v].v[j]) * rb * to_f(wpost[v].v[j]) * (full || channel ? to_f(g[v].v[j]) : gt);
-        x[v][j] = fmaf(a.res_scale, to_f(h[v].v[j]), u);
-        s = fmaf(x[v][j], x[v][j], s);
+      for (int j = 0; j < 4; ++j) {
+        float2 u = mul2(mul2(two(b[v], j), k), two(wpost[v], j));
+        if (full || channel) u = mul2(u, two(g[v], j));
+        x[v][j] = fma2(sc, two(h[v], j), u);
+        s = fma2(x[v][j], x[v][j], s);
       }
       store8<RES, VEC>(a.H_out, row, (v * a.team + t) * 8, d, x[v]);
     }
-    s = team_sum(make_float2(s, 0.f), slot, which, team_id, a.team, t).x;
+    const float rh = rsqrtf(team_sum(s.x + s.y, slot, which, team_id, a.team, t) * inv_d + a.eps);
     which ^= 1;
-    const float rh = rsqrtf(s * inv_d + a.eps);
+    const float2 rh2 = both(rh);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[v][j] *= rh * to_f(wpre[v].v[j]);
+      for (int j = 0; j < 4; ++j) x[v][j] = mul2(x[v][j], mul2(rh2, two(wpre[v], j)));
       store8<IN, VEC>(a.N, row, (v * a.team + t) * 8, d, x[v]);
     }
     if (t == 0) {

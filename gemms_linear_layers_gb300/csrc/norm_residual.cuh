@@ -9,7 +9,7 @@
 // The kernels are bound by HBM, and what feeds it is bytes in flight: about
 // 50 KB an SM at its latency.  Each thread copies its own groups of the team's
 // next row into shared memory with cp.async while it works on the present one
-// (a thread reads only what it copied itself, so the ring needs no barrier).
+// (a warp reads only what it copied itself, so the ring needs no barrier).
 // Rows in registers alone left the loads waiting behind each row's two sums:
 // 16,384 x 2,304 forward ran at 2.7 TB/s that way.
 #pragma once
@@ -23,9 +23,8 @@ namespace tg {
 namespace nr {
 
 constexpr int MAX_TEAM = 512;
-constexpr int CTA_THREADS = 576;  // most threads of a CTA
 constexpr int MAX_TEAMS = 15;     // named barriers 1..15
-constexpr int SMEM_BYTES = 220 * 1024;  // dynamic, beside 4 KB of the teams' slots
+constexpr int SMEM_BYTES = 216 * 1024;  // dynamic, beside up to 7.5 KB of the teams' slots
 
 struct Args {
   const void *B, *H, *w_post, *w_pre, *gate, *dH_out, *dN;
@@ -70,6 +69,36 @@ __device__ __forceinline__ Pack<T> zeros() {
   return r;
 }
 
+// Two FP32 operations in one instruction (the kernels would otherwise be bound
+// by instruction issue before HBM).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return reinterpret_cast<float2&>(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return reinterpret_cast<float2&>(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return reinterpret_cast<float2&>(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+// elements 2i, 2i + 1
+template <typename T>
+__device__ __forceinline__ float2 two(const Pack<T>& p, int i) {
+  return make_float2(to_f(p.v[2 * i]), to_f(p.v[2 * i + 1]));
+}
+
 // c: first column; VEC: rows start at multiples of 16 bytes and d is a
 // multiple of 8 (checked on the host); otherwise element by element
 template <typename T, bool VEC>
@@ -89,16 +118,30 @@ __device__ __forceinline__ Pack<T> load8(const void* base, long long row, int c,
   return r;
 }
 template <typename T, bool VEC>
-__device__ __forceinline__ void store8(void* base, long long row, int c, int d, const float* f) {
+__device__ __forceinline__ void store8(void* base, long long row, int c, int d, const float2* f) {
   T* p = static_cast<T*>(base) + row * d + c;
   Pack<T> r;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) r.v[j] = from_f<T>(f[j]);
-  if (VEC) {
-    if (c < d) {
-#pragma unroll
-      for (int i = 0; i < Pack<T>::WORDS; ++i) reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<uint4*>(&r)[i];
-    }
+  for (int j = 0; j < 4; ++j) {
+    r.v[2 * j] = from_f<T>(f[j].x);
+    r.v[2 * j + 1] = from_f<T>(f[j].y);
+  }
+  if (VEC && sizeof(T) == 2) {
+    if (c < d) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(&r);
+  } else if (VEC) {
+    // lanes 2i and 2i + 1 exchange a word, so that a store fills whole sectors:
+    // words 0 and 1 of the even lane's group, then those of the odd lane's
+    const int odd = threadIdx.x & 1;
+    uint4* x = reinterpret_cast<uint4*>(&r);
+    const uint4 give = odd ? x[0] : x[1];
+    uint4 got;
+    got.x = __shfl_xor_sync(~0u, give.x, 1);
+    got.y = __shfl_xor_sync(~0u, give.y, 1);
+    got.z = __shfl_xor_sync(~0u, give.z, 1);
+    got.w = __shfl_xor_sync(~0u, give.w, 1);
+    T* even = p - 8 * odd + 4 * odd;
+    if (c - 8 * odd < d) *reinterpret_cast<uint4*>(even) = odd ? got : x[0];
+    if (c - 8 * odd + 8 < d) *reinterpret_cast<uint4*>(even + 8) = odd ? x[1] : got;
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -107,7 +150,14 @@ __device__ __forceinline__ void store8(void* base, long long row, int c, int d, 
 }
 
 // ------------------------------------------------------------ ring of rows
-// Word w of stage s of this thread sits at ((s * words + w) * threads + tid) * 16.
+// A row in the ring is `words` planes of 16 bytes a thread: word w of stage s
+// of thread `tid` sits at ((s * words + w) * threads + tid) * 16.  A group of
+// 16-bit values is one word.  A group of FP32 values is two; a lane copies
+// words `lane` and `lane + 32` of its warp's 64 instead of its own two, so that
+// a copy takes whole 32-byte sectors (a lane's own words are 32 bytes apart
+// from the next lane's: every sector would travel twice), and reads its own two
+// from the two planes: word k of the warp's 64 is word (k ^ bit 3 of k) % 32 of
+// plane k / 32, an order without bank conflicts.
 struct Ring {
   uint32_t base;  // shared address of this thread's word 0 of stage 0
   uint32_t word, stage;  // bytes from one word to the next, one stage to the next
@@ -119,33 +169,56 @@ __device__ __forceinline__ Ring ring_of(const void* smem, int words) {
   r.stage = r.word * words;
   return r;
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 template <typename T>
 __device__ __forceinline__ void ring_copy(const Ring& r, int stage, int& w, const void* base, long long row, int c, int d) {
-  const T* p = static_cast<const T*>(base) + row * d + c;
-#pragma unroll
-  for (int i = 0; i < Pack<T>::WORDS; ++i, ++w)
-    if (c < d)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(r.base + stage * r.stage + w * r.word),
-                   "l"(reinterpret_cast<const char*>(p) + 16 * i)
-                   : "memory");
+  const T* p = static_cast<const T*>(base) + row * d;
+  const uint32_t at = r.base + stage * r.stage + w * r.word;
+  if constexpr (sizeof(T) == 2) {
+    if (c < d) copy16(at, p + c);
+  } else {
+    const int lane = threadIdx.x & 31;
+    const int c0 = c - 8 * lane + 4 * lane;  // the warp's word `lane`
+    const uint32_t to = at - 16 * lane + 16 * (lane ^ ((lane >> 3) & 1));
+    if (c0 < d) copy16(to, p + c0);
+    if (c0 + 128 < d) copy16(to + r.word, p + c0 + 128);
+  }
+  w += Pack<T>::WORDS;
 }
 __device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// this thread's copies, and (FP32 planes) the other lanes', have landed
 template <int N>
 __device__ __forceinline__ void ring_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+  __syncwarp();
+}
+__device__ __forceinline__ uint4 read16(uint32_t at) {
+  uint4 x;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "r"(at)
+               : "memory");
+  return x;
 }
 template <typename T>
 __device__ __forceinline__ Pack<T> ring_read(const Ring& r, int stage, int& w, int c, int d) {
   Pack<T> v = zeros<T>();
-#pragma unroll
-  for (int i = 0; i < Pack<T>::WORDS; ++i, ++w)
-    if (c < d) {
-      uint4& x = reinterpret_cast<uint4*>(&v)[i];
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                   : "r"(r.base + stage * r.stage + w * r.word)
-                   : "memory");
+  const uint32_t at = r.base + stage * r.stage + w * r.word;
+  uint4* x = reinterpret_cast<uint4*>(&v);
+  if (c < d) {
+    if constexpr (sizeof(T) == 2) {
+      x[0] = read16(at);
+    } else {
+      // words 2 lane and 2 lane + 1 of the warp's 64
+      const int lane = threadIdx.x & 31, k = 2 * lane & 31, flip = (k >> 3) & 1;
+      const uint32_t plane = at - 16 * lane + (lane >> 4) * r.word;
+      x[0] = read16(plane + 16 * (k ^ flip));
+      x[1] = read16(plane + 16 * ((k + 1) ^ flip));
     }
+  }
+  w += Pack<T>::WORDS;
   return v;
 }
 
@@ -154,26 +227,41 @@ __device__ __forceinline__ void team_sync(int team_id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(team_id + 1), "r"(threads) : "memory");
 }
 
-// Sums of (x, y) over the team; every thread gets them, added in the same
-// order.  `slot`: shared space for 2 x 16 pairs of this team; `which` alternates
+// Sums over the team; every thread gets them, added in the same order.
+// `slot`: shared space for 2 x 16 warps of this team; `which` alternates
 // between its halves, so one barrier a call is enough.
-__device__ __forceinline__ float2 team_sum(float2 v, float2* slot, int which, int team_id, int team, int t) {
+__device__ __forceinline__ float team_sum(float v, float* slot, int which, int team_id, int team, int t) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  const int warps = team >> 5;
+  if (warps == 1) return v;
+  float* s = slot + which * 16;
+  if ((t & 31) == 0) s[t >> 5] = v;
+  team_sync(team_id, team);
+  float r = s[0];
+  for (int i = 1; i < warps; ++i) r += s[i];
+  return r;
+}
+__device__ __forceinline__ float3 team_sum3(float3 v, float4* slot, int which, int team_id, int team, int t) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     v.x += __shfl_xor_sync(~0u, v.x, o);
     v.y += __shfl_xor_sync(~0u, v.y, o);
+    v.z += __shfl_xor_sync(~0u, v.z, o);
   }
   const int warps = team >> 5;
   if (warps == 1) return v;
-  float2* s = slot + which * 16;
-  if ((t & 31) == 0) s[t >> 5] = v;
+  float4* s = slot + which * 16;
+  if ((t & 31) == 0) s[t >> 5] = make_float4(v.x, v.y, v.z, 0.f);
   team_sync(team_id, team);
-  float2 r = s[0];
+  float4 r = s[0];
   for (int i = 1; i < warps; ++i) {
-    r.x += s[i].x;
-    r.y += s[i].y;
+    const float4 x = s[i];
+    r.x += x.x;
+    r.y += x.y;
+    r.z += x.z;
   }
-  return r;
+  return make_float3(r.x, r.y, r.z);
 }
 
 // ----------------------------------------------------------------- host side
