@@ -7,8 +7,8 @@
 // FP32 arithmetic, every output rounded once; the stored H' is what the
 // derivative is taken at.  Bound by HBM: 4 values (5 with an element-wise
 // gate) read and 2 (3) written an element, in one pass: the column sums build
-// up in registers (rows of up to 4,096 columns; in shared memory beyond, where
-// 16 or 32 columns a thread would spill); the teams of a CTA are added in
+// up in registers (while a thread has 8 columns; in shared memory beyond, where
+// 16 or 32 would spill); the teams of a CTA are added in
 // shared memory, the CTAs by a second launch, all in a fixed order.  The
 // second mean is taken from sums that do not wait for the first (q and e
 // below), so a row costs one exchange between its threads, not two.
@@ -32,13 +32,13 @@ __device__ __forceinline__ void put_kind(void* p, long long i, float v, int kind
 // EL: the gate differs from element to element (full or channel); otherwise
 // it is one value a row, or 1
 template <typename IN, typename RES, int VPT, int FEED, bool EL>
-__global__ void __launch_bounds__(VPT > 1 ? MAX_TEAM : bwd_threads(EL), 1) norm_bwd_kernel(const Args a) {
+__global__ void __launch_bounds__(VPT > 1 ? WIDE_TEAM : bwd_threads(EL), 1) norm_bwd_kernel(const Args a) {
   constexpr bool VEC = FEED != FEED_SCALAR;
   constexpr int D = BWD_DEPTH;
   extern __shared__ __align__(16) uint8_t ring_smem[];  // the ring, then the column sums [3][d]
-  __shared__ float4 slots[MAX_TEAMS][32];
+  __shared__ float4 slots[2][32];
   const int team_id = threadIdx.x / a.team, t = threadIdx.x - team_id * a.team;
-  float4* slot = slots[team_id];
+  float4* slot = slots[0] + team_id * (a.team >> 5);
   const int d = a.d;
   const float inv_d = 1.f / static_cast<float>(d);
   const bool full = EL && a.gate_kind == GATE_FULL, channel = EL && a.gate_kind == GATE_CHANNEL;
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(256) norm_cols_kernel(const float* part, int c
 }
 
 Geo bwd_geometry(int64_t T, int64_t d, int sms, bool el) {
-  Geo g = geometry(T, d, sms, bwd_threads(el), 1);
+  Geo g = geometry(T, d, sms, bwd_threads(el), bwd_threads(el), 1);
   if (g.vpt > 1) {  // one row at a time
     g.teams = 1;
     g.ctas = static_cast<int>(T < sms ? T : sms);

@@ -13,18 +13,19 @@ namespace tg {
 namespace {
 using namespace nr;
 
-constexpr int FWD_THREADS = 512;  // of a CTA
-constexpr int FWD_PER_SM = 3;     // CTAs (registers hold three of 288 threads: a fourth ran as a second wave, 81 us for 73)
+constexpr int FWD_TEAM = 1024;    // most threads of a row
+constexpr int FWD_THREADS = 512;  // of a CTA of several rows
+constexpr int FWD_RESIDENT = 1024;  // threads an SM's registers hold (64 each)
 constexpr int FWD_DEPTH = 2;      // rows in the ring
 
 template <typename IN, typename RES, int VPT, int FEED>
-__global__ void __launch_bounds__(FWD_THREADS) norm_fwd_kernel(const Args a) {
+__global__ void __launch_bounds__(VPT > 1 ? WIDE_TEAM : FWD_TEAM) norm_fwd_kernel(const Args a) {
   constexpr bool VEC = FEED != FEED_SCALAR;
   constexpr int D = FWD_DEPTH;
   extern __shared__ __align__(16) uint8_t ring_smem[];
-  __shared__ float slots[MAX_TEAMS][32];
+  __shared__ float slots[2][32];
   const int team_id = threadIdx.x / a.team, t = threadIdx.x - team_id * a.team;
-  float* slot = slots[team_id];
+  float* slot = slots[0] + team_id * (a.team >> 5);
   const int d = a.d;
   const float inv_d = 1.f / static_cast<float>(d);
   const bool full = a.gate_kind == GATE_FULL, channel = a.gate_kind == GATE_CHANNEL;
@@ -142,16 +143,13 @@ cudaError_t fwd_one(const NormResidual& n, const Geo& g) {
 }
 template <typename IN, typename RES>
 cudaError_t fwd_types(const NormResidual& n) {
-  const Geo g = geometry(n.T, n.d, n.num_sms, FWD_THREADS, FWD_PER_SM);
+  const Geo g = geometry(n.T, n.d, n.num_sms, FWD_TEAM, FWD_THREADS, FWD_RESIDENT);
   // a gate of one value a row needs no alignment
   const bool wide_gate = n.gate_kind == GATE_FULL || n.gate_kind == GATE_CHANNEL;
   const bool vec = vec_ok({n.B, n.H, n.w_post, n.w_pre, n.H_out, n.N, wide_gate ? n.gate : nullptr}, n.d);
-  // the ring: up to 8,192 columns (64 KB of FP32 stream and 32 KB of 16-bit values a row at most)
-  switch (g.vpt) {
-    case 1: return vec ? fwd_one<IN, RES, 1, FEED_RING>(n, g) : fwd_one<IN, RES, 1, FEED_SCALAR>(n, g);
-    case 2: return vec ? fwd_one<IN, RES, 2, FEED_RING>(n, g) : fwd_one<IN, RES, 2, FEED_SCALAR>(n, g);
-    default: return vec ? fwd_one<IN, RES, 4, FEED_VEC>(n, g) : fwd_one<IN, RES, 4, FEED_SCALAR>(n, g);
-  }
+  // the ring holds up to 8,192 columns (two rows of FP32 stream and two 16-bit operands: 128 KB; all FP32: 192 KB)
+  if (g.vpt == 1) return vec ? fwd_one<IN, RES, 1, FEED_RING>(n, g) : fwd_one<IN, RES, 1, FEED_SCALAR>(n, g);
+  return vec ? fwd_one<IN, RES, 4, FEED_VEC>(n, g) : fwd_one<IN, RES, 4, FEED_SCALAR>(n, g);
 }
 
 }  // namespace

@@ -2,7 +2,7 @@
 // around a block share: eight-element loads and stores, the ring of rows in
 // flight, sums over the threads of a row, the launch geometry.
 //
-// A team of 32..512 threads owns a row, thread t the 8-element groups t,
+// A team of 32..1,024 threads owns a row, thread t the 8-element groups t,
 // t + team, ..; a CTA holds several teams when rows are short.  Columns stay
 // with their thread from row to row.
 //
@@ -22,9 +22,9 @@
 namespace tg {
 namespace nr {
 
-constexpr int MAX_TEAM = 512;
+constexpr int WIDE_TEAM = 512;    // threads of a team with more than one group a thread
 constexpr int MAX_TEAMS = 15;     // named barriers 1..15
-constexpr int SMEM_BYTES = 216 * 1024;  // dynamic, beside up to 7.5 KB of the teams' slots
+constexpr int SMEM_BYTES = 224 * 1024;  // dynamic, beside 1 KB of the warps' slots
 
 struct Args {
   const void *B, *H, *w_post, *w_pre, *gate, *dH_out, *dN;
@@ -228,14 +228,14 @@ __device__ __forceinline__ void team_sync(int team_id, int threads) {
 }
 
 // Sums over the team; every thread gets them, added in the same order.
-// `slot`: shared space for 2 x 16 warps of this team; `which` alternates
-// between its halves, so one barrier a call is enough.
+// `slot`: shared space of this team's warps in each of two arrays of 32;
+// `which` alternates between them, so one barrier a call is enough.
 __device__ __forceinline__ float team_sum(float v, float* slot, int which, int team_id, int team, int t) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   const int warps = team >> 5;
   if (warps == 1) return v;
-  float* s = slot + which * 16;
+  float* s = slot + which * 32;
   if ((t & 31) == 0) s[t >> 5] = v;
   team_sync(team_id, team);
   float r = s[0];
@@ -251,7 +251,7 @@ __device__ __forceinline__ float3 team_sum3(float3 v, float4* slot, int which, i
   }
   const int warps = team >> 5;
   if (warps == 1) return v;
-  float4* s = slot + which * 16;
+  float4* s = slot + which * 32;
   if ((t & 31) == 0) s[t >> 5] = make_float4(v.x, v.y, v.z, 0.f);
   team_sync(team_id, team);
   float4 r = s[0];
@@ -268,19 +268,21 @@ __device__ __forceinline__ float3 team_sum3(float3 v, float4* slot, int which, i
 struct Geo {
   int vpt, team, teams, ctas;
 };
-// Threads of a team: one per 8-element group up to 512, then 2 or 4 groups a
-// thread; teams to fill a CTA.
-inline Geo geometry(int64_t T, int64_t d, int sms, int threads, int ctas_per_sm) {
+// Threads of a team: one per 8-element group up to `most`, then 2 or 4 groups
+// a thread; teams to fill a CTA of `threads`; CTAs that an SM holds at once
+// (`resident` threads: a CTA more would run as a second wave).
+inline Geo geometry(int64_t T, int64_t d, int sms, int most_team, int threads, int resident) {
   Geo g;
   const int groups = static_cast<int>((d + 7) / 8);
-  g.vpt = groups <= MAX_TEAM ? 1 : groups <= 2 * MAX_TEAM ? 2 : 4;
+  g.vpt = groups <= most_team ? 1 : groups <= 2 * WIDE_TEAM ? 2 : 4;
   g.team = ((groups + g.vpt - 1) / g.vpt + 31) / 32 * 32;
   g.teams = threads / g.team;
   if (g.teams < 1) g.teams = 1;
   if (g.teams > MAX_TEAMS) g.teams = MAX_TEAMS;
   const int64_t rows = (T + sms - 1) / sms;  // rows of an SM
   if (g.teams > rows) g.teams = static_cast<int>(rows);
-  const int64_t most = (T + g.teams - 1) / g.teams, want = static_cast<int64_t>(sms) * ctas_per_sm;
+  const int per_sm = resident / (g.team * g.teams) > 1 ? resident / (g.team * g.teams) : 1;
+  const int64_t most = (T + g.teams - 1) / g.teams, want = static_cast<int64_t>(sms) * per_sm;
   g.ctas = static_cast<int>(most < want ? most : want);
   return g;
 }
