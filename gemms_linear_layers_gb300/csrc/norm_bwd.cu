@@ -18,9 +18,13 @@ namespace tg {
 namespace {
 using namespace nr;
 
-// Threads of a CTA; one CTA an SM (few partial sums).  27 warps at 72 registers;
-// an element-wise gate needs more registers (18 warps at 112).
-constexpr int bwd_threads(bool el) { return el ? 576 : 864; }
+// Groups a thread: 1 while an SM's registers hold a row's threads (16,384 x 576
+// takes 42 us with 1, 60 with 3: fewer warps); `many` beyond, 3, or 2 with an
+// element-wise gate (column sums in registers: 128 of them for 512 threads);
+// then 4 (sums in shared memory).  One CTA an SM (few partial sums): its threads.
+constexpr int bwd_many(bool el) { return el ? 2 : 3; }
+constexpr int BWD_WIDEST = 4;
+constexpr int bwd_threads(bool el, int vpt) { return vpt > 1 ? 512 : el ? 576 : 864; }
 constexpr int BWD_DEPTH = 2;      // rows in the ring
 
 __device__ __forceinline__ void put_kind(void* p, long long i, float v, int kind) {
@@ -32,7 +36,7 @@ __device__ __forceinline__ void put_kind(void* p, long long i, float v, int kind
 // EL: the gate differs from element to element (full or channel); otherwise
 // it is one value a row, or 1
 template <typename IN, typename RES, int VPT, int FEED, bool EL>
-__global__ void __launch_bounds__(VPT > 1 ? WIDE_TEAM : bwd_threads(EL), 1) norm_bwd_kernel(const Args a) {
+__global__ void __launch_bounds__(bwd_threads(EL, VPT), 1) norm_bwd_kernel(const Args a) {
   constexpr bool VEC = FEED != FEED_SCALAR;
   constexpr int D = BWD_DEPTH;
   extern __shared__ __align__(16) uint8_t ring_smem[];  // the ring, then the column sums [3][d]
@@ -52,12 +56,12 @@ __global__ void __launch_bounds__(VPT > 1 ? WIDE_TEAM : bwd_threads(EL), 1) norm
       int w = 0;
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
-        const int c = (v * a.team + t) * 8;
-        ring_copy<RES>(ring, stage, w, a.H, row, c, d);
-        ring_copy<IN>(ring, stage, w, a.B, row, c, d);
-        if (full) ring_copy<IN>(ring, stage, w, a.gate, row, c, d);
-        ring_copy<IN>(ring, stage, w, a.dN, row, c, d);
-        ring_copy<RES>(ring, stage, w, a.dH_out, row, c, d);
+        const Cols<VEC> c(v, t, a.team, d);
+        ring_copy<RES>(ring, stage, w, a.H, row, c.first, d);
+        ring_copy<IN>(ring, stage, w, a.B, row, c.first, d);
+        if (full) ring_copy<IN>(ring, stage, w, a.gate, row, c.first, d);
+        ring_copy<IN>(ring, stage, w, a.dN, row, c.first, d);
+        ring_copy<RES>(ring, stage, w, a.dH_out, row, c.first, d);
       }
     }
     ring_commit();
@@ -66,8 +70,8 @@ __global__ void __launch_bounds__(VPT > 1 ? WIDE_TEAM : bwd_threads(EL), 1) norm
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) fetch(row0 + i * step, i);
   }
-  // VPT > 1 (one team a CTA): column sum k of the thread's group v, half i at (((k * VPT + v) * 2 + i) * team + t)
-  constexpr bool IN_SMEM = VPT > 1;
+  // 4 groups a thread (one team a CTA): column sum k of the thread's group v, half i at (((k * VPT + v) * 2 + i) * team + t)
+  constexpr bool IN_SMEM = VPT == BWD_WIDEST;
   const int ring_bytes = FEED == FEED_RING ? D * static_cast<int>(ring.stage) : 0;
   float4* accs = reinterpret_cast<float4*>(ring_smem + ring_bytes) + t;
   auto at = [&](int k, int v, int i) -> float4& { return accs[((k * VPT + v) * 2 + i) * a.team]; };
@@ -87,7 +91,8 @@ __global__ void __launch_bounds__(VPT > 1 ? WIDE_TEAM : bwd_threads(EL), 1) norm
 #pragma unroll
       for (int v = 0; v < VPT; ++v) at(k, v, 0) = at(k, v, 1) = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  float2 acc_post[4] = {}, acc_pre[4] = {}, acc_gate[4] = {};
+  constexpr int KEPT = IN_SMEM ? 1 : VPT;
+  float2 acc_post[KEPT][4] = {}, acc_pre[KEPT][4] = {}, acc_gate[KEPT][4] = {};
   int which = 0, stage = 0;
   // a row's scalars are loaded a row ahead too
   const bool token = !EL && a.gate_kind == GATE_TOKEN;
@@ -106,20 +111,26 @@ __global__ void __launch_bounds__(VPT > 1 ? WIDE_TEAM : bwd_threads(EL), 1) norm
     if (FEED == FEED_RING) {
       fetch(row + (D - 1) * step, stage + D - 1 < D ? stage + D - 1 : stage - 1);
       ring_wait<D - 1>();
+    } else if (row + step < a.T) {
+      prefetch_row<RES>(a.H, row + step, d, t, a.team);
+      prefetch_row<IN>(a.B, row + step, d, t, a.team);
+      prefetch_row<IN>(a.dN, row + step, d, t, a.team);
+      prefetch_row<RES>(a.dH_out, row + step, d, t, a.team);
+      if (full) prefetch_row<IN>(a.gate, row + step, d, t, a.team);
     }
     // Group v of the thread: everything for the sums; for the results H', B
     // and the gate are taken again (all of it kept between the two would spill).
     Pack<IN> b, dn, g, wpre, wpost;
     Pack<RES> h, dho;
     auto take = [&](int v, bool sums) {
-      const int c = (v * a.team + t) * 8;
+      const Cols<VEC> c(v, t, a.team, d);
       if (FEED == FEED_RING) {
         int w = v * (2 * Pack<RES>::WORDS + (full ? 3 : 2) * Pack<IN>::WORDS);
-        h = ring_read<RES>(ring, stage, w, c, d);
-        b = ring_read<IN>(ring, stage, w, c, d);
-        if (full) g = ring_read<IN>(ring, stage, w, c, d);
-        if (sums) dn = ring_read<IN>(ring, stage, w, c, d);
-        if (sums) dho = ring_read<RES>(ring, stage, w, c, d);
+        h = ring_read<RES>(ring, stage, w, c.first, d);
+        b = ring_read<IN>(ring, stage, w, c.first, d);
+        if (full) g = ring_read<IN>(ring, stage, w, c.first, d);
+        if (sums) dn = ring_read<IN>(ring, stage, w, c.first, d);
+        if (sums) dho = ring_read<RES>(ring, stage, w, c.first, d);
       } else {
         h = load8<RES, VEC>(a.H, row, c, d);
         b = load8<IN, VEC>(a.B, row, c, d);
@@ -145,7 +156,7 @@ __global__ void __launch_bounds__(VPT > 1 ? WIDE_TEAM : bwd_threads(EL), 1) norm
         const float2 x = two(h, j), n = two(dn, j), g1 = mul2(n, two(wpre, j));
         s1 = fma2(g1, x, s1);
         p[j] = mul2(n, x);  // dw_pre's term, without rstd_h
-        if (!IN_SMEM) acc_pre[j] = fma2(p[j], rh2, acc_pre[j]);
+        if constexpr (!IN_SMEM) acc_pre[v][j] = fma2(p[j], rh2, acc_pre[v][j]);
         float2 q = mul2(two(b, j), two(wpost, j));
         if (EL) q = mul2(q, two(g, j));
         e[v][j] = fma2(rh2, g1, two(dho, j));
@@ -164,7 +175,7 @@ __global__ void __launch_bounds__(VPT > 1 ? WIDE_TEAM : bwd_threads(EL), 1) norm
     const float2 mk1 = both(-k1), c1 = both(rb * gt), c2 = both(-rb * (rb * (gt * s2 * inv_d))), sc = both(a.res_scale);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      const int c = (v * a.team + t) * 8;
+      const Cols<VEC> c(v, t, a.team, d);
       float2 dh[4], o[4];
       take(v, false);
 #pragma unroll
@@ -179,11 +190,13 @@ __global__ void __launch_bounds__(VPT > 1 ? WIDE_TEAM : bwd_threads(EL), 1) norm
         const float2 x = two(b, j), w = two(wpost, j);
         const float2 du = EL ? mul2(dh[j], two(g, j)) : dh[j];  // without a gate of one value a row: c1 holds it
         q[j] = mul2(du, x);
-        if (!IN_SMEM) acc_post[j] = fma2(q[j], c1, acc_post[j]);
+        if constexpr (!IN_SMEM) acc_post[v][j] = fma2(q[j], c1, acc_post[v][j]);
         o[j] = fma2(mul2(du, w), c1, mul2(c2, x));
         if (EL) {
           dh[j] = mul2(mul2(dh[j], x), mul2(w, c1));  // the gate's gradient, element by element
-          if (!IN_SMEM && channel) acc_gate[j] = add2(acc_gate[j], dh[j]);
+          if constexpr (!IN_SMEM) {
+            if (channel) acc_gate[v][j] = add2(acc_gate[v][j], dh[j]);
+          }
         }
       }
       store8<IN, VEC>(a.dB, row, c, d, o);
@@ -202,15 +215,14 @@ __global__ void __launch_bounds__(VPT > 1 ? WIDE_TEAM : bwd_threads(EL), 1) norm
     for (int k = 0; k < sums; ++k)
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
-        const int c = (v * a.team + t) * 8;
+        const Cols<VEC> c(v, t, a.team, d);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float4 f = at(k, v, i);
-          float* p = out + k * d + c + 4 * i;
-          if (c + 4 * i < d) p[0] = f.x;
-          if (c + 4 * i + 1 < d) p[1] = f.y;
-          if (c + 4 * i + 2 < d) p[2] = f.z;
-          if (c + 4 * i + 3 < d) p[3] = f.w;
+          if (c[4 * i] < d) out[k * d + c[4 * i]] = f.x;
+          if (c[4 * i + 1] < d) out[k * d + c[4 * i + 1]] = f.y;
+          if (c[4 * i + 2] < d) out[k * d + c[4 * i + 2]] = f.z;
+          if (c[4 * i + 3] < d) out[k * d + c[4 * i + 3]] = f.w;
         }
       }
     return;
@@ -221,13 +233,17 @@ __global__ void __launch_bounds__(VPT > 1 ? WIDE_TEAM : bwd_threads(EL), 1) norm
     __syncthreads();
     if (team_id == k) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (t * 8 + j < d) {
-          float* p = col + t * 8 + j;
-          p[0] = (k ? p[0] : 0.f) + (j & 1 ? acc_post[j / 2].y : acc_post[j / 2].x);
-          p[d] = (k ? p[d] : 0.f) + (j & 1 ? acc_pre[j / 2].y : acc_pre[j / 2].x);
-          if (EL && channel) p[2 * d] = (k ? p[2 * d] : 0.f) + (j & 1 ? acc_gate[j / 2].y : acc_gate[j / 2].x);
-        }
+      for (int v = 0; v < KEPT; ++v) {
+        const Cols<VEC> c(v, t, a.team, d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c[j] < d) {
+            float* p = col + c[j];
+            p[0] = (k ? p[0] : 0.f) + (j & 1 ? acc_post[v][j / 2].y : acc_post[v][j / 2].x);
+            p[d] = (k ? p[d] : 0.f) + (j & 1 ? acc_pre[v][j / 2].y : acc_pre[v][j / 2].x);
+            if (EL && channel) p[2 * d] = (k ? p[2 * d] : 0.f) + (j & 1 ? acc_gate[v][j / 2].y : acc_gate[v][j / 2].x);
+          }
+      }
     }
   }
   __syncthreads();
@@ -258,25 +274,27 @@ __global__ void __launch_bounds__(256) norm_cols_kernel(const float* part, int c
 }
 
 Geo bwd_geometry(int64_t T, int64_t d, int sms, bool el) {
-  Geo g = geometry(T, d, sms, bwd_threads(el), bwd_threads(el), 1);
-  if (g.vpt > 1) {  // one row at a time
+  int vpt = 1;
+  for (const int v : {bwd_many(el), BWD_WIDEST})
+    if (team_of(d, vpt) > bwd_threads(el, vpt)) vpt = v;
+  Geo g = geometry(T, d, sms, vpt, bwd_threads(el, vpt), 1);
+  if (vpt == BWD_WIDEST) {  // one row at a time
     g.teams = 1;
     g.ctas = static_cast<int>(T < sms ? T : sms);
   }
   return g;
 }
-// Bytes of the ring and of the column sums beside it (VPT > 1) or in its place.
+// Bytes of the ring, and of the column sums beside it (4 groups a thread) or in its place.
 int ring_bytes(const Geo& g, int words) { return BWD_DEPTH * words * g.team * g.teams * 16; }
-int sum_bytes(const Geo& g, int64_t d) { return static_cast<int>(g.vpt > 1 ? 3 * g.vpt * g.team * 32 : 3 * d * 4); }
+int sum_bytes(const Geo& g, int64_t d) { return static_cast<int>(g.vpt == BWD_WIDEST ? 3 * g.vpt * g.team * 32 : 3 * d * 4); }
 
-template <typename IN, typename RES, int VPT, int FEED>
+template <typename IN, typename RES, int VPT, int FEED, bool EL>
 cudaError_t bwd_one(const NormResidual& n, const Geo& g) {
   const Args a = to_args(n, g);
-  const bool el = n.gate_kind == GATE_FULL || n.gate_kind == GATE_CHANNEL;
-  auto kern = el ? norm_bwd_kernel<IN, RES, VPT, FEED, true> : norm_bwd_kernel<IN, RES, VPT, FEED, false>;
+  auto kern = norm_bwd_kernel<IN, RES, VPT, FEED, EL>;
   const int words = VPT * (2 * Pack<RES>::WORDS + (n.gate_kind == GATE_FULL ? 3 : 2) * Pack<IN>::WORDS);
   const int ring = FEED == FEED_RING ? ring_bytes(g, words) : 0, sums_at = sum_bytes(g, n.d);
-  const int smem = VPT > 1 ? ring + sums_at : ring > sums_at ? ring : sums_at;
+  const int smem = VPT == BWD_WIDEST ? ring + sums_at : ring > sums_at ? ring : sums_at;
   cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   e = launch_k(kern, dim3(g.ctas), dim3(g.team * g.teams), smem, n.stream, a);
@@ -286,24 +304,25 @@ cudaError_t bwd_one(const NormResidual& n, const Geo& g) {
                   static_cast<const float*>(n.ws), g.ctas, static_cast<int>(n.d), sums, n.dw_post, n.dw_pre, n.dgate,
                   n.out_kind);
 }
-template <typename IN, typename RES>
-cudaError_t bwd_types(const NormResidual& n) {
-  const bool full = n.gate_kind == GATE_FULL, wide_gate = full || n.gate_kind == GATE_CHANNEL;
-  Geo g = bwd_geometry(n.T, n.d, n.num_sms, wide_gate);
-  const bool vec = vec_ok({n.B, n.H, n.w_post, n.w_pre, n.dH_out, n.dN, n.dB, n.dH, wide_gate ? n.gate : nullptr,
+template <typename IN, typename RES, bool EL>
+cudaError_t bwd_gate(const NormResidual& n) {
+  const bool full = n.gate_kind == GATE_FULL;
+  Geo g = bwd_geometry(n.T, n.d, n.num_sms, EL);
+  const bool vec = vec_ok({n.B, n.H, n.w_post, n.w_pre, n.dH_out, n.dN, n.dB, n.dH, EL ? n.gate : nullptr,
                            full ? n.dgate : nullptr},
                           n.d);
   const int words = g.vpt * (2 * Pack<RES>::WORDS + (full ? 3 : 2) * Pack<IN>::WORDS);
   while (g.teams > 1 && ring_bytes(g, words) > SMEM_BYTES) --g.teams;  // fewer rows at once, no fewer CTAs
-  const bool ring = vec && ring_bytes(g, words) + (g.vpt > 1 ? sum_bytes(g, n.d) : 0) <= SMEM_BYTES;
-  switch (g.vpt) {
-    case 1: return ring ? bwd_one<IN, RES, 1, FEED_RING>(n, g) : bwd_one<IN, RES, 1, FEED_SCALAR>(n, g);
-    case 2:
-      return ring  ? bwd_one<IN, RES, 2, FEED_RING>(n, g)
-             : vec ? bwd_one<IN, RES, 2, FEED_VEC>(n, g)
-                   : bwd_one<IN, RES, 2, FEED_SCALAR>(n, g);
-    default: return vec ? bwd_one<IN, RES, 4, FEED_VEC>(n, g) : bwd_one<IN, RES, 4, FEED_SCALAR>(n, g);
-  }
+  const bool ring = vec && ring_bytes(g, words) + (g.vpt == BWD_WIDEST ? sum_bytes(g, n.d) : 0) <= SMEM_BYTES;
+  constexpr int MANY = bwd_many(EL);
+  if (g.vpt == 1) return ring ? bwd_one<IN, RES, 1, FEED_RING, EL>(n, g) : bwd_one<IN, RES, 1, FEED_SCALAR, EL>(n, g);
+  if (g.vpt == MANY)
+    return ring ? bwd_one<IN, RES, MANY, FEED_RING, EL>(n, g) : bwd_one<IN, RES, MANY, FEED_SCALAR, EL>(n, g);
+  return vec ? bwd_one<IN, RES, BWD_WIDEST, FEED_VEC, EL>(n, g) : bwd_one<IN, RES, BWD_WIDEST, FEED_SCALAR, EL>(n, g);
+}
+template <typename IN, typename RES>
+cudaError_t bwd_types(const NormResidual& n) {
+  return n.gate_kind == GATE_FULL || n.gate_kind == GATE_CHANNEL ? bwd_gate<IN, RES, true>(n) : bwd_gate<IN, RES, false>(n);
 }
 
 }  // namespace

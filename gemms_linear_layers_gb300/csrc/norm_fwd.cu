@@ -13,13 +13,15 @@ namespace tg {
 namespace {
 using namespace nr;
 
-constexpr int FWD_TEAM = 1024;    // most threads of a row
-constexpr int FWD_THREADS = 512;  // of a CTA of several rows
-constexpr int FWD_RESIDENT = 1024;  // threads an SM's registers hold (64 each)
-constexpr int FWD_DEPTH = 2;      // rows in the ring
+// Groups a thread: 1 (up to 8,192 columns) or 3.  Threads of a CTA, and of an
+// SM (64 or 80 registers each).
+constexpr int FWD_MANY = 3;
+constexpr int fwd_threads(int vpt) { return vpt == 1 ? 1024 : 768; }
+constexpr int FWD_CTA = 384;  // a CTA of several rows
+constexpr int FWD_DEPTH = 2;  // rows in the ring
 
 template <typename IN, typename RES, int VPT, int FEED>
-__global__ void __launch_bounds__(VPT > 1 ? WIDE_TEAM : FWD_TEAM) norm_fwd_kernel(const Args a) {
+__global__ void __launch_bounds__(fwd_threads(VPT)) norm_fwd_kernel(const Args a) {
   constexpr bool VEC = FEED != FEED_SCALAR;
   constexpr int D = FWD_DEPTH;
   extern __shared__ __align__(16) uint8_t ring_smem[];
@@ -39,10 +41,10 @@ __global__ void __launch_bounds__(VPT > 1 ? WIDE_TEAM : FWD_TEAM) norm_fwd_kerne
       int w = 0;
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
-        const int c = (v * a.team + t) * 8;
-        ring_copy<IN>(ring, stage, w, a.B, row, c, d);
-        ring_copy<RES>(ring, stage, w, a.H, row, c, d);
-        if (full) ring_copy<IN>(ring, stage, w, a.gate, row, c, d);
+        const Cols<VEC> c(v, t, a.team, d);
+        ring_copy<IN>(ring, stage, w, a.B, row, c.first, d);
+        ring_copy<RES>(ring, stage, w, a.H, row, c.first, d);
+        if (full) ring_copy<IN>(ring, stage, w, a.gate, row, c.first, d);
       }
     }
     ring_commit();
@@ -51,51 +53,34 @@ __global__ void __launch_bounds__(VPT > 1 ? WIDE_TEAM : FWD_TEAM) norm_fwd_kerne
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) fetch(row0 + i * step, i);
   }
-  Pack<IN> wpost[VPT], wpre[VPT], g[VPT];
-#pragma unroll
-  for (int v = 0; v < VPT; ++v) {
-    const int c = (v * a.team + t) * 8;
-    wpost[v] = load8<IN, VEC>(a.w_post, 0, c, d);
-    wpre[v] = load8<IN, VEC>(a.w_pre, 0, c, d);
-    if (channel) g[v] = load8<IN, VEC>(a.gate, 0, c, d);
-  }
   int which = 0, stage = 0;
   const bool token = a.gate_kind == GATE_TOKEN;
   float gt_next = token && row0 < a.T ? to_f(static_cast<const IN*>(a.gate)[row0]) : 1.f;
   for (long long row = row0; row < a.T; row += step) {
-    Pack<IN> b[VPT];
-    Pack<RES> h[VPT];
     const float gt = gt_next;  // loaded a row ahead
     if (token && row + step < a.T) gt_next = to_f(static_cast<const IN*>(a.gate)[row + step]);
     if (FEED == FEED_RING) {
       fetch(row + (D - 1) * step, stage + D - 1 < D ? stage + D - 1 : stage - 1);
       ring_wait<D - 1>();
-      int w = 0;
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int c = (v * a.team + t) * 8;
-        b[v] = ring_read<IN>(ring, stage, w, c, d);
-        h[v] = ring_read<RES>(ring, stage, w, c, d);
-        if (full) g[v] = ring_read<IN>(ring, stage, w, c, d);
-      }
-      stage = stage + 1 < D ? stage + 1 : 0;
-    } else {
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int c = (v * a.team + t) * 8;
-        b[v] = load8<IN, VEC>(a.B, row, c, d);
-        h[v] = load8<RES, VEC>(a.H, row, c, d);
-        if (full) g[v] = load8<IN, VEC>(a.gate, row, c, d);
-      }
+    } else if (row + step < a.T) {
+      prefetch_row<IN>(a.B, row + step, d, t, a.team);
+      prefetch_row<RES>(a.H, row + step, d, t, a.team);
+      if (full) prefetch_row<IN>(a.gate, row + step, d, t, a.team);
     }
+    // word w of the ring's group v
+    const int words = Pack<RES>::WORDS + (full ? 2 : 1) * Pack<IN>::WORDS;
     float2 s = both(0.f);
 #pragma unroll
-    for (int v = 0; v < VPT; ++v)
+    for (int v = 0; v < VPT; ++v) {
+      const Cols<VEC> c(v, t, a.team, d);
+      int w = v * words;
+      const Pack<IN> b = FEED == FEED_RING ? ring_read<IN>(ring, stage, w, c.first, d) : load8<IN, VEC>(a.B, row, c, d);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 x = two(b[v], j);
+        const float2 x = two(b, j);
         s = fma2(x, x, s);
       }
+    }
     const float rb = rsqrtf(team_sum(s.x + s.y, slot, which, team_id, a.team, t) * inv_d + a.eps);
     which ^= 1;
     const float2 k = both(rb * gt), sc = both(a.res_scale);
@@ -103,24 +88,42 @@ __global__ void __launch_bounds__(VPT > 1 ? WIDE_TEAM : FWD_TEAM) norm_fwd_kerne
     s = both(0.f);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
+      const Cols<VEC> c(v, t, a.team, d);
+      int w = v * words;
+      Pack<IN> b, g;
+      Pack<RES> h;
+      if (FEED == FEED_RING) {
+        b = ring_read<IN>(ring, stage, w, c.first, d);
+        h = ring_read<RES>(ring, stage, w, c.first, d);
+        if (full) g = ring_read<IN>(ring, stage, w, c.first, d);
+      } else {
+        b = load8<IN, VEC>(a.B, row, c, d);
+        h = load8<RES, VEC>(a.H, row, c, d);
+        if (full) g = load8<IN, VEC>(a.gate, row, c, d);
+      }
+      if (channel) g = load8<IN, VEC>(a.gate, 0, c, d);
+      const Pack<IN> wpost = load8<IN, VEC>(a.w_post, 0, c, d);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        float2 u = mul2(mul2(two(b[v], j), k), two(wpost[v], j));
-        if (full || channel) u = mul2(u, two(g[v], j));
-        x[v][j] = fma2(sc, two(h[v], j), u);
+        float2 u = mul2(mul2(two(b, j), k), two(wpost, j));
+        if (full || channel) u = mul2(u, two(g, j));
+        x[v][j] = fma2(sc, two(h, j), u);
         s = fma2(x[v][j], x[v][j], s);
       }
-      store8<RES, VEC>(a.H_out, row, (v * a.team + t) * 8, d, x[v]);
+      store8<RES, VEC>(a.H_out, row, c, d, x[v]);
     }
     const float rh = rsqrtf(team_sum(s.x + s.y, slot, which, team_id, a.team, t) * inv_d + a.eps);
     which ^= 1;
     const float2 rh2 = both(rh);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
+      const Cols<VEC> c(v, t, a.team, d);
+      const Pack<IN> wpre = load8<IN, VEC>(a.w_pre, 0, c, d);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[v][j] = mul2(x[v][j], mul2(rh2, two(wpre[v], j)));
-      store8<IN, VEC>(a.N, row, (v * a.team + t) * 8, d, x[v]);
+      for (int j = 0; j < 4; ++j) x[v][j] = mul2(x[v][j], mul2(rh2, two(wpre, j)));
+      store8<IN, VEC>(a.N, row, c, d, x[v]);
     }
+    stage = stage + 1 < D ? stage + 1 : 0;
     if (t == 0) {
       if (a.rstd_b) a.rstd_b[row] = rb;
       if (a.rstd_h) a.rstd_h[row] = rh;
@@ -143,13 +146,18 @@ cudaError_t fwd_one(const NormResidual& n, const Geo& g) {
 }
 template <typename IN, typename RES>
 cudaError_t fwd_types(const NormResidual& n) {
-  const Geo g = geometry(n.T, n.d, n.num_sms, FWD_TEAM, FWD_THREADS, FWD_RESIDENT);
   // a gate of one value a row needs no alignment
   const bool wide_gate = n.gate_kind == GATE_FULL || n.gate_kind == GATE_CHANNEL;
   const bool vec = vec_ok({n.B, n.H, n.w_post, n.w_pre, n.H_out, n.N, wide_gate ? n.gate : nullptr}, n.d);
-  // the ring holds up to 8,192 columns (two rows of FP32 stream and two 16-bit operands: 128 KB; all FP32: 192 KB)
-  if (g.vpt == 1) return vec ? fwd_one<IN, RES, 1, FEED_RING>(n, g) : fwd_one<IN, RES, 1, FEED_SCALAR>(n, g);
-  return vec ? fwd_one<IN, RES, 4, FEED_VEC>(n, g) : fwd_one<IN, RES, 4, FEED_SCALAR>(n, g);
+  // rows that the ring cannot take keep one group a thread: more threads hide more of their loads
+  const int vpt = n.d > 8192 ? FWD_MANY : vec ? groups_a_thread(n.T, n.d, n.num_sms, FWD_MANY) : 1;
+  const Geo g = geometry(n.T, n.d, n.num_sms, vpt, FWD_CTA, fwd_threads(vpt));
+  const int words = vpt * (Pack<RES>::WORDS + (n.gate_kind == GATE_FULL ? 2 : 1) * Pack<IN>::WORDS);
+  const bool ring = vec && FWD_DEPTH * words * g.team * g.teams * 16 <= SMEM_BYTES;
+  if (vpt == 1) return ring ? fwd_one<IN, RES, 1, FEED_RING>(n, g) : fwd_one<IN, RES, 1, FEED_SCALAR>(n, g);
+  return ring  ? fwd_one<IN, RES, FWD_MANY, FEED_RING>(n, g)
+         : vec ? fwd_one<IN, RES, FWD_MANY, FEED_VEC>(n, g)
+               : fwd_one<IN, RES, FWD_MANY, FEED_SCALAR>(n, g);
 }
 
 }  // namespace

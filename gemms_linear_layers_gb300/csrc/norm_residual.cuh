@@ -22,7 +22,6 @@
 namespace tg {
 namespace nr {
 
-constexpr int WIDE_TEAM = 512;    // threads of a team with more than one group a thread
 constexpr int MAX_TEAMS = 15;     // named barriers 1..15
 constexpr int SMEM_BYTES = 224 * 1024;  // dynamic, beside 1 KB of the warps' slots
 
@@ -99,27 +98,41 @@ __device__ __forceinline__ float2 two(const Pack<T>& p, int i) {
   return make_float2(to_f(p.v[2 * i]), to_f(p.v[2 * i + 1]));
 }
 
-// c: first column; VEC: rows start at multiples of 16 bytes and d is a
-// multiple of 8 (checked on the host); otherwise element by element
+// The eight columns of group v of thread t: eight in a row when d is a
+// multiple of 8 (VEC: and rows start at multiples of 16 bytes, checked on the
+// host).  Otherwise one from each of eight runs of `team` columns, so that the
+// lanes of a warp, element by element, still take neighbouring columns.
+template <bool VEC>
+struct Cols {
+  int first, step;
+  __device__ __forceinline__ Cols(int v, int t, int team, int d) {
+    const bool row = VEC || (d & 7) == 0;
+    first = row ? (v * team + t) * 8 : v * 8 * team + t;
+    step = row ? 1 : team;
+  }
+  __device__ __forceinline__ int operator[](int j) const { return first + j * step; }
+};
+
 template <typename T, bool VEC>
-__device__ __forceinline__ Pack<T> load8(const void* base, long long row, int c, int d) {
+__device__ __forceinline__ Pack<T> load8(const void* base, long long row, const Cols<VEC>& c, int d) {
   Pack<T> r = zeros<T>();
-  const T* p = static_cast<const T*>(base) + row * d + c;
+  const T* p = static_cast<const T*>(base) + row * d;
   if (VEC) {
-    if (c < d) {
+    if (c.first < d) {
 #pragma unroll
-      for (int i = 0; i < Pack<T>::WORDS; ++i) reinterpret_cast<uint4*>(&r)[i] = reinterpret_cast<const uint4*>(p)[i];
+      for (int i = 0; i < Pack<T>::WORDS; ++i)
+        reinterpret_cast<uint4*>(&r)[i] = reinterpret_cast<const uint4*>(p + c.first)[i];
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (c + j < d) r.v[j] = p[j];
+      if (c[j] < d) r.v[j] = p[c[j]];
   }
   return r;
 }
 template <typename T, bool VEC>
-__device__ __forceinline__ void store8(void* base, long long row, int c, int d, const float2* f) {
-  T* p = static_cast<T*>(base) + row * d + c;
+__device__ __forceinline__ void store8(void* base, long long row, const Cols<VEC>& c, int d, const float2* f) {
+  T* p = static_cast<T*>(base) + row * d;
   Pack<T> r;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -127,7 +140,7 @@ __device__ __forceinline__ void store8(void* base, long long row, int c, int d, 
     r.v[2 * j + 1] = from_f<T>(f[j].y);
   }
   if (VEC && sizeof(T) == 2) {
-    if (c < d) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(&r);
+    if (c.first < d) *reinterpret_cast<uint4*>(p + c.first) = *reinterpret_cast<uint4*>(&r);
   } else if (VEC) {
     // lanes 2i and 2i + 1 exchange a word, so that a store fills whole sectors:
     // words 0 and 1 of the even lane's group, then those of the odd lane's
@@ -139,13 +152,13 @@ __device__ __forceinline__ void store8(void* base, long long row, int c, int d, 
     got.y = __shfl_xor_sync(~0u, give.y, 1);
     got.z = __shfl_xor_sync(~0u, give.z, 1);
     got.w = __shfl_xor_sync(~0u, give.w, 1);
-    T* even = p - 8 * odd + 4 * odd;
-    if (c - 8 * odd < d) *reinterpret_cast<uint4*>(even) = odd ? got : x[0];
-    if (c - 8 * odd + 8 < d) *reinterpret_cast<uint4*>(even + 8) = odd ? x[1] : got;
+    const int even = c.first - 8 * odd;  // the even lane's first column
+    if (even < d) *reinterpret_cast<uint4*>(p + even + 4 * odd) = odd ? got : x[0];
+    if (even + 8 < d) *reinterpret_cast<uint4*>(p + even + 8 + 4 * odd) = odd ? x[1] : got;
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (c + j < d) p[j] = r.v[j];
+      if (c[j] < d) p[c[j]] = r.v[j];
   }
 }
 
@@ -238,44 +251,67 @@ __device__ __forceinline__ float team_sum(float v, float* slot, int which, int t
   float* s = slot + which * 32;
   if ((t & 31) == 0) s[t >> 5] = v;
   team_sync(team_id, team);
-  float r = s[0];
-  for (int i = 1; i < warps; ++i) r += s[i];
-  return r;
+  v = (t & 31) < warps ? s[t & 31] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  return v;
 }
 __device__ __forceinline__ float3 team_sum3(float3 v, float4* slot, int which, int team_id, int team, int t) {
+  auto warp_sum = [&] {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(~0u, v.x, o);
-    v.y += __shfl_xor_sync(~0u, v.y, o);
-    v.z += __shfl_xor_sync(~0u, v.z, o);
-  }
+    for (int o = 16; o > 0; o >>= 1) {
+      v.x += __shfl_xor_sync(~0u, v.x, o);
+      v.y += __shfl_xor_sync(~0u, v.y, o);
+      v.z += __shfl_xor_sync(~0u, v.z, o);
+    }
+  };
+  warp_sum();
   const int warps = team >> 5;
   if (warps == 1) return v;
   float4* s = slot + which * 32;
   if ((t & 31) == 0) s[t >> 5] = make_float4(v.x, v.y, v.z, 0.f);
   team_sync(team_id, team);
-  float4 r = s[0];
-  for (int i = 1; i < warps; ++i) {
-    const float4 x = s[i];
-    r.x += x.x;
-    r.y += x.y;
-    r.z += x.z;
-  }
-  return make_float3(r.x, r.y, r.z);
+  const float4 x = (t & 31) < warps ? s[t & 31] : make_float4(0.f, 0.f, 0.f, 0.f);
+  v = make_float3(x.x, x.y, x.z);
+  warp_sum();
+  return v;
+}
+
+// The next row's lines on their way to L2 while this one is worked on (rows
+// that the ring cannot take): thread t asks for line t, t + team, ..
+template <typename T>
+__device__ __forceinline__ void prefetch_row(const void* base, long long row, int d, int t, int team) {
+  const char* p = reinterpret_cast<const char*>(static_cast<const T*>(base) + row * d);
+  for (int i = t * 128; i < d * static_cast<int>(sizeof(T)); i += team * 128)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i) : "memory");
 }
 
 // ----------------------------------------------------------------- host side
 struct Geo {
   int vpt, team, teams, ctas;
 };
-// Threads of a team: one per 8-element group up to `most`, then 2 or 4 groups
-// a thread; teams to fill a CTA of `threads`; CTAs that an SM holds at once
-// (`resident` threads: a CTA more would run as a second wave).
-inline Geo geometry(int64_t T, int64_t d, int sms, int most_team, int threads, int resident) {
-  Geo g;
+// Threads of a team with v groups a thread, and the share of their lanes at work.
+inline int team_of(int64_t d, int v) {
   const int groups = static_cast<int>((d + 7) / 8);
-  g.vpt = groups <= most_team ? 1 : groups <= 2 * WIDE_TEAM ? 2 : 4;
-  g.team = ((groups + g.vpt - 1) / g.vpt + 31) / 32 * 32;
+  return ((groups + v - 1) / v + 31) / 32 * 32;
+}
+inline double lanes_busy(int64_t d, int v) { return static_cast<double>((d + 7) / 8) / (v * team_of(d, v)); }
+
+// Groups a thread: `many` where rows are many (a row's two exchanges, loop and
+// addresses are paid once a thread: 16,384 x 576 forward 24.6 us with 1,
+// 4,096 x 5,760 75 us), 1 where each SM has a row or two (a row's latency counts),
+// or where `many` leaves more than a fifth more lanes idle.
+inline int groups_a_thread(int64_t T, int64_t d, int sms, int many) {
+  if (T <= 2 * static_cast<int64_t>(sms) || lanes_busy(d, many) < 0.8 * lanes_busy(d, 1)) return 1;
+  return many;
+}
+
+// Teams to fill a CTA of `threads`; CTAs that an SM holds at once (`resident`
+// threads: a CTA more would run as a second wave).
+inline Geo geometry(int64_t T, int64_t d, int sms, int vpt, int threads, int resident) {
+  Geo g;
+  g.vpt = vpt;
+  g.team = team_of(d, vpt);
   g.teams = threads / g.team;
   if (g.teams < 1) g.teams = 1;
   if (g.teams > MAX_TEAMS) g.teams = MAX_TEAMS;
