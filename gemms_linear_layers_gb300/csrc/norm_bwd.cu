@@ -37,7 +37,7 @@ __device__ __forceinline__ void put_kind(void* p, long long i, float v, int kind
 // it is one value a row, or 1
 template <typename IN, typename RES, int VPT, int FEED, bool EL>
 __global__ void __launch_bounds__(bwd_threads(EL, VPT), 1) norm_bwd_kernel(const Args a) {
-  constexpr bool VEC = FEED != FEED_SCALAR;
+  constexpr bool RING = FEED == FEED_RING || FEED == FEED_SHIFT;
   constexpr int D = BWD_DEPTH;
   extern __shared__ __align__(16) uint8_t ring_smem[];  // the ring, then the column sums [3][d]
   __shared__ float4 slots[2][32];
@@ -49,30 +49,35 @@ __global__ void __launch_bounds__(bwd_threads(EL, VPT), 1) norm_bwd_kernel(const
   const Ring ring = ring_of(ring_smem, VPT * (2 * Pack<RES>::WORDS + (full ? 3 : 2) * Pack<IN>::WORDS));
   pdl_wait();
   pdl_trigger();
+  // rows: those congruent to `cls` modulo a.classes, dealt to the teams of the CTAs with that class in turn
+  const int cls = blockIdx.x % a.classes;
   const long long step = static_cast<long long>(gridDim.x) * a.teams;
-  const long long row0 = static_cast<long long>(blockIdx.x) * a.teams + team_id;
+  const long long row0 = cls + static_cast<long long>(a.classes) * ((blockIdx.x / a.classes) * a.teams + team_id);
+  const int shift = FEED == FEED_SHIFT ? static_cast<int>((static_cast<long long>(cls) * d) & 7) : 0;
   auto fetch = [&](long long row, int stage) {
     if (row < a.T) {
+      const long long rest = (a.T - row) * d;
+      const int left = rest < (1 << 30) ? static_cast<int>(rest) : 1 << 30;
       int w = 0;
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
-        const Cols<VEC> c(v, t, a.team, d);
-        ring_copy<RES>(ring, stage, w, a.H, row, c.first, d);
-        ring_copy<IN>(ring, stage, w, a.B, row, c.first, d);
-        if (full) ring_copy<IN>(ring, stage, w, a.gate, row, c.first, d);
-        ring_copy<IN>(ring, stage, w, a.dN, row, c.first, d);
-        ring_copy<RES>(ring, stage, w, a.dH_out, row, c.first, d);
+        const Cols<FEED> c(v, t, a.team, d, shift);
+        ring_copy<RES, FEED>(ring, stage, w, a.H, row, c, d, left);
+        ring_copy<IN, FEED>(ring, stage, w, a.B, row, c, d, left);
+        if (full) ring_copy<IN, FEED>(ring, stage, w, a.gate, row, c, d, left);
+        ring_copy<IN, FEED>(ring, stage, w, a.dN, row, c, d, left);
+        ring_copy<RES, FEED>(ring, stage, w, a.dH_out, row, c, d, left);
       }
     }
     ring_commit();
   };
-  if (FEED == FEED_RING) {
+  if (RING) {
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) fetch(row0 + i * step, i);
   }
   // 4 groups a thread (one team a CTA): column sum k of the thread's group v, half i at (((k * VPT + v) * 2 + i) * team + t)
   constexpr bool IN_SMEM = VPT == BWD_WIDEST;
-  const int ring_bytes = FEED == FEED_RING ? D * static_cast<int>(ring.stage) : 0;
+  const int ring_bytes = RING ? D * static_cast<int>(ring.stage) : 0;
   float4* accs = reinterpret_cast<float4*>(ring_smem + ring_bytes) + t;
   auto at = [&](int k, int v, int i) -> float4& { return accs[((k * VPT + v) * 2 + i) * a.team]; };
   auto add8 = [&](int k, int v, const float2* x, float by) {
@@ -91,6 +96,19 @@ __global__ void __launch_bounds__(bwd_threads(EL, VPT), 1) norm_bwd_kernel(const
 #pragma unroll
       for (int v = 0; v < VPT; ++v) at(k, v, 0) = at(k, v, 1) = make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  // FEED_SHIFT: w_post, w_pre and a channel gate, beside the ring
+  IN* sw = reinterpret_cast<IN*>(ring_smem + ring_bytes);
+  const int groups = VPT * a.team;
+  if (FEED == FEED_SHIFT) {
+    lay_shifted<IN>(sw, 0, a.w_post, groups, d, shift);
+    lay_shifted<IN>(sw, 1, a.w_pre, groups, d, shift);
+    if (channel) lay_shifted<IN>(sw, 2, a.gate, groups, d, shift);
+    __syncthreads();
+  }
+  auto vector = [&](int which, const void* from, int v, const Cols<FEED>& c) {
+    if constexpr (FEED == FEED_SHIFT) return read_shifted<IN>(sw, which, groups, v * a.team + t);
+    else return load8<IN, FEED>(from, 0, c, d);
+  };
   constexpr int KEPT = IN_SMEM ? 1 : VPT;
   float2 acc_post[KEPT][4] = {}, acc_pre[KEPT][4] = {}, acc_gate[KEPT][4] = {};
   int which = 0, stage = 0;
@@ -108,7 +126,7 @@ __global__ void __launch_bounds__(bwd_threads(EL, VPT), 1) norm_bwd_kernel(const
   for (long long row = row0; row < a.T; row += step) {
     const float rb = rb_next, rh = rh_next, gt = gt_next;
     scalars(row + step);
-    if (FEED == FEED_RING) {
+    if (RING) {
       fetch(row + (D - 1) * step, stage + D - 1 < D ? stage + D - 1 : stage - 1);
       ring_wait<D - 1>();
     } else if (row + step < a.T) {
@@ -123,24 +141,24 @@ __global__ void __launch_bounds__(bwd_threads(EL, VPT), 1) norm_bwd_kernel(const
     Pack<IN> b, dn, g, wpre, wpost;
     Pack<RES> h, dho;
     auto take = [&](int v, bool sums) {
-      const Cols<VEC> c(v, t, a.team, d);
-      if (FEED == FEED_RING) {
+      const Cols<FEED> c(v, t, a.team, d, shift);
+      if (RING) {
         int w = v * (2 * Pack<RES>::WORDS + (full ? 3 : 2) * Pack<IN>::WORDS);
-        h = ring_read<RES>(ring, stage, w, c.first, d);
-        b = ring_read<IN>(ring, stage, w, c.first, d);
-        if (full) g = ring_read<IN>(ring, stage, w, c.first, d);
-        if (sums) dn = ring_read<IN>(ring, stage, w, c.first, d);
-        if (sums) dho = ring_read<RES>(ring, stage, w, c.first, d);
+        h = ring_read<RES, FEED>(ring, stage, w, c, d);
+        b = ring_read<IN, FEED>(ring, stage, w, c, d);
+        if (full) g = ring_read<IN, FEED>(ring, stage, w, c, d);
+        if (sums) dn = ring_read<IN, FEED>(ring, stage, w, c, d);
+        if (sums) dho = ring_read<RES, FEED>(ring, stage, w, c, d);
       } else {
-        h = load8<RES, VEC>(a.H, row, c, d);
-        b = load8<IN, VEC>(a.B, row, c, d);
-        if (full) g = load8<IN, VEC>(a.gate, row, c, d);
-        if (sums) dn = load8<IN, VEC>(a.dN, row, c, d);
-        if (sums) dho = load8<RES, VEC>(a.dH_out, row, c, d);
+        h = load8<RES, FEED>(a.H, row, c, d);
+        b = load8<IN, FEED>(a.B, row, c, d);
+        if (full) g = load8<IN, FEED>(a.gate, row, c, d);
+        if (sums) dn = load8<IN, FEED>(a.dN, row, c, d);
+        if (sums) dho = load8<RES, FEED>(a.dH_out, row, c, d);
       }
-      if (channel) g = load8<IN, VEC>(a.gate, 0, c, d);
-      if (sums) wpre = load8<IN, VEC>(a.w_pre, 0, c, d);
-      wpost = load8<IN, VEC>(a.w_post, 0, c, d);
+      if (channel) g = vector(2, a.gate, v, c);
+      if (sums) wpre = vector(1, a.w_pre, v, c);
+      wpost = vector(0, a.w_post, v, c);
     };
     // With g1 = dN w_pre, q = B w_post (times an element-wise gate) and
     // e = dH' + rstd_h g1:  sum of g2 bn = rstd_b (sum of q e - rstd_h^2 mean(g1 H') (sum of q H'))
@@ -175,7 +193,7 @@ __global__ void __launch_bounds__(bwd_threads(EL, VPT), 1) norm_bwd_kernel(const
     const float2 mk1 = both(-k1), c1 = both(rb * gt), c2 = both(-rb * (rb * (gt * s2 * inv_d))), sc = both(a.res_scale);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      const Cols<VEC> c(v, t, a.team, d);
+      const Cols<FEED> c(v, t, a.team, d, shift);
       float2 dh[4], o[4];
       take(v, false);
 #pragma unroll
@@ -183,7 +201,7 @@ __global__ void __launch_bounds__(bwd_threads(EL, VPT), 1) norm_bwd_kernel(const
         dh[j] = fma2(mk1, two(h, j), e[v][j]);
         o[j] = mul2(sc, dh[j]);
       }
-      store8<RES, VEC>(a.dH, row, c, d, o);
+      store8<RES, FEED>(a.dH, row, c, d, o);
       float2 q[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -199,8 +217,8 @@ __global__ void __launch_bounds__(bwd_threads(EL, VPT), 1) norm_bwd_kernel(const
           }
         }
       }
-      store8<IN, VEC>(a.dB, row, c, d, o);
-      if (EL && full) store8<IN, VEC>(a.dgate, row, c, d, dh);
+      store8<IN, FEED>(a.dB, row, c, d, o);
+      if (EL && full) store8<IN, FEED>(a.dgate, row, c, d, dh);
       if (IN_SMEM) {
         add8(0, v, q, rb * gt);
         if (EL && channel) add8(2, v, dh, 1.f);
@@ -208,14 +226,14 @@ __global__ void __launch_bounds__(bwd_threads(EL, VPT), 1) norm_bwd_kernel(const
     }
     stage = stage + 1 < D ? stage + 1 : 0;
   }
-  if (FEED == FEED_RING) ring_wait<0>();
+  if (RING) ring_wait<0>();
   const int sums = channel ? 3 : 2;
   float* out = a.part + static_cast<long long>(blockIdx.x) * 3 * d;
   if (IN_SMEM) {
     for (int k = 0; k < sums; ++k)
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
-        const Cols<VEC> c(v, t, a.team, d);
+        const Cols<FEED> c(v, t, a.team, d, shift);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float4 f = at(k, v, i);
@@ -234,10 +252,10 @@ __global__ void __launch_bounds__(bwd_threads(EL, VPT), 1) norm_bwd_kernel(const
     if (team_id == k) {
 #pragma unroll
       for (int v = 0; v < KEPT; ++v) {
-        const Cols<VEC> c(v, t, a.team, d);
+        const Cols<FEED> c(v, t, a.team, d, shift);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (c[j] < d) {
+          if (c[j] >= 0 && c[j] < d) {
             float* p = col + c[j];
             p[0] = (k ? p[0] : 0.f) + (j & 1 ? acc_post[v][j / 2].y : acc_post[v][j / 2].x);
             p[d] = (k ? p[d] : 0.f) + (j & 1 ? acc_pre[v][j / 2].y : acc_pre[v][j / 2].x);
@@ -273,28 +291,34 @@ __global__ void __launch_bounds__(256) norm_cols_kernel(const float* part, int c
   }
 }
 
-Geo bwd_geometry(int64_t T, int64_t d, int sms, bool el) {
+Geo bwd_geometry(int64_t T, int64_t d, bool shift, int sms, bool el) {
   int vpt = 1;
   for (const int v : {bwd_many(el), BWD_WIDEST})
-    if (team_of(d, vpt) > bwd_threads(el, vpt)) vpt = v;
-  Geo g = geometry(T, d, sms, vpt, bwd_threads(el, vpt), 1);
+    if (team_of(width_of(d, shift), vpt) > bwd_threads(el, vpt)) vpt = v;
+  Geo g = geometry(T, d, shift, sms, vpt, bwd_threads(el, vpt), 1);
   if (vpt == BWD_WIDEST) {  // one row at a time
     g.teams = 1;
     g.ctas = static_cast<int>(T < sms ? T : sms);
   }
   return g;
 }
-// Bytes of the ring, and of the column sums beside it (4 groups a thread) or in its place.
-int ring_bytes(const Geo& g, int words) { return BWD_DEPTH * words * g.team * g.teams * 16; }
+// Bytes of the column sums, beside the rest (4 groups a thread) or in its
+// place, and of shared memory in all.
 int sum_bytes(const Geo& g, int64_t d) { return static_cast<int>(g.vpt == BWD_WIDEST ? 3 * g.vpt * g.team * 32 : 3 * d * 4); }
+template <typename IN, typename RES>
+int bwd_smem(const NormResidual& n, const Geo& g, int feed) {
+  const int words = g.vpt * (2 * Pack<RES>::WORDS + (n.gate_kind == GATE_FULL ? 3 : 2) * Pack<IN>::WORDS);
+  int rows = feed == FEED_RING || feed == FEED_SHIFT ? BWD_DEPTH * words * g.team * g.teams * 16 : 0;
+  if (feed == FEED_SHIFT) rows += 3 * g.vpt * g.team * 8 * static_cast<int>(sizeof(IN));
+  const int sums = sum_bytes(g, n.d);
+  return g.vpt == BWD_WIDEST ? rows + sums : rows > sums ? rows : sums;
+}
 
 template <typename IN, typename RES, int VPT, int FEED, bool EL>
 cudaError_t bwd_one(const NormResidual& n, const Geo& g) {
   const Args a = to_args(n, g);
   auto kern = norm_bwd_kernel<IN, RES, VPT, FEED, EL>;
-  const int words = VPT * (2 * Pack<RES>::WORDS + (n.gate_kind == GATE_FULL ? 3 : 2) * Pack<IN>::WORDS);
-  const int ring = FEED == FEED_RING ? ring_bytes(g, words) : 0, sums_at = sum_bytes(g, n.d);
-  const int smem = VPT == BWD_WIDEST ? ring + sums_at : ring > sums_at ? ring : sums_at;
+  const int smem = bwd_smem<IN, RES>(n, g, FEED);
   cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   e = launch_k(kern, dim3(g.ctas), dim3(g.team * g.teams), smem, n.stream, a);
@@ -307,18 +331,25 @@ cudaError_t bwd_one(const NormResidual& n, const Geo& g) {
 template <typename IN, typename RES, bool EL>
 cudaError_t bwd_gate(const NormResidual& n) {
   const bool full = n.gate_kind == GATE_FULL;
-  Geo g = bwd_geometry(n.T, n.d, n.num_sms, EL);
-  const bool vec = vec_ok({n.B, n.H, n.w_post, n.w_pre, n.dH_out, n.dN, n.dB, n.dH, EL ? n.gate : nullptr,
-                           full ? n.dgate : nullptr},
-                          n.d);
-  const int words = g.vpt * (2 * Pack<RES>::WORDS + (full ? 3 : 2) * Pack<IN>::WORDS);
-  while (g.teams > 1 && ring_bytes(g, words) > SMEM_BYTES) --g.teams;  // fewer rows at once, no fewer CTAs
-  const bool ring = vec && ring_bytes(g, words) + (g.vpt == BWD_WIDEST ? sum_bytes(g, n.d) : 0) <= SMEM_BYTES;
+  const bool words = aligned16({n.B, n.H, n.w_post, n.w_pre, n.dH_out, n.dN, n.dB, n.dH, EL ? n.gate : nullptr,
+                                full ? n.dgate : nullptr});
   constexpr int MANY = bwd_many(EL);
-  if (g.vpt == 1) return ring ? bwd_one<IN, RES, 1, FEED_RING, EL>(n, g) : bwd_one<IN, RES, 1, FEED_SCALAR, EL>(n, g);
-  if (g.vpt == MANY)
-    return ring ? bwd_one<IN, RES, MANY, FEED_RING, EL>(n, g) : bwd_one<IN, RES, MANY, FEED_SCALAR, EL>(n, g);
-  return vec ? bwd_one<IN, RES, BWD_WIDEST, FEED_VEC, EL>(n, g) : bwd_one<IN, RES, BWD_WIDEST, FEED_SCALAR, EL>(n, g);
+  // through the ring, with fewer rows at once (no fewer CTAs) where they do not fit
+  auto fit = [&](bool shift, int feed, Geo* g) {
+    *g = bwd_geometry(n.T, n.d, shift, n.num_sms, EL);
+    while (g->teams > 1 && bwd_smem<IN, RES>(n, *g, feed) > SMEM_BYTES) --g->teams;
+    return words && (n.d % 8 != 0) == shift && g->vpt != BWD_WIDEST && bwd_smem<IN, RES>(n, *g, feed) <= SMEM_BYTES;
+  };
+  Geo g;
+  if (fit(true, FEED_SHIFT, &g))
+    return g.vpt == 1 ? bwd_one<IN, RES, 1, FEED_SHIFT, EL>(n, g) : bwd_one<IN, RES, MANY, FEED_SHIFT, EL>(n, g);
+  if (fit(false, FEED_RING, &g))
+    return g.vpt == 1 ? bwd_one<IN, RES, 1, FEED_RING, EL>(n, g) : bwd_one<IN, RES, MANY, FEED_RING, EL>(n, g);
+  g = bwd_geometry(n.T, n.d, false, n.num_sms, EL);
+  if (g.vpt == 1) return bwd_one<IN, RES, 1, FEED_SCALAR, EL>(n, g);
+  if (g.vpt == MANY) return bwd_one<IN, RES, MANY, FEED_SCALAR, EL>(n, g);
+  return words && n.d % 8 == 0 ? bwd_one<IN, RES, BWD_WIDEST, FEED_VEC, EL>(n, g)
+                               : bwd_one<IN, RES, BWD_WIDEST, FEED_SCALAR, EL>(n, g);
 }
 template <typename IN, typename RES>
 cudaError_t bwd_types(const NormResidual& n) {
@@ -329,7 +360,7 @@ cudaError_t bwd_types(const NormResidual& n) {
 
 size_t norm_residual_bwd_ws_bytes(int64_t T, int64_t d, int num_sms) {
   if (T <= 0 || d <= 0) return 0;
-  return static_cast<size_t>(T < num_sms ? T : num_sms) * 3 * d * 4;  // of each CTA
+  return static_cast<size_t>((T < num_sms ? T : num_sms) + 7) * 3 * d * 4;  // of each CTA (whole rounds of up to 8 classes)
 }
 
 cudaError_t norm_residual_bwd_launch(const NormResidual& n) {

@@ -22,6 +22,20 @@
 namespace tg {
 namespace nr {
 
+// How a kernel takes its rows.
+//   FEED_RING, FEED_VEC: rows start at multiples of 16 bytes and d is a
+//     multiple of 8; through the ring, or straight into registers where two
+//     rows do not fit shared memory.
+//   FEED_SHIFT: the same ring for any d.  Row r starts s = (r d) % 8 elements
+//     into an aligned group of eight, so the row is taken as the groups it
+//     touches, columns -s .. -s + 7 first; what its first and last group hold
+//     of the neighbouring rows is masked off.  A CTA takes rows of one s only
+//     (the rows congruent to its index modulo 8 / gcd(8, d)), so columns stay
+//     with their thread here too; the weights are laid out with the same shift
+//     in shared memory.
+//   FEED_SCALAR: bases off 16 bytes, and wide rows with such a d: element by element.
+enum Feed : int { FEED_SCALAR = 0, FEED_VEC = 1, FEED_RING = 2, FEED_SHIFT = 3 };
+
 constexpr int MAX_TEAMS = 15;     // named barriers 1..15
 constexpr int SMEM_BYTES = 224 * 1024;  // dynamic, beside 1 KB of the warps' slots
 
@@ -33,6 +47,7 @@ struct Args {
   long long T;
   int d;
   int team, teams;  // threads of a team, teams of a CTA
+  int classes;      // FEED_SHIFT: 8 / gcd(8, d), otherwise 1
   float res_scale, eps;
   int gate_kind, out_kind;
 };
@@ -98,26 +113,28 @@ __device__ __forceinline__ float2 two(const Pack<T>& p, int i) {
   return make_float2(to_f(p.v[2 * i]), to_f(p.v[2 * i + 1]));
 }
 
-// The eight columns of group v of thread t: eight in a row when d is a
-// multiple of 8 (VEC: and rows start at multiples of 16 bytes, checked on the
-// host).  Otherwise one from each of eight runs of `team` columns, so that the
-// lanes of a warp, element by element, still take neighbouring columns.
-template <bool VEC>
+// The eight columns of group v of thread t: eight in a row, from -shift on,
+// when rows are taken in groups of eight.  FEED_SCALAR with another d: one from
+// each of eight runs of `team` columns, so that the lanes of a warp, element by
+// element, still take neighbouring columns.
+template <int FEED>
 struct Cols {
   int first, step;
-  __device__ __forceinline__ Cols(int v, int t, int team, int d) {
-    const bool row = VEC || (d & 7) == 0;
-    first = row ? (v * team + t) * 8 : v * 8 * team + t;
+  __device__ __forceinline__ Cols(int v, int t, int team, int d, int shift) {
+    const bool row = FEED != FEED_SCALAR || (d & 7) == 0;
+    first = row ? (v * team + t) * 8 - (FEED == FEED_SHIFT ? shift : 0) : v * 8 * team + t;
     step = row ? 1 : team;
   }
   __device__ __forceinline__ int operator[](int j) const { return first + j * step; }
+  // FEED_SHIFT: some of the eight are not of this row
+  __device__ __forceinline__ bool edge(int d) const { return FEED == FEED_SHIFT && (first < 0 || first + 8 > d); }
 };
 
-template <typename T, bool VEC>
-__device__ __forceinline__ Pack<T> load8(const void* base, long long row, const Cols<VEC>& c, int d) {
+template <typename T, int FEED>
+__device__ __forceinline__ Pack<T> load8(const void* base, long long row, const Cols<FEED>& c, int d) {
   Pack<T> r = zeros<T>();
   const T* p = static_cast<const T*>(base) + row * d;
-  if (VEC) {
+  if (FEED != FEED_SCALAR) {
     if (c.first < d) {
 #pragma unroll
       for (int i = 0; i < Pack<T>::WORDS; ++i)
@@ -130,8 +147,8 @@ __device__ __forceinline__ Pack<T> load8(const void* base, long long row, const 
   }
   return r;
 }
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(void* base, long long row, const Cols<VEC>& c, int d, const float2* f) {
+template <typename T, int FEED>
+__device__ __forceinline__ void store8(void* base, long long row, const Cols<FEED>& c, int d, const float2* f) {
   T* p = static_cast<T*>(base) + row * d;
   Pack<T> r;
 #pragma unroll
@@ -139,26 +156,30 @@ __device__ __forceinline__ void store8(void* base, long long row, const Cols<VEC
     r.v[2 * j] = from_f<T>(f[j].x);
     r.v[2 * j + 1] = from_f<T>(f[j].y);
   }
-  if (VEC && sizeof(T) == 2) {
-    if (c.first < d) *reinterpret_cast<uint4*>(p + c.first) = *reinterpret_cast<uint4*>(&r);
-  } else if (VEC) {
-    // lanes 2i and 2i + 1 exchange a word, so that a store fills whole sectors:
-    // words 0 and 1 of the even lane's group, then those of the odd lane's
-    const int odd = threadIdx.x & 1;
-    uint4* x = reinterpret_cast<uint4*>(&r);
+  // FP32: lanes 2i and 2i + 1 exchange a word, so that a store fills whole
+  // sectors: words 0 and 1 of the even lane's group, then those of the odd lane's
+  const int odd = threadIdx.x & 1;
+  const int even = c.first - 8 * odd;  // the even lane's first column
+  uint4 got = make_uint4(0, 0, 0, 0);
+  if constexpr (FEED != FEED_SCALAR && sizeof(T) == 4) {
+    const uint4* x = reinterpret_cast<const uint4*>(&r);
     const uint4 give = odd ? x[0] : x[1];
-    uint4 got;
     got.x = __shfl_xor_sync(~0u, give.x, 1);
     got.y = __shfl_xor_sync(~0u, give.y, 1);
     got.z = __shfl_xor_sync(~0u, give.z, 1);
     got.w = __shfl_xor_sync(~0u, give.w, 1);
-    const int even = c.first - 8 * odd;  // the even lane's first column
-    if (even < d) *reinterpret_cast<uint4*>(p + even + 4 * odd) = odd ? got : x[0];
-    if (even + 8 < d) *reinterpret_cast<uint4*>(p + even + 8 + 4 * odd) = odd ? x[1] : got;
-  } else {
+  }
+  const bool edge = sizeof(T) == 4 ? FEED == FEED_SHIFT && (even < 0 || even + 16 > d) : c.edge(d);
+  if (FEED == FEED_SCALAR || edge) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (c[j] < d) p[c[j]] = r.v[j];
+      if (c[j] >= 0 && c[j] < d) p[c[j]] = r.v[j];
+  } else if (sizeof(T) == 2) {
+    if (c.first < d) *reinterpret_cast<uint4*>(p + c.first) = *reinterpret_cast<uint4*>(&r);
+  } else {
+    const uint4* x = reinterpret_cast<const uint4*>(&r);
+    if (even < d) *reinterpret_cast<uint4*>(p + even + 4 * odd) = odd ? got : x[0];
+    if (even + 8 < d) *reinterpret_cast<uint4*>(p + even + 8 + 4 * odd) = odd ? x[1] : got;
   }
 }
 
@@ -182,21 +203,34 @@ __device__ __forceinline__ Ring ring_of(const void* smem, int words) {
   r.stage = r.word * words;
   return r;
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// `bytes` of 16 (the rest becomes zeros)
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-template <typename T>
-__device__ __forceinline__ void ring_copy(const Ring& r, int stage, int& w, const void* base, long long row, int c, int d) {
+// left: elements from the row's first to the tensor's end (FEED_SHIFT: the
+// last group of the last row may end beyond it)
+template <typename T, int FEED>
+__device__ __forceinline__ void ring_copy(const Ring& r, int stage, int& w, const void* base, long long row,
+                                          const Cols<FEED>& cols, int d, int left) {
+  constexpr int N = 16 / sizeof(T);
   const T* p = static_cast<const T*>(base) + row * d;
   const uint32_t at = r.base + stage * r.stage + w * r.word;
+  const int c = cols.first;
+  auto copy = [&](uint32_t to, int col) {
+    if (FEED == FEED_SHIFT) {
+      if (col > -N && col < d) copy16(to, p + col, left - col >= N ? 16 : (left - col) * static_cast<int>(sizeof(T)));
+    } else if (col < d) {
+      copy16(to, p + col, 16);
+    }
+  };
   if constexpr (sizeof(T) == 2) {
-    if (c < d) copy16(at, p + c);
+    copy(at, c);
   } else {
     const int lane = threadIdx.x & 31;
     const int c0 = c - 8 * lane + 4 * lane;  // the warp's word `lane`
     const uint32_t to = at - 16 * lane + 16 * (lane ^ ((lane >> 3) & 1));
-    if (c0 < d) copy16(to, p + c0);
-    if (c0 + 128 < d) copy16(to + r.word, p + c0 + 128);
+    copy(to, c0);
+    copy(to + r.word, c0 + 128);
   }
   w += Pack<T>::WORDS;
 }
@@ -215,12 +249,12 @@ __device__ __forceinline__ uint4 read16(uint32_t at) {
                : "memory");
   return x;
 }
-template <typename T>
-__device__ __forceinline__ Pack<T> ring_read(const Ring& r, int stage, int& w, int c, int d) {
+template <typename T, int FEED>
+__device__ __forceinline__ Pack<T> ring_read(const Ring& r, int stage, int& w, const Cols<FEED>& c, int d) {
   Pack<T> v = zeros<T>();
   const uint32_t at = r.base + stage * r.stage + w * r.word;
   uint4* x = reinterpret_cast<uint4*>(&v);
-  if (c < d) {
+  if (c.first < d) {
     if constexpr (sizeof(T) == 2) {
       x[0] = read16(at);
     } else {
@@ -230,9 +264,28 @@ __device__ __forceinline__ Pack<T> ring_read(const Ring& r, int stage, int& w, i
       x[0] = read16(plane + 16 * (k ^ flip));
       x[1] = read16(plane + 16 * ((k + 1) ^ flip));
     }
+    if (c.edge(d)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c[j] < 0 || c[j] >= d) v.v[j] = from_f<T>(0.f);
+    }
   }
   w += Pack<T>::WORDS;
   return v;
+}
+
+// FEED_SHIFT: `n` vectors of d values each as the CTA's threads take them,
+// [n][groups a thread * team] groups of eight, zeros outside the row.
+template <typename T>
+__device__ __forceinline__ void lay_shifted(T* to, int which, const void* from, int groups, int d, int shift) {
+  for (int i = threadIdx.x; i < groups * 8; i += blockDim.x) {
+    const int c = i - shift;
+    to[which * groups * 8 + i] = c >= 0 && c < d ? static_cast<const T*>(from)[c] : from_f<T>(0.f);
+  }
+}
+template <typename T>
+__device__ __forceinline__ Pack<T> read_shifted(const T* at, int which, int groups, int group) {
+  return reinterpret_cast<const Pack<T>*>(at)[which * groups + group];
 }
 
 // -------------------------------------------------------- sums over a team
@@ -288,7 +341,7 @@ __device__ __forceinline__ void prefetch_row(const void* base, long long row, in
 
 // ----------------------------------------------------------------- host side
 struct Geo {
-  int vpt, team, teams, ctas;
+  int vpt, team, teams, ctas, classes;
 };
 // Threads of a team with v groups a thread, and the share of their lanes at work.
 inline int team_of(int64_t d, int v) {
@@ -306,25 +359,32 @@ inline int groups_a_thread(int64_t T, int64_t d, int sms, int many) {
   return many;
 }
 
+// Columns to provide threads for: a shifted row touches up to seven more.
+inline int64_t width_of(int64_t d, bool shift) { return shift ? d + 7 : d; }
+
 // Teams to fill a CTA of `threads`; CTAs that an SM holds at once (`resident`
-// threads: a CTA more would run as a second wave).
-inline Geo geometry(int64_t T, int64_t d, int sms, int vpt, int threads, int resident) {
+// threads: a CTA more would run as a second wave), in whole rounds of classes.
+inline Geo geometry(int64_t T, int64_t d, bool shift, int sms, int vpt, int threads, int resident) {
   Geo g;
   g.vpt = vpt;
-  g.team = team_of(d, vpt);
+  g.team = team_of(width_of(d, shift), vpt);
+  g.classes = 1;
+  if (shift)
+    for (int64_t k = d; k % 8; k *= 2) g.classes *= 2;
   g.teams = threads / g.team;
   if (g.teams < 1) g.teams = 1;
   if (g.teams > MAX_TEAMS) g.teams = MAX_TEAMS;
   const int64_t rows = (T + sms - 1) / sms;  // rows of an SM
   if (g.teams > rows) g.teams = static_cast<int>(rows);
   const int per_sm = resident / (g.team * g.teams) > 1 ? resident / (g.team * g.teams) : 1;
-  const int64_t most = (T + g.teams - 1) / g.teams, want = static_cast<int64_t>(sms) * per_sm;
-  g.ctas = static_cast<int>(most < want ? most : want);
+  const int64_t most = (T + g.teams - 1) / g.teams;
+  int64_t want = static_cast<int64_t>(sms) * per_sm;
+  if (most < want) want = most + g.classes - 1;
+  g.ctas = static_cast<int>(want < g.classes ? g.classes : want / g.classes * g.classes);
   return g;
 }
 
-inline bool vec_ok(std::initializer_list<const void*> ps, int64_t d) {
-  if (d % 8) return false;
+inline bool aligned16(std::initializer_list<const void*> ps) {
   for (const void* p : ps)
     if (reinterpret_cast<uintptr_t>(p) % 16) return false;
   return true;
@@ -351,15 +411,13 @@ inline Args to_args(const NormResidual& n, const Geo& g) {
   a.d = static_cast<int>(n.d);
   a.team = g.team;
   a.teams = g.teams;
+  a.classes = g.classes;
   a.res_scale = n.res_scale;
   a.eps = n.eps;
   a.gate_kind = n.gate_kind;
   a.out_kind = n.out_kind;
   return a;
 }
-
-// How a kernel takes its rows.
-enum Feed : int { FEED_SCALAR = 0, FEED_VEC = 1, FEED_RING = 2 };
 
 }  // namespace nr
 }  // namespace tg
