@@ -24,5 +24,6 @@ __all__ = [
 def __getattr__(name):
     if name in __all__:
         from . import _binding
-        return getattr(_binding, name)
+        value = globals()[name] = getattr(_binding, name)  # looked up once
+        return value
     raise AttributeError(name)

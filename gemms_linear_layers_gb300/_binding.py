@@ -487,27 +487,59 @@ def tg_bmm_attn(op, A, B, C=None, out_dtype=None, ws=None, stream=None):
     return C
 
 
+# The operators below are called many times a step on small tensors: their
+# checks read each tensor's attributes once, and addresses go to ctypes as
+# plain integers (0: NULL, for an empty tensor).
+def _raw_stream(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _scratch(op, dims, din, dout, ws, device):
+    """(address, bytes, buffer allocated here or None) of a call's workspace."""
+    n = (_lib or lib()).tg_workspace_size(op, *dims, din, dout)
+    if n == 0:
+        return 0, 0, None
+    if n == SIZE_MAX:
+        raise ValueError(f"invalid sizes {dims} for workspace query {op}")
+    if ws is not None and ws.numel() * ws.element_size() >= n:
+        return ws.data_ptr(), ws.numel() * ws.element_size(), None
+    buf = torch.empty(n, dtype=torch.uint8, device=device)
+    return buf.data_ptr(), n, buf
+
+
+def _like(t, name, shape, dtype, device):
+    """Address of a tensor that must be contiguous with this shape, type and device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on {device}")
+    return t.data_ptr()
+
+
 def _grouped(name, op, A, B, W_shape, offsets, rows, out_arg, out_shape, out_name, out_dtype, ws, stream):
     """A, B: the two operands as the C entry point takes them; W_shape: (E, d_out, d_in)."""
     E, d_out, d_in = W_shape
-    if not isinstance(offsets, torch.Tensor) or offsets.device != A.device or offsets.dtype != torch.int32 \
-            or tuple(offsets.shape) != (E + 1,) or not offsets.is_contiguous():
-        raise ValueError(f"offsets must be a contiguous int32 tensor of {E + 1} values on the operands' device")
-    if B.device != A.device:
+    dev, dt = A.device, A.dtype
+    if B.device != dev:
         raise ValueError("the operands must be on one device")
-    C = _out(out_arg, out_shape, out_dtype or getattr(out_arg, "dtype", A.dtype), A.device, out_name)
-    if C.device != A.device:
-        raise ValueError(f"{out_name} must be on the operands' device")
-    din, dout = _DT.get(A.dtype, -1), _DT.get(C.dtype, -1)
-    wp, wn, keep = ctypes.c_void_p(0), 0, None
+    off = _like(offsets, "offsets", (E + 1,), torch.int32, dev)
+    if out_arg is None:
+        C = torch.empty(out_shape, dtype=out_dtype or dt, device=dev)
+        c = C.data_ptr()
+    else:
+        C = out_arg
+        c = _like(C, out_name, out_shape, out_dtype or getattr(C, "dtype", dt), dev)
+    din, dout = _DT.get(dt, -1), _DT.get(C.dtype, -1)
+    a, b = A.data_ptr(), B.data_ptr()
+    wp, wn, keep = 0, 0, None
     # rows of whole 16-byte words at 16-byte aligned bases need no workspace
-    aligned = (A.data_ptr() | B.data_ptr()) % 16 == 0
-    if not aligned or d_in % 8 or d_out % 8:
-        wp, wn, keep = _workspace(op if aligned else TG_OP_GROUPED_UNALIGNED, (rows, E, d_out, d_in), din, dout, ws,
-                                  A.device)
-    _check(getattr(lib(), name)(_ptr(A), _ptr(B), ctypes.c_void_p(offsets.data_ptr()), _ptr(C), rows, E, d_out, d_in,
-                                din, dout, wp, wn, _stream(stream)), name)
-    if keep is not ws:
+    if (a | b) & 15 or d_in % 8 or d_out % 8:
+        wp, wn, keep = _scratch(TG_OP_GROUPED_UNALIGNED if (a | b) & 15 else op, (rows, E, d_out, d_in), din, dout, ws,
+                                dev)
+    status = getattr(_lib or lib(), name)(a, b, off, c, rows, E, d_out, d_in, din, dout, wp, wn,
+                                          _raw_stream(stream, dev))
+    if status:
+        raise TGError(status, name)
+    if keep is not None:
         _keep(keep, stream)
     return C
 
@@ -517,10 +549,11 @@ def tg_grouped_fwd(X, W, offsets, Y=None, out_dtype=None, ws=None, stream=None):
     expert: X [T, d_in], W [E, d_out, d_in], offsets [E + 1] int32 on the device."""
     _need(X, "X", 2), _need(W, "W", 3)
     T, d_in = X.shape
-    if W.shape[2] != d_in or W.dtype != X.dtype:
+    E, d_out, k = W.shape
+    if k != d_in or W.dtype != X.dtype:
         raise ValueError("W must be [E, d_out, d_in] with X's dtype")
-    return _grouped("tg_grouped_fwd", TG_OP_GROUPED_FWD, X, W, W.shape, offsets, T, Y, (T, W.shape[1]), "Y", out_dtype,
-                    ws, stream)
+    return _grouped("tg_grouped_fwd", TG_OP_GROUPED_FWD, X, W, (E, d_out, d_in), offsets, T, Y, (T, d_out), "Y",
+                    out_dtype, ws, stream)
 
 
 def tg_grouped_dgrad(dY, W, offsets, dX=None, out_dtype=None, ws=None, stream=None):
@@ -528,9 +561,10 @@ def tg_grouped_dgrad(dY, W, offsets, dX=None, out_dtype=None, ws=None, stream=No
     W [E, d_out, d_in], offsets [E + 1] int32 on the device."""
     _need(dY, "dY", 2), _need(W, "W", 3)
     T, d_out = dY.shape
-    if W.shape[1] != d_out or W.dtype != dY.dtype:
+    E, k, d_in = W.shape
+    if k != d_out or W.dtype != dY.dtype:
         raise ValueError("W must be [E, d_out, d_in] with dY's dtype")
-    return _grouped("tg_grouped_dgrad", TG_OP_GROUPED_DGRAD, dY, W, W.shape, offsets, T, dX, (T, W.shape[2]), "dX",
+    return _grouped("tg_grouped_dgrad", TG_OP_GROUPED_DGRAD, dY, W, (E, d_out, d_in), offsets, T, dX, (T, d_in), "dX",
                     out_dtype, ws, stream)
 
 
@@ -548,24 +582,32 @@ def tg_grouped_wgrad(dY, X, offsets, dW=None, out_dtype=None, ws=None, stream=No
                     stream)
 
 
-def _gate_kind(gate, T, d, dtype, device):
+def _gate(gate, T, d, dtype, device):
+    """(kind, shape, address) of a gate."""
     if gate is None:
-        return TG_GATE_NONE
-    kind = {(d,): TG_GATE_CHANNEL, (T, 1): TG_GATE_TOKEN, (T, d): TG_GATE_FULL}.get(tuple(gate.shape))
-    if kind is None or gate.dtype != dtype or gate.device != device or not gate.is_contiguous():
-        raise ValueError("gate must be a contiguous [d], [T, 1] or [T, d] tensor with B's dtype on B's device")
-    return kind
+        return TG_GATE_NONE, None, 0
+    shape = tuple(gate.shape)
+    kind = TG_GATE_CHANNEL if shape == (d,) else TG_GATE_TOKEN if shape == (T, 1) else TG_GATE_FULL
+    if kind == TG_GATE_FULL and shape != (T, d):
+        raise ValueError("gate must be [d], [T, 1] or [T, d]")
+    return kind, shape, _like(gate, "gate", shape, dtype, device)
 
 
-def _need_like(t, name, shape, dtype, device):
-    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape) \
-            or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on {device}")
-    return t
+def _result(res, outs, name, shape, dtype, device):
+    """Address of an output: the caller's, or a new one; kept in res."""
+    t = outs.get(name) if outs else None
+    if t is None:
+        t = res[name] = torch.empty(shape, dtype=dtype, device=device)
+        return t.data_ptr()
+    res[name] = t
+    return _like(t, name, shape, dtype, device)
 
 
-def _out_like(t, name, shape, dtype, device):
-    return torch.empty(shape, dtype=dtype, device=device) if t is None else _need_like(t, name, shape, dtype, device)
+def _stream_type(H, name, dtype):
+    rt = getattr(H, "dtype", None)
+    if rt is not dtype and rt is not torch.float32:
+        raise ValueError(f"{name} must have B's dtype or FP32")
+    return rt
 
 
 def tg_norm_residual_fwd(B, H, w_post, w_pre, gate=None, res_scale=1.0, eps=1e-6, outs=None, stream=None):
@@ -573,22 +615,20 @@ def tg_norm_residual_fwd(B, H, w_post, w_pre, gate=None, res_scale=1.0, eps=1e-6
     over the row: B, H [T, d], w_post, w_pre [d], gate None, [d], [T, 1] or [T, d].  H may be FP32 beside 16-bit B.
     Returns {"H", "N", "rstd_b", "rstd_h"} (outs may give any of them; outs["H"] may be H)."""
     _need(B, "B", 2)
-    T, d = B.shape
+    T, d = shape = tuple(B.shape)
     dev, dt = B.device, B.dtype
-    if not isinstance(H, torch.Tensor) or H.dtype not in (dt, torch.float32):
-        raise ValueError("H must have B's dtype or FP32")
-    _need_like(H, "H", (T, d), H.dtype, dev)
-    _need_like(w_post, "w_post", (d,), dt, dev)
-    _need_like(w_pre, "w_pre", (d,), dt, dev)
-    kind = _gate_kind(gate, T, d, dt, dev)
-    outs = outs or {}
-    res = {"H": _out_like(outs.get("H"), "H", (T, d), H.dtype, dev), "N": _out_like(outs.get("N"), "N", (T, d), dt, dev),
-           "rstd_b": _out_like(outs.get("rstd_b"), "rstd_b", (T,), torch.float32, dev),
-           "rstd_h": _out_like(outs.get("rstd_h"), "rstd_h", (T,), torch.float32, dev)}
-    _check(lib().tg_norm_residual_fwd(_ptr(B), _ptr(H), _ptr(w_post), _ptr(w_pre), _ptr(gate), kind, _ptr(res["H"]),
-                                      _ptr(res["N"]), _ptr(res["rstd_b"]), _ptr(res["rstd_h"]), T, d, float(res_scale),
-                                      float(eps), _DT.get(dt, -1), _DT.get(H.dtype, -1), _stream(stream)),
-           "tg_norm_residual_fwd")
+    rt = _stream_type(H, "H", dt)
+    h = _like(H, "H", shape, rt, dev)
+    wq, wp = _like(w_post, "w_post", (d,), dt, dev), _like(w_pre, "w_pre", (d,), dt, dev)
+    kind, _, g = _gate(gate, T, d, dt, dev)
+    res = {}
+    ho, n = _result(res, outs, "H", shape, rt, dev), _result(res, outs, "N", shape, dt, dev)
+    rb, rh = (_result(res, outs, k, (T,), torch.float32, dev) for k in ("rstd_b", "rstd_h"))
+    status = (_lib or lib()).tg_norm_residual_fwd(B.data_ptr(), h, wq, wp, g, kind, ho, n, rb, rh, T, d, res_scale, eps,
+                                                  _DT.get(dt, -1), _DT[rt] if rt in _DT else -1,
+                                                  _raw_stream(stream, dev))
+    if status:
+        raise TGError(status, "tg_norm_residual_fwd")
     return res
 
 
@@ -598,34 +638,28 @@ def tg_norm_residual_bwd(dH_out, dN, B, H_out, w_post, w_pre, rstd_b, rstd_h, ga
     "dw_pre"} and "dgate" when there is a gate.  out_dtype (B's dtype or FP32): dw_post, dw_pre and the gradient
     of a broadcast gate.  outs may give any of them."""
     _need(B, "B", 2)
-    T, d = B.shape
+    T, d = shape = tuple(B.shape)
     dev, dt = B.device, B.dtype
-    if not isinstance(H_out, torch.Tensor) or H_out.dtype not in (dt, torch.float32):
-        raise ValueError("H_out must have B's dtype or FP32")
-    rt = H_out.dtype
-    _need_like(H_out, "H_out", (T, d), rt, dev)
-    _need_like(dH_out, "dH_out", (T, d), rt, dev)
-    _need_like(dN, "dN", (T, d), dt, dev)
-    _need_like(w_post, "w_post", (d,), dt, dev)
-    _need_like(w_pre, "w_pre", (d,), dt, dev)
-    _need_like(rstd_b, "rstd_b", (T,), torch.float32, dev)
-    _need_like(rstd_h, "rstd_h", (T,), torch.float32, dev)
-    kind = _gate_kind(gate, T, d, dt, dev)
-    outs = outs or {}
-    ot = out_dtype or (outs["dw_post"].dtype if "dw_post" in outs else dt)
-    res = {"dB": _out_like(outs.get("dB"), "dB", (T, d), dt, dev), "dH": _out_like(outs.get("dH"), "dH", (T, d), rt, dev),
-           "dw_post": _out_like(outs.get("dw_post"), "dw_post", (d,), ot, dev),
-           "dw_pre": _out_like(outs.get("dw_pre"), "dw_pre", (d,), ot, dev)}
-    dgate = None
-    if kind != TG_GATE_NONE:
-        dgate = res["dgate"] = _out_like(outs.get("dgate"), "dgate", gate.shape, dt if kind == TG_GATE_FULL else ot, dev)
+    rt = _stream_type(H_out, "H_out", dt)
+    f32 = torch.float32
+    ho, dho = _like(H_out, "H_out", shape, rt, dev), _like(dH_out, "dH_out", shape, rt, dev)
+    dn = _like(dN, "dN", shape, dt, dev)
+    wq, wp = _like(w_post, "w_post", (d,), dt, dev), _like(w_pre, "w_pre", (d,), dt, dev)
+    rb, rh = _like(rstd_b, "rstd_b", (T,), f32, dev), _like(rstd_h, "rstd_h", (T,), f32, dev)
+    kind, gshape, g = _gate(gate, T, d, dt, dev)
+    ot = out_dtype or (outs["dw_post"].dtype if outs and "dw_post" in outs else dt)
+    res = {}
+    db, dh = _result(res, outs, "dB", shape, dt, dev), _result(res, outs, "dH", shape, rt, dev)
+    dwq, dwp = _result(res, outs, "dw_post", (d,), ot, dev), _result(res, outs, "dw_pre", (d,), ot, dev)
+    dg = 0 if kind == TG_GATE_NONE else _result(res, outs, "dgate", gshape, dt if kind == TG_GATE_FULL else ot, dev)
     din, dout = _DT.get(dt, -1), _DT.get(ot, -1)
-    wp, wn, keep = _workspace(TG_OP_NORM_RESIDUAL_BWD, (T, d, 0, 0), din, dout, ws, dev)
-    _check(lib().tg_norm_residual_bwd(_ptr(dH_out), _ptr(dN), _ptr(B), _ptr(H_out), _ptr(w_post), _ptr(w_pre), _ptr(gate),
-                                      kind, _ptr(rstd_b), _ptr(rstd_h), _ptr(res["dB"]), _ptr(res["dH"]),
-                                      _ptr(res["dw_post"]), _ptr(res["dw_pre"]), _ptr(dgate), T, d, float(res_scale), din,
-                                      _DT.get(rt, -1), dout, wp, wn, _stream(stream)), "tg_norm_residual_bwd")
-    if keep is not ws:
+    wsp, wsn, keep = _scratch(TG_OP_NORM_RESIDUAL_BWD, (T, d, 0, 0), din, dout, ws, dev)
+    status = (_lib or lib()).tg_norm_residual_bwd(dho, dn, B.data_ptr(), ho, wq, wp, g, kind, rb, rh, db, dh, dwq, dwp,
+                                                  dg, T, d, res_scale, din, _DT.get(rt, -1), dout, wsp, wsn,
+                                                  _raw_stream(stream, dev))
+    if status:
+        raise TGError(status, "tg_norm_residual_bwd")
+    if keep is not None:
         _keep(keep, stream)
     return res
 
@@ -642,7 +676,8 @@ class TGTensorList:
             if t.device != self.tensors[0].device:
                 raise ValueError("the tensors must be on one device")
         n = len(self.tensors)
-        self.shape_key = [(t.numel(), t.dtype) for t in self.tensors]
+        self.device = self.tensors[0].device if n else None
+        self.kinds = [(t.numel(), t.dtype) for t in self.tensors]
         self.pointers = (ctypes.c_void_p * n)(*[t.data_ptr() if t.numel() else 0 for t in self.tensors])
         self.numels = (ctypes.c_int64 * n)(*[t.numel() for t in self.tensors])
         self.dtypes = (ctypes.c_int32 * n)(*[_DT[t.dtype] for t in self.tensors])
@@ -659,39 +694,41 @@ def tg_tensor_list(tensors) -> TGTensorList:
     return tensors if isinstance(tensors, TGTensorList) else TGTensorList(tensors)
 
 
-def _grad_args(grads, norm, ws):
+def _grads(name, grads, outs, max_norm, norm, ws, stream):
     g = tg_tensor_list(grads)
-    dev = g.tensors[0].device if len(g) else (norm.device if norm is not None else torch.device("cuda"))
-    norm = _out_like(norm, "norm", (1,), torch.float32, dev)
-    wp, wn, keep = _workspace(TG_OP_GRAD_CLIP, (len(g), 0, 0, 0), TG_F32, TG_F32, ws, dev)
-    return g, norm, wp, wn, keep
+    n = len(g.tensors)
+    dev = g.device
+    if dev is None:
+        dev = norm.device if norm is not None else torch.device("cuda", torch.cuda.current_device())
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=dev)
+    at = _like(norm, "norm", (1,), torch.float32, dev)
+    wp, wn, keep = _scratch(TG_OP_GRAD_CLIP, (n, 0, 0, 0), TG_F32, TG_F32, ws, dev)
+    s = _raw_stream(stream, dev)
+    if name == "tg_grad_norm":
+        status = (_lib or lib()).tg_grad_norm(g.pointers, g.numels, g.dtypes, n, at, wp, wn, s)
+    else:
+        o = g if outs is None else tg_tensor_list(outs)
+        if o is not g and (o.kinds != g.kinds or o.device != g.device):
+            raise ValueError("outs must match the gradients' sizes and dtypes one by one, on their device")
+        status = (_lib or lib()).tg_grad_clip(g.pointers, o.pointers, g.numels, g.dtypes, n, max_norm, at, wp, wn, s)
+    if status:
+        raise TGError(status, name)
+    if keep is not None:
+        _keep(keep, stream)
+    return norm
 
 
 def tg_grad_norm(grads, norm=None, ws=None, stream=None):
     """The L2 norm of all the tensors' elements together, as one FP32 value on the device ([1])."""
-    g, norm, wp, wn, keep = _grad_args(grads, norm, ws)
-    _check(lib().tg_grad_norm(g.pointers, g.numels, g.dtypes, len(g), _ptr(norm), wp, wn, _stream(stream)),
-           "tg_grad_norm")
-    if keep is not ws:
-        _keep(keep, stream)
-    return norm
+    return _grads("tg_grad_norm", grads, None, 0.0, norm, ws, stream)
 
 
 def tg_grad_clip(grads, max_norm, outs=None, norm=None, ws=None, stream=None):
     """Scale every tensor by min(1, max_norm / (norm + 1e-6)), norm the L2 norm of all their elements together:
     in place, or into outs (tensors of the same types and sizes).  grads and outs: tensors, or lists laid out
     once with tg_tensor_list.  Returns the norm (before scaling), one FP32 value on the device ([1])."""
-    g, norm, wp, wn, keep = _grad_args(grads, norm, ws)
-    o = g if outs is None else tg_tensor_list(outs)
-    if o is not g and o.shape_key != g.shape_key:
-        raise ValueError("outs must match the gradients' sizes and dtypes one by one")
-    if o is not g and len(o) and o.tensors[0].device != g.tensors[0].device:
-        raise ValueError("outs must be on the gradients' device")
-    _check(lib().tg_grad_clip(g.pointers, o.pointers, g.numels, g.dtypes, len(g), float(max_norm), _ptr(norm), wp, wn,
-                              _stream(stream)), "tg_grad_clip")
-    if keep is not ws:
-        _keep(keep, stream)
-    return norm
+    return _grads("tg_grad_clip", grads, outs, max_norm, norm, ws, stream)
 
 
 def tg_workspace_size(op, d0, d1, d2, d3, din, dout) -> int:
