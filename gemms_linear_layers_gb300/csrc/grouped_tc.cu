@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
 
   if (warp == 0) {
     // ------------------------------------------------ producer (both CTAs)
-    if (lane == 0) {
+    if (elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
       int issued[S];
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------- MMA issuer (rank 0 only)
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
