@@ -19,14 +19,15 @@
 // neighbouring group that a load box takes in end in accumulator columns that
 // are never stored, so whatever they hold (NaN too) stays with them.
 //
-// In the weight gradient the ragged size is the reduction.  The last 64-row
-// block of a group takes in rows of the next group, which must not reach the
-// sums: the MMAs of that block stop at the last 16-row slice with a row of
-// the group, and the rest of that slice is overwritten with zeros in both
-// operands in shared memory before the MMA may read it (zeroing one operand
-// only would leave 0 * NaN).  A "mender" warp of each CTA does this; the
-// block's copies complete on a barrier of its own CTA, and the mender's
-// arrival stands for them on rank 0's "stage full" barrier.
+// In the weight gradient the ragged size is the reduction.  Whole 16-row slices
+// of a group go through the ring (the MMAs of its last 64-row block stop at the
+// last of them).  What is left, up to 15 rows, comes with rows of the next group
+// that must not reach the sums: that slice is loaded into a small buffer of its
+// own, a "mender" warp of each CTA overwrites the foreign rows with zeros in both
+// operands (zeroing one only would leave 0 * NaN), and the MMA takes it last.
+// The slice is requested before the group's blocks, so mending it costs no time
+// once a group has a few blocks: mended in the ring, 8 uneven groups of 4,096
+// rows (2,304 x 5,760) took 92 us; with all sizes multiples of 16, 78.
 //
 // Roles of a CTA (7 warps): 0 producer (TMA), 1 MMA issuer (rank 0 of the
 // pair), 2-5 epilogue, 6 mender (weight gradient).  Every wait is bounded.
@@ -49,18 +50,18 @@ constexpr int GT_BK = 64;
 constexpr int GT_STAGES = 6;
 constexpr int GT_A_BYTES = 128 * GT_BK * 2;  // one CTA's operand halves of a stage
 constexpr int GT_B_BYTES = 128 * GT_BK * 2;
-constexpr int GT_EPI_BUF = 32 * 128;
-constexpr int GT_EPI_BYTES = 4 * 2 * GT_EPI_BUF;  // weight gradient only
+constexpr int GT_SLICES = 4;      // weight gradient: buffers of a group's last 16-row slice
+constexpr int GT_SLICE_BYTES = 4 * 16 * 128;  // two 64-column chunks of each operand
 constexpr int GT_MAXG = GROUPED_PER_LAUNCH + 2;   // experts of a launch, rows before and after them
-constexpr int GT_BAR_BYTES = 256;
+constexpr int GT_BAR_BYTES = 384;
 
 template <int OP>
 struct GtCfg {
-  static constexpr int EPI = OP == G_WGRAD ? GT_EPI_BYTES : 0;
+  static constexpr int SLICES = OP == G_WGRAD ? GT_SLICES * GT_SLICE_BYTES : 0;
   static constexpr int TAB = (GT_MAXG + 1) * 4 * (OP == G_WGRAD ? 1 : 2);
-  static constexpr int SMEM = 1024 + GT_STAGES * (GT_A_BYTES + GT_B_BYTES) + EPI + GT_BAR_BYTES + TAB;
+  static constexpr int SMEM = 1024 + GT_STAGES * (GT_A_BYTES + GT_B_BYTES) + SLICES + GT_BAR_BYTES + TAB;
   static_assert(SMEM <= 232448, "shared memory budget");
-  static_assert((3 * GT_STAGES + 5) * 8 + 8 <= GT_BAR_BYTES, "barrier area");
+  static_assert((2 * GT_STAGES + 3 * GT_SLICES + 5) * 8 + 16 <= GT_BAR_BYTES, "barrier area");
 };
 
 struct GtArgs {
@@ -76,7 +77,7 @@ struct GtArgs {
   int n_width;     // weight gradient: width of a column tile (a multiple of 64)
   int first, last; // this launch holds the first / last experts: it zeroes the rows outside every group
   int out_kind;
-  int wide;        // forward, input gradient: two 16-bit features in one store; weight gradient: TMA stores
+  int wide;        // forward, input gradient: two 16-bit features in one store; weight gradient: 32-byte stores
   uint32_t idesc;  // without N
   unsigned long long timeout_ns;
   unsigned int* status;
@@ -84,20 +85,22 @@ struct GtArgs {
 
 struct GtMaps {
   CUtensorMap A;     // forward: W (box 64 x 128 rows); input gradient: W (64 x 64); weight gradient: dY (64 x 64)
-  CUtensorMap B[4];  // forward, input gradient: rows in boxes of 128, 64, 32, 16; weight gradient: [0] = X (64 x 64)
-  CUtensorMap C;     // weight gradient: dW store
+  CUtensorMap B[4];  // forward, input gradient: rows in boxes of 128, 64, 32, 16; weight gradient: [0] = X (64 x
+                     // 64), and boxes of 16 rows for the slices: [1] = dY, [2] = X
 };
 
 // One unit of work: a tile of one group.
 struct GtUnit {
   int m0;    // first feature row of the pair's tile
   int n0;    // first column: row of the activations, or (weight gradient) column of dW
-  int n;     // columns that are stored
+  int n;     // columns that are stored; 0 or less: nothing to do
   int nmma;  // columns the MMA computes (a multiple of 32)
   int e;     // expert (index of this launch)
   int r0;    // weight gradient: first row of the reduction
-  int kb;    // 64-deep blocks of the reduction; 0: the tile is zeros
-  int tail;  // rows (or columns) of the last block, 1..64
+  int kb;    // 64-deep blocks of the reduction (weight gradient: of whole 16-row slices)
+  int tail;  // 16-deep slices of the last block, 1..4
+  int rest;  // weight gradient: rows in the last slice (0: none, or all 16 in a block)
+  __device__ __forceinline__ bool zero() const { return kb == 0 && rest == 0; }  // an empty sum
 };
 
 __device__ __forceinline__ int pairs_in_grid() { return static_cast<int>(gridDim.x >> 1); }
@@ -112,12 +115,16 @@ struct GtTab {
   int* off;  // weight gradient: off[0..E]; otherwise start[0..E+2]
   int* cum;  // forward, input gradient
   int units;
+  // Forward, input gradient: the tiles of the last round, when they are at most
+  // half the pairs, are cut into `cuts` narrower ones each, so that the round
+  // ends sooner (8 uneven groups of 4,096 rows, 2,304 features: 162 tiles for 76 pairs).
+  int whole, cuts;  // units of the rounds before it
 };
 
 __device__ __forceinline__ int tiles_of(int rows) { return (rows + GT_BN - 1) / GT_BN; }
 
 template <int OP>
-__device__ void gt_build(const GtArgs& a, GtTab<OP>& t, int* s_units) {
+__device__ void gt_build(const GtArgs& a, GtTab<OP>& t, int* s_plan) {
   // one warp: running maximum of the clamped offsets, then (forward, input
   // gradient) running sum of the groups' unit counts
   const int lane = threadIdx.x & 31;
@@ -138,7 +145,7 @@ __device__ void gt_build(const GtArgs& a, GtTab<OP>& t, int* s_units) {
   }
   __syncwarp();
   if (OP == G_WGRAD) {
-    if (lane == 0) *s_units = a.E * a.m_tiles * a.n_tiles;
+    if (lane == 0) s_plan[0] = a.E * a.m_tiles * a.n_tiles;
     return;
   }
   if (lane == 0) {
@@ -147,8 +154,8 @@ __device__ void gt_build(const GtArgs& a, GtTab<OP>& t, int* s_units) {
     t.off[a.E + 2] = a.last ? T : t.off[a.E + 1];
   }
   __syncwarp();
-  int sum = 0;
   const int G = a.E + 2;
+  int sum = 0;
   for (int b = 0; b < G; b += 32) {
     const int g = b + lane;
     const int u = g < G ? tiles_of(t.off[g + 1] - t.off[g]) * a.m_tiles : 0;
@@ -163,7 +170,12 @@ __device__ void gt_build(const GtArgs& a, GtTab<OP>& t, int* s_units) {
   }
   if (lane == 0) {
     t.cum[G] = sum;
-    *s_units = sum;
+    // the last round
+    const int pairs = pairs_in_grid(), whole = sum / pairs * pairs, tail = sum - whole;
+    const int cuts = whole == 0 || tail == 0 ? 1 : min(pairs / tail, GT_BN / 32);
+    s_plan[0] = whole + tail * cuts;
+    s_plan[1] = whole;
+    s_plan[2] = cuts;
   }
 }
 
@@ -181,9 +193,17 @@ __device__ __forceinline__ GtUnit gt_unit(const GtArgs& a, const GtTab<OP>& t, i
     c.nmma = (c.n + 63) / 64 * 64;
     c.r0 = t.off[c.e];
     const int rows = t.off[c.e + 1] - c.r0;
-    c.kb = (rows + GT_BK - 1) / GT_BK;
-    c.tail = rows - (c.kb - 1) * GT_BK;
+    const int slices = rows >> 4;
+    c.rest = rows & 15;
+    c.kb = (slices + 3) >> 2;
+    c.tail = slices - (c.kb - 1) * 4;
   } else {
+    int cut = 0;
+    if (u >= t.whole) {
+      const int v = u - t.whole;
+      cut = v % t.cuts;
+      u = t.whole + v / t.cuts;
+    }
     int lo = 0, hi = a.E + 1;  // the last group whose units start at or before u
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -198,12 +218,18 @@ __device__ __forceinline__ GtUnit gt_unit(const GtArgs& a, const GtTab<OP>& t, i
     c.m0 = (r - nt * a.m_tiles) * GT_BM;
     c.n0 = start + nt * width;
     c.n = min(width, rows - nt * width);
+    if (u >= t.whole && t.cuts > 1) {
+      const int part = ((c.n + t.cuts - 1) / t.cuts + 31) / 32 * 32;
+      c.n0 += cut * part;
+      c.n = min(part, c.n - cut * part);  // nothing is left for the last cuts of a narrow tile
+    }
     c.nmma = (c.n + 31) / 32 * 32;
     c.e = lo - 1;
     const bool expert = lo >= 1 && lo <= a.E;
     c.r0 = 0;
     c.kb = expert ? (a.K + GT_BK - 1) / GT_BK : 0;
-    c.tail = a.K - (c.kb - 1) * GT_BK;
+    c.tail = (a.K - (c.kb - 1) * GT_BK + 15) >> 4;
+    c.rest = 0;
   }
   return c;
 }
@@ -228,6 +254,13 @@ __device__ __forceinline__ uint32_t pack_16(float lo, float hi, int kind) {
   return kind == EK_F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
 }
 
+// 32 bytes to a 32-byte aligned address
+__device__ __forceinline__ void store_32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 template <int OP>
 __global__ void __launch_bounds__(GT_THREADS, 1)
     grouped_kernel(const __grid_constant__ GtMaps maps, const GtArgs args) {
@@ -238,18 +271,20 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sA = smem;
   uint8_t* sB = sA + S * GT_A_BYTES;
-  uint8_t* sE = sB + S * GT_B_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sE + Cfg::EPI);
+  uint8_t* sS = sB + S * GT_B_BYTES;  // slices: two chunks of A, two of B each
+  uint64_t* full = reinterpret_cast<uint64_t*>(sS + Cfg::SLICES);
   uint64_t* empty = full + S;
-  uint64_t* landed = empty + S;  // weight gradient: a group's last block has landed in this CTA
-  uint64_t* tfull = landed + S;
+  uint64_t* landed = empty + S;         // a slice has landed in this CTA
+  uint64_t* sfull = landed + GT_SLICES;  // it has been mended in both
+  uint64_t* sempty = sfull + GT_SLICES;
+  uint64_t* tfull = sempty + GT_SLICES;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* s_units = reinterpret_cast<int*>(sE + Cfg::EPI + GT_BAR_BYTES - 4);
+  int* s_plan = reinterpret_cast<int*>(sS + Cfg::SLICES + GT_BAR_BYTES - 16);
   GtTab<OP> tab;
-  tab.off = reinterpret_cast<int*>(sE + Cfg::EPI + GT_BAR_BYTES);
+  tab.off = reinterpret_cast<int*>(sS + Cfg::SLICES + GT_BAR_BYTES);
   tab.cum = tab.off + GT_MAXG + 1;
 
   const int warp = threadIdx.x >> 5;
@@ -260,7 +295,11 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
     for (int s = 0; s < S; ++s) {
       mbar_init(smem_u32(&full[s]), 2);    // rank 0's: an arrival from each CTA, and both CTAs' bytes
       mbar_init(smem_u32(&empty[s]), 1);   // one multicast commit
-      mbar_init(smem_u32(&landed[s]), 1);  // this CTA's producer
+    }
+    for (int b = 0; b < GT_SLICES; ++b) {
+      mbar_init(smem_u32(&landed[b]), 1);  // this CTA's producer
+      mbar_init(smem_u32(&sfull[b]), 2);   // rank 0's: the mender of each CTA
+      mbar_init(smem_u32(&sempty[b]), 1);  // one multicast commit
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&tfull[i]), 1);
@@ -271,7 +310,10 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
     fence_mbar_init();
     prefetch_tmap(&maps.A);
     prefetch_tmap(&maps.B[0]);
-    if (OP == G_WGRAD) prefetch_tmap(&maps.C);
+    if (OP == G_WGRAD) {
+      prefetch_tmap(&maps.B[1]);
+      prefetch_tmap(&maps.B[2]);
+    }
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), 512);
@@ -280,14 +322,16 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
   }
   pdl_wait();
   pdl_trigger();
-  if (warp == 2) gt_build<OP>(args, tab, s_units);
+  if (warp == 2) gt_build<OP>(args, tab, s_plan);
   __syncthreads();
   // both CTAs' barriers are initialised before either signals the other's
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const unsigned long long tmo = args.timeout_ns;
-  tab.units = *s_units;
+  tab.units = s_plan[0];
+  tab.whole = s_plan[1];
+  tab.cuts = s_plan[2];
   const int pair = static_cast<int>(blockIdx.x >> 1);
 
   if (warp == 0) {
@@ -298,29 +342,40 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
       int issued[S];
 #pragma unroll
       for (int s = 0; s < S; ++s) issued[s] = -1;
+      int slice = 0, slices_issued = 0;
+      uint32_t slice_phase = 0;
       bool ok = true;
       for (int u = pair; ok && u < tab.units; u += pairs_in_grid()) {
         const GtUnit c = gt_unit<OP>(args, tab, u);
+        if (c.n <= 0) continue;
         const int m = c.m0 + static_cast<int>(rank) * 128;
         const int half = c.nmma / 2;  // this CTA's columns
         const int n = c.n0 + static_cast<int>(rank) * half;
         const int chunks = (half + 63) / 64;
         const uint32_t bytes = GT_A_BYTES + (OP == G_WGRAD ? chunks * 64 * GT_BK * 2 : half * GT_BK * 2);
+        if (OP == G_WGRAD && c.rest > 0) {
+          // the group's last, partial 16-row slice, ahead of its blocks
+          if (!mbar_wait<true>(smem_u32(&sempty[slice]), slice_phase ^ 1u, tmo, abort_flag, args.status, 0x48)) break;
+          const uint32_t bar = smem_u32(&landed[slice]);
+          const uint32_t dst = smem_u32(sS + slice * GT_SLICE_BYTES);
+          const int row = c.r0 + (c.kb > 0 ? (c.kb - 1) * GT_BK + c.tail * 16 : 0);
+          mbar_arrive_expect_tx(bar, (2 + chunks) * 2048);
+          tma_load_3d_pair(dst, &maps.B[1], bar, m, row, 0);
+          tma_load_3d_pair(dst + 2048, &maps.B[1], bar, m + 64, row, 0);
+          for (int j = 0; j < chunks; ++j) tma_load_3d_pair(dst + 4096 + j * 2048, &maps.B[2], bar, n + 64 * j, row, 0);
+          ++slices_issued;
+          if (++slice == GT_SLICES) {
+            slice = 0;
+            slice_phase ^= 1u;
+          }
+        }
         for (int kb = 0; kb < c.kb; ++kb) {
           if (!mbar_wait<true>(smem_u32(&empty[stage]), phase ^ 1u, tmo, abort_flag, args.status, 0x41)) {
             ok = false;
             break;
           }
-          // the last block of a group whose rows end inside a 16-row slice goes through the mender
-          const bool mend = OP == G_WGRAD && kb == c.kb - 1 && (c.tail & 15) != 0;
-          uint32_t bar;
-          if (mend) {
-            bar = smem_u32(&landed[stage]);
-            mbar_arrive_expect_tx(bar, bytes);
-          } else {
-            bar = mapa_shared(smem_u32(&full[stage]), 0);
-            arrive_expect_tx_cluster(bar, bytes);
-          }
+          const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
+          arrive_expect_tx_cluster(bar, bytes);
           const uint32_t a_dst = smem_u32(sA + stage * GT_A_BYTES);
           const uint32_t b_dst = smem_u32(sB + stage * GT_B_BYTES);
           const int k0 = kb * GT_BK;
@@ -363,6 +418,9 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
           if (issued[s] >= 0 && !mbar_wait<true>(smem_u32(&empty[s]), static_cast<uint32_t>(issued[s]), tmo, abort_flag,
                                                  args.status, 0x42))
             break;
+        for (int i = slices_issued > GT_SLICES ? slices_issued - GT_SLICES : 0; i < slices_issued; ++i)
+          if (!mbar_wait<true>(smem_u32(&sempty[i % GT_SLICES]), (i / GT_SLICES) & 1u, tmo, abort_flag, args.status, 0x49))
+            break;
       }
       if (!ok || *abort_flag) {
         // a wait ran out: give the copies in flight (they complete on barriers
@@ -378,10 +436,12 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
+      int slice = 0;
+      uint32_t slice_phase = 0;
       bool ok = true;
       for (int u = pair; ok && u < tab.units; u += pairs_in_grid()) {
         const GtUnit c = gt_unit<OP>(args, tab, u);
-        if (c.kb == 0) continue;
+        if (c.n <= 0 || c.zero()) continue;
         if (!mbar_wait<true>(smem_u32(&tempty[acc]), acc_phase ^ 1u, tmo, abort_flag, args.status, 0x43)) {
           ok = false;
           break;
@@ -397,7 +457,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
           tc_fence_after();
           const uint32_t a_base = smem_u32(sA + stage * GT_A_BYTES);
           const uint32_t b_base = smem_u32(sB + stage * GT_B_BYTES);
-          const int slices = kb == c.kb - 1 ? (c.tail + 15) / 16 : GT_BK / 16;
+          const int slices = kb == c.kb - 1 ? c.tail : GT_BK / 16;
 #pragma unroll
           for (int kk = 0; kk < GT_BK / 16; ++kk) {
             if (kk < slices) {
@@ -415,6 +475,21 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
           }
         }
         if (!ok) break;
+        if (OP == G_WGRAD && c.rest > 0) {
+          if (!mbar_wait<true>(smem_u32(&sfull[slice]), slice_phase, tmo, abort_flag, args.status, 0x4a)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_base = smem_u32(sS + slice * GT_SLICE_BYTES);
+          umma_f16_pair(d_tmem, sdesc_sw128(a_base, 2048, 1024), sdesc_sw128(a_base + 4096, 2048, 1024), idesc,
+                        c.kb > 0 ? 1u : 0u);
+          umma_commit_pair(smem_u32(&sempty[slice]), 0x3);
+          if (++slice == GT_SLICES) {
+            slice = 0;
+            slice_phase ^= 1u;
+          }
+        }
         umma_commit_pair(smem_u32(&tfull[acc]), 0x3);
         if (++acc == 2) {
           acc = 0;
@@ -428,27 +503,26 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
   } else if (warp == 6) {
     // ------------------------------------------------- mender (both CTAs)
     if (OP == G_WGRAD) {
-      int at = 0;                // stage of the unit's first block
-      uint32_t phases = 0;       // parity of each stage's `landed`
+      int slice = 0;
+      uint32_t phase = 0;
       for (int u = pair; u < tab.units; u += pairs_in_grid()) {
         const GtUnit c = gt_unit<OP>(args, tab, u);
-        if (c.kb == 0) continue;
-        const int stage = (at + c.kb - 1) % S;
-        at = (at + c.kb) % S;
-        if ((c.tail & 15) == 0) continue;
-        if (!mbar_wait(smem_u32(&landed[stage]), (phases >> stage) & 1u, tmo, abort_flag, args.status, 0x46)) break;
-        phases ^= 1u << stage;
-        // 16-row slices are 2,048 bytes of each 64-column chunk, a row 128 bytes
-        const int words = (16 - (c.tail & 15)) * 8;  // 16-byte words of one chunk
+        if (c.rest == 0) continue;
+        if (!mbar_wait(smem_u32(&landed[slice]), phase, tmo, abort_flag, args.status, 0x46)) break;
+        // rows rest..15 of each chunk of 16 rows of 128 bytes
+        const int words = (16 - c.rest) * 8;  // of 16 bytes
         const int chunks = (c.nmma / 2 + 63) / 64;
         for (int j = 0; j < 2 + chunks; ++j) {
-          uint8_t* chunk = j < 2 ? sA + stage * GT_A_BYTES + j * 8192 : sB + stage * GT_B_BYTES + (j - 2) * 8192;
-          uint4* z = reinterpret_cast<uint4*>(chunk + c.tail * 128);
+          uint4* z = reinterpret_cast<uint4*>(sS + slice * GT_SLICE_BYTES + j * 2048 + c.rest * 128);
           for (int i = lane; i < words; i += 32) z[i] = make_uint4(0, 0, 0, 0);
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) arrive_release_cluster(mapa_shared(smem_u32(&full[stage]), 0));
+        if (lane == 0) arrive_release_cluster(mapa_shared(smem_u32(&sfull[slice]), 0));
+        if (++slice == GT_SLICES) {
+          slice = 0;
+          phase ^= 1u;
+        }
       }
     }
   } else {
@@ -458,10 +532,11 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
     const int kind = args.out_kind;
     int acc = 0;
     uint32_t acc_phase = 0;
-    int nstore = 0;
     for (int u = pair; u < tab.units; u += pairs_in_grid()) {
       const GtUnit c = gt_unit<OP>(args, tab, u);
-      if (c.kb > 0 &&
+      if (c.n <= 0) continue;
+      const bool sum = !c.zero();
+      if (sum &&
           !mbar_wait<true>(smem_u32(&tfull[acc]), acc_phase, tmo, abort_flag, args.status, 0x47))
         break;
       tc_fence_after();
@@ -475,7 +550,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
 #pragma unroll 1
         for (int ch = 0; ch < nch; ++ch) {
           uint32_t r[32];
-          if (c.kb > 0) {
+          if (sum) {
             tmem_ld_32x32b_x32(t_row + ch * 32, r);
             tmem_ld_wait();
           } else {
@@ -508,85 +583,64 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
               if (live && j < left) p[static_cast<long long>(j) * args.M] = to_16(__uint_as_float(r[j]), kind);
           }
         }
-        if (c.kb > 0) {
+        if (sum) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(tempty_cl + static_cast<uint32_t>(acc * 8));
         }
       } else {
-        // dW: lane = row of dW, column = column of dW; 128-byte rows of columns staged in shared memory
-        const bool f32 = kind == EK_F32;
-        const int per = f32 ? 32 : 64;  // columns of a staged row
-        const int nst = (c.n + per - 1) / per;
-        const int esz = f32 ? 4 : 2;
+        // dW: lane = row, column = column: each lane stores along its own row,
+        // whole 32-byte sectors at a time
+        const long long esz = kind == EK_F32 ? 4 : 2;
+        const bool live = row + lane < args.M;
+        char* out = static_cast<char*>(args.out) +
+                    ((static_cast<long long>(c.e) * args.M + row + lane) * args.N + c.n0) * esz;
 #pragma unroll 1
-        for (int ch = 0; ch < nst; ++ch) {
-          uint32_t r[64];
-          if (c.kb > 0) {
-            tmem_ld_32x32b_x32(t_row + ch * per, r);
-            if (!f32) tmem_ld_32x32b_x32(t_row + ch * per + 32, r + 32);
+        for (int ch = 0; ch < nch; ++ch) {
+          uint32_t r[32];
+          if (sum) {
+            tmem_ld_32x32b_x32(t_row + ch * 32, r);
             tmem_ld_wait();
           } else {
 #pragma unroll
-            for (int j = 0; j < 64; ++j) r[j] = 0;
+            for (int j = 0; j < 32; ++j) r[j] = 0;
           }
-          if (ch == nst - 1 && c.kb > 0) {
+          if (ch == nch - 1 && sum) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(tempty_cl + static_cast<uint32_t>(acc * 8));
           }
-          uint8_t* buf = sE + (q * 2 + (nstore & 1)) * GT_EPI_BUF;
-          if (args.wide) {
-            if (lane == 0 && nstore >= 2) bulk_wait_read<1>();
-          }
-          __syncwarp();
-          uint8_t* rowp = buf + lane * 128;
+          char* p = out + ch * 32 * esz;
+          const int left = c.n - ch * 32;
+          if (args.wide && left >= 32) {
+            if (kind == EK_F32) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint4 v;
-            if (f32) {
-              v = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+              for (int j = 0; j < 4; ++j)
+                if (live) store_32(p + j * 32, r + 8 * j);
             } else {
-              const uint32_t* x = r + 8 * j;
-              v.x = pack_16(__uint_as_float(x[0]), __uint_as_float(x[1]), kind);
-              v.y = pack_16(__uint_as_float(x[2]), __uint_as_float(x[3]), kind);
-              v.z = pack_16(__uint_as_float(x[4]), __uint_as_float(x[5]), kind);
-              v.w = pack_16(__uint_as_float(x[6]), __uint_as_float(x[7]), kind);
-            }
-            // 128-byte swizzle: 16-byte word j of row `lane` sits at word j ^ (lane % 8)
-            *reinterpret_cast<uint4*>(rowp + ((j ^ (lane & 7)) << 4)) = v;
-          }
-          if (args.wide) {
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_3d(&maps.C, smem_u32(buf), c.n0 + ch * per, row, c.e);
-              bulk_commit();
-            }
-          } else {
-            // rows of dW that are no multiple of 16 bytes: element by element, along the rows
-            __syncwarp();
-            const int left = min(per, c.n - ch * per);
-            for (int i = 0; i < 32 && row + i < args.M; ++i) {
-              const long long at = (static_cast<long long>(c.e) * args.M + row + i) * args.N + c.n0 + ch * per;
-              for (int j = lane; j < left; j += 32) {
-                const int byte = j * esz;
-                const uint8_t* src = buf + i * 128 + (((byte >> 4) ^ (i & 7)) << 4) + (byte & 15);
-                if (f32) static_cast<uint32_t*>(args.out)[at + j] = *reinterpret_cast<const uint32_t*>(src);
-                else static_cast<uint16_t*>(args.out)[at + j] = *reinterpret_cast<const uint16_t*>(src);
+              uint32_t h[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) h[j] = pack_16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), kind);
+              if (live) {
+                store_32(p, h);
+                store_32(p + 32, h + 8);
               }
             }
-            __syncwarp();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (live && j < left) {
+                if (kind == EK_F32) reinterpret_cast<uint32_t*>(p)[j] = r[j];
+                else reinterpret_cast<uint16_t*>(p)[j] = to_16(__uint_as_float(r[j]), kind);
+              }
           }
-          ++nstore;
         }
       }
-      if (c.kb > 0 && ++acc == 2) {
+      if (sum && ++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;
       }
     }
-    if (OP == G_WGRAD && lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -651,7 +705,7 @@ cudaError_t launch_op(const GroupedCall& g, const void* A, int64_t lda, const vo
   a.status = g.status;
   const int esz = elem_bytes(g.out_kind);
   const uintptr_t out = reinterpret_cast<uintptr_t>(g.C);
-  a.wide = OP == G_WGRAD ? (a.N * esz) % 16 == 0 && out % 16 == 0 : a.M % 2 == 0 && out % 4 == 0;
+  a.wide = OP == G_WGRAD ? (a.N * esz) % 32 == 0 && out % 32 == 0 : a.M % 2 == 0 && out % 4 == 0;
 
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -676,17 +730,16 @@ cudaError_t launch_op(const GroupedCall& g, const void* A, int64_t lda, const vo
     if (OP == G_WGRAD) {
       ok = encode_tmap_3d(&m.A, A, g.in_kind, dn, T, 1, pa, 0, 64, 64, 128) &&
            encode_tmap_3d(&m.B[0], B, g.in_kind, di, T, 1, pb, 0, 64, 64, 128);
-      m.B[1] = m.B[2] = m.B[3] = m.C = m.B[0];
+      ok = ok && encode_tmap_3d(&m.B[1], A, g.in_kind, dn, T, 1, pa, 0, 64, 16, 128) &&
+           encode_tmap_3d(&m.B[2], B, g.in_kind, di, T, 1, pb, 0, 64, 16, 128);
+      m.B[3] = m.B[0];
       a.out = static_cast<char*>(g.C) + e0 * g.d_out * g.d_in * esz;
-      if (ok && a.wide)
-        ok = encode_tmap_3d(&m.C, a.out, g.out_kind, di, dn, ne, di * esz, dn * di * esz, esz == 4 ? 32 : 64, 32, 128);
     } else {
       // A: the weights [E][d_out][pitch]; B: the rows
       const char* W = static_cast<const char*>(A) + e0 * dn * pa;
       ok = encode_tmap_3d(&m.A, W, g.in_kind, di, dn, ne, pa, dn * pa, 64, OP == G_FWD ? 128 : 64, 128);
       for (int i = 0; i < 4 && ok; ++i)
         ok = encode_tmap_3d(&m.B[i], B, g.in_kind, OP == G_FWD ? di : dn, T, 1, pb, 0, 64, 128 >> i, 128);
-      m.C = m.A;
     }
     if (!ok) return cudaErrorInvalidValue;
     a.offsets = g.offsets + e0;
