@@ -499,8 +499,8 @@ def _scratch(op, dims, din, dout, ws, device):
     n = (_lib or lib()).tg_workspace_size(op, *dims, din, dout)
     if n == 0:
         return 0, 0, None
-    if n == SIZE_MAX:
-        raise ValueError(f"invalid sizes {dims} for workspace query {op}")
+    if n == SIZE_MAX:  # sizes or types that the call itself will refuse
+        return 0, 0, None
     if ws is not None and ws.numel() * ws.element_size() >= n:
         return ws.data_ptr(), ws.numel() * ws.element_size(), None
     buf = torch.empty(n, dtype=torch.uint8, device=device)
@@ -530,11 +530,7 @@ def _grouped(name, op, A, B, W_shape, offsets, rows, out_arg, out_shape, out_nam
         c = _like(C, out_name, out_shape, out_dtype or getattr(C, "dtype", dt), dev)
     din, dout = _DT.get(dt, -1), _DT.get(C.dtype, -1)
     a, b = A.data_ptr(), B.data_ptr()
-    wp, wn, keep = 0, 0, None
-    # rows of whole 16-byte words at 16-byte aligned bases need no workspace
-    if (a | b) & 15 or d_in % 8 or d_out % 8:
-        wp, wn, keep = _scratch(TG_OP_GROUPED_UNALIGNED if (a | b) & 15 else op, (rows, E, d_out, d_in), din, dout, ws,
-                                dev)
+    wp, wn, keep = _scratch(TG_OP_GROUPED_UNALIGNED if (a | b) & 15 else op, (rows, E, d_out, d_in), din, dout, ws, dev)
     status = getattr(_lib or lib(), name)(a, b, off, c, rows, E, d_out, d_in, din, dout, wp, wn,
                                           _raw_stream(stream, dev))
     if status:

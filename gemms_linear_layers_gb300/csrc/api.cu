@@ -1904,12 +1904,12 @@ size_t tg_workspace_size(tg_op op, int64_t d0, int64_t d1, int64_t d2, int64_t d
     case TG_OP_ATTN_BWD: return d2 == 64 ? attn_bwd_ws_bytes(d0, d1) : SIZE_MAX;
     case TG_OP_GEMM_FWD_LORA: return layer_lora_ws(LAYOUT_NT, d0, d1, d2, d3, in, out, ctx->sms);
     case TG_OP_GEMM_DGRAD_LORA: return layer_lora_ws(LAYOUT_NN, d0, d2, d1, d3, in, out, ctx->sms);
-    case TG_OP_GROUPED_FWD: return grouped_ws_bytes(0, d0, d1, d2, d3, false);
-    case TG_OP_GROUPED_DGRAD: return grouped_ws_bytes(1, d0, d1, d2, d3, false);
-    case TG_OP_GROUPED_WGRAD: return grouped_ws_bytes(2, d0, d1, d2, d3, false);
+    case TG_OP_GROUPED_FWD: return grouped_ws_bytes(0, d0, d1, d2, d3, false, ctx->sms);
+    case TG_OP_GROUPED_DGRAD: return grouped_ws_bytes(1, d0, d1, d2, d3, false, ctx->sms);
+    case TG_OP_GROUPED_WGRAD: return grouped_ws_bytes(2, d0, d1, d2, d3, false, ctx->sms);
     case TG_OP_GROUPED_UNALIGNED: {
       size_t most = 0;
-      for (int k = 0; k < 3; ++k) most = std::max(most, grouped_ws_bytes(k, d0, d1, d2, d3, true));
+      for (int k = 0; k < 3; ++k) most = std::max(most, grouped_ws_bytes(k, d0, d1, d2, d3, true, ctx->sms));
       return most;
     }
     case TG_OP_NORM_RESIDUAL_BWD: return norm_residual_bwd_ws_bytes(d0, d1, ctx->sms);

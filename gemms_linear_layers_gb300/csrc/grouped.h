@@ -16,14 +16,15 @@ struct GroupedCall {
   int in_kind, out_kind;
   void* ws;
   size_t ws_bytes;
+  void* parts;  // set by the launcher
   int num_sms;
   unsigned int* status;
   unsigned long long timeout_ns;
   cudaStream_t stream;
 };
 
-// Bytes of staged copies; any_base: for bases that are not 16-byte aligned.
-size_t grouped_ws_bytes(int op, int64_t T, int64_t E, int64_t d_out, int64_t d_in, bool any_base);
+// Bytes of the workspace; any_base: for bases that are not 16-byte aligned.
+size_t grouped_ws_bytes(int op, int64_t T, int64_t E, int64_t d_out, int64_t d_in, bool any_base, int num_sms);
 // *need: 0, or the workspace the call lacked (nothing was launched then).
 cudaError_t grouped_launch(const GroupedCall& g, size_t* need);
 

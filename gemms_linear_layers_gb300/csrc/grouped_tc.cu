@@ -50,16 +50,18 @@ constexpr int GT_BK = 64;
 constexpr int GT_STAGES = 6;
 constexpr int GT_A_BYTES = 128 * GT_BK * 2;  // one CTA's operand halves of a stage
 constexpr int GT_B_BYTES = 128 * GT_BK * 2;
-constexpr int GT_SLICES = 4;      // weight gradient: buffers of a group's last 16-row slice
+constexpr int GT_SLICES = 2;      // weight gradient: buffers of a group's last 16-row slice
 constexpr int GT_SLICE_BYTES = 4 * 16 * 128;  // two 64-column chunks of each operand
 constexpr int GT_MAXG = GROUPED_PER_LAUNCH + 2;   // experts of a launch, rows before and after them
 constexpr int GT_BAR_BYTES = 384;
+constexpr int GT_SPLIT_SAVES = 20;  // blocks that splitting reductions has to save a pair
 
 template <int OP>
 struct GtCfg {
   static constexpr int SLICES = OP == G_WGRAD ? GT_SLICES * GT_SLICE_BYTES : 0;
+  static constexpr int TURN = OP == G_WGRAD ? 4 * 32 * 33 * 4 : 0;  // 32 x 32 values of each epilogue warp
   static constexpr int TAB = (GT_MAXG + 1) * 4 * (OP == G_WGRAD ? 1 : 2);
-  static constexpr int SMEM = 1024 + GT_STAGES * (GT_A_BYTES + GT_B_BYTES) + SLICES + GT_BAR_BYTES + TAB;
+  static constexpr int SMEM = 1024 + GT_STAGES * (GT_A_BYTES + GT_B_BYTES) + SLICES + TURN + GT_BAR_BYTES + TAB;
   static_assert(SMEM <= 232448, "shared memory budget");
   static_assert((2 * GT_STAGES + 3 * GT_SLICES + 5) * 8 + 16 <= GT_BAR_BYTES, "barrier area");
 };
@@ -75,6 +77,7 @@ struct GtArgs {
   int m_tiles;     // of 256
   int n_tiles;     // weight gradient: column tiles
   int n_width;     // weight gradient: width of a column tile (a multiple of 64)
+  int ksplit;      // every tile's reduction in so many ranges, FP32 sums of each to out [ksplit][..]
   int first, last; // this launch holds the first / last experts: it zeroes the rows outside every group
   int out_kind;
   int wide;        // forward, input gradient: two 16-bit features in one store; weight gradient: 32-byte stores
@@ -97,10 +100,12 @@ struct GtUnit {
   int nmma;  // columns the MMA computes (a multiple of 32)
   int e;     // expert (index of this launch)
   int r0;    // weight gradient: first row of the reduction
+  int s;     // range of the reduction
   int kb;    // 64-deep blocks of the reduction (weight gradient: of whole 16-row slices)
+  int k0, k1;  // those of this range
   int tail;  // 16-deep slices of the last block, 1..4
-  int rest;  // weight gradient: rows in the last slice (0: none, or all 16 in a block)
-  __device__ __forceinline__ bool zero() const { return kb == 0 && rest == 0; }  // an empty sum
+  int rest;  // weight gradient: rows in the last slice (0: none, or all 16 in a block, or in another range)
+  __device__ __forceinline__ bool zero() const { return k0 == k1 && rest == 0; }  // an empty sum
 };
 
 __device__ __forceinline__ int pairs_in_grid() { return static_cast<int>(gridDim.x >> 1); }
@@ -145,7 +150,7 @@ __device__ void gt_build(const GtArgs& a, GtTab<OP>& t, int* s_plan) {
   }
   __syncwarp();
   if (OP == G_WGRAD) {
-    if (lane == 0) s_plan[0] = a.E * a.m_tiles * a.n_tiles;
+    if (lane == 0) s_plan[0] = a.E * a.m_tiles * a.n_tiles * a.ksplit;
     return;
   }
   if (lane == 0) {
@@ -172,8 +177,8 @@ __device__ void gt_build(const GtArgs& a, GtTab<OP>& t, int* s_plan) {
     t.cum[G] = sum;
     // the last round
     const int pairs = pairs_in_grid(), whole = sum / pairs * pairs, tail = sum - whole;
-    const int cuts = whole == 0 || tail == 0 ? 1 : min(pairs / tail, GT_BN / 32);
-    s_plan[0] = whole + tail * cuts;
+    const int cuts = whole == 0 || tail == 0 || a.ksplit > 1 ? 1 : min(pairs / tail, GT_BN / 32);
+    s_plan[0] = a.ksplit > 1 ? sum * a.ksplit : whole + tail * cuts;
     s_plan[1] = whole;
     s_plan[2] = cuts;
   }
@@ -182,6 +187,8 @@ __device__ void gt_build(const GtArgs& a, GtTab<OP>& t, int* s_plan) {
 template <int OP>
 __device__ __forceinline__ GtUnit gt_unit(const GtArgs& a, const GtTab<OP>& t, int u) {
   GtUnit c;
+  c.s = u % a.ksplit;
+  u /= a.ksplit;
   if (OP == G_WGRAD) {
     const int per = a.m_tiles * a.n_tiles;
     c.e = u / per;
@@ -231,6 +238,9 @@ __device__ __forceinline__ GtUnit gt_unit(const GtArgs& a, const GtTab<OP>& t, i
     c.tail = (a.K - (c.kb - 1) * GT_BK + 15) >> 4;
     c.rest = 0;
   }
+  c.k0 = c.s * c.kb / a.ksplit;
+  c.k1 = (c.s + 1) * c.kb / a.ksplit;
+  if (c.s + 1 < a.ksplit) c.rest = 0;  // the last range's
   return c;
 }
 
@@ -272,7 +282,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
   uint8_t* sA = smem;
   uint8_t* sB = sA + S * GT_A_BYTES;
   uint8_t* sS = sB + S * GT_B_BYTES;  // slices: two chunks of A, two of B each
-  uint64_t* full = reinterpret_cast<uint64_t*>(sS + Cfg::SLICES);
+  float* sT = reinterpret_cast<float*>(sS + Cfg::SLICES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sS + Cfg::SLICES + Cfg::TURN);
   uint64_t* empty = full + S;
   uint64_t* landed = empty + S;         // a slice has landed in this CTA
   uint64_t* sfull = landed + GT_SLICES;  // it has been mended in both
@@ -282,9 +293,9 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* s_plan = reinterpret_cast<int*>(sS + Cfg::SLICES + GT_BAR_BYTES - 16);
+  int* s_plan = reinterpret_cast<int*>(sS + Cfg::SLICES + Cfg::TURN + GT_BAR_BYTES - 16);
   GtTab<OP> tab;
-  tab.off = reinterpret_cast<int*>(sS + Cfg::SLICES + GT_BAR_BYTES);
+  tab.off = reinterpret_cast<int*>(sS + Cfg::SLICES + Cfg::TURN + GT_BAR_BYTES);
   tab.cum = tab.off + GT_MAXG + 1;
 
   const int warp = threadIdx.x >> 5;
@@ -369,7 +380,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
             slice_phase ^= 1u;
           }
         }
-        for (int kb = 0; kb < c.kb; ++kb) {
+        for (int kb = c.k0; kb < c.k1; ++kb) {
           if (!mbar_wait<true>(smem_u32(&empty[stage]), phase ^ 1u, tmo, abort_flag, args.status, 0x41)) {
             ok = false;
             break;
@@ -449,7 +460,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
         const uint32_t idesc = args.idesc | (static_cast<uint32_t>(c.nmma >> 3) << 17);
-        for (int kb = 0; kb < c.kb; ++kb) {
+        for (int kb = c.k0; kb < c.k1; ++kb) {
           if (!mbar_wait<true>(smem_u32(&full[stage]), phase, tmo, abort_flag, args.status, 0x44)) {
             ok = false;
             break;
@@ -465,7 +476,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
                                               : sdesc_sw128(a_base + kk * 2048, 8192, 1024);
               const uint64_t bd = OP == G_WGRAD ? sdesc_sw128(b_base + kk * 2048, 8192, 1024)
                                                 : sdesc_sw128(b_base + kk * 32, 16, 1024);
-              umma_f16_pair(d_tmem, ad, bd, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+              umma_f16_pair(d_tmem, ad, bd, idesc, (kb > c.k0 || kk > 0) ? 1u : 0u);
             }
           }
           umma_commit_pair(smem_u32(&empty[stage]), 0x3);
@@ -483,7 +494,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
           tc_fence_after();
           const uint32_t a_base = smem_u32(sS + slice * GT_SLICE_BYTES);
           umma_f16_pair(d_tmem, sdesc_sw128(a_base, 2048, 1024), sdesc_sw128(a_base + 4096, 2048, 1024), idesc,
-                        c.kb > 0 ? 1u : 0u);
+                        c.k1 > c.k0 ? 1u : 0u);
           umma_commit_pair(smem_u32(&sempty[slice]), 0x3);
           if (++slice == GT_SLICES) {
             slice = 0;
@@ -558,7 +569,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
             for (int j = 0; j < 32; ++j) r[j] = 0;
           }
           const int left = c.n - ch * 32;  // columns of this chunk that are stored
-          const long long base = static_cast<long long>(c.n0 + ch * 32) * args.M + f;
+          const long long base = (c.s * args.T + c.n0 + ch * 32) * args.M + f;
           if (kind == EK_F32) {
             float* p = static_cast<float*>(args.out) + base;
 #pragma unroll
@@ -594,7 +605,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
         const long long esz = kind == EK_F32 ? 4 : 2;
         const bool live = row + lane < args.M;
         char* out = static_cast<char*>(args.out) +
-                    ((static_cast<long long>(c.e) * args.M + row + lane) * args.N + c.n0) * esz;
+                    (((static_cast<long long>(c.s) * args.E + c.e) * args.M + row + lane) * args.N + c.n0) * esz;
 #pragma unroll 1
         for (int ch = 0; ch < nch; ++ch) {
           uint32_t r[32];
@@ -627,11 +638,19 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
               }
             }
           } else {
+            // rows that are no whole sectors: turned in shared memory, then
+            // stored row by row with the lanes along the row
+            float* t = sT + q * 32 * 33;
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (live && j < left) {
-                if (kind == EK_F32) reinterpret_cast<uint32_t*>(p)[j] = r[j];
-                else reinterpret_cast<uint16_t*>(p)[j] = to_16(__uint_as_float(r[j]), kind);
+            for (int j = 0; j < 32; ++j) t[lane * 33 + j] = __uint_as_float(r[j]);
+            __syncwarp();
+            const int rows = min(32, args.M - row);
+            char* at = p - (static_cast<long long>(lane) * args.N - lane) * esz;  // the warp's first row, column `lane`
+            if (lane < left)
+              for (int i = 0; i < rows; ++i, at += args.N * esz) {
+                if (kind == EK_F32) *reinterpret_cast<float*>(at) = t[i * 33 + lane];
+                else *reinterpret_cast<uint16_t*>(at) = to_16(t[i * 33 + lane], kind);
               }
           }
         }
@@ -651,6 +670,34 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// out[i] = the sum over s of parts[s][i], s ascending; n elements, `wide` in fours
+__global__ void __launch_bounds__(256) grouped_sum_kernel(const float* parts, void* out, long long n, int splits, int kind,
+                                                          int wide) {
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
+  long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (wide) {
+    for (; i < n / 4; i += step) {
+      float4 v = reinterpret_cast<const float4*>(parts)[i];
+      for (int s = 1; s < splits; ++s) {
+        const float4 x = reinterpret_cast<const float4*>(parts + s * n)[i];
+        v.x += x.x;
+        v.y += x.y;
+        v.z += x.z;
+        v.w += x.w;
+      }
+      if (kind == EK_F32) reinterpret_cast<float4*>(out)[i] = v;
+      else reinterpret_cast<uint2*>(out)[i] = make_uint2(pack_16(v.x, v.y, kind), pack_16(v.z, v.w, kind));
+    }
+    return;
+  }
+  for (; i < n; i += step) {
+    float v = parts[i];
+    for (int s = 1; s < splits; ++s) v += parts[s * n + i];
+    if (kind == EK_F32) static_cast<float*>(out)[i] = v;
+    else static_cast<uint16_t*>(out)[i] = to_16(v, kind);
   }
 }
 
@@ -682,6 +729,23 @@ __global__ void grouped_pitch_kernel(const uint16_t* src, uint16_t* dst, long lo
 int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
+// Ranges of every tile's reduction: more than one where the tiles are at most
+// half the pairs and the reduction is long enough that a pair saves more (0.33 us
+// a block) than the sums' second pass costs.  From sizes that the host knows: the
+// tiles there can be at most (forward, input gradient), the blocks of an even
+// share (weight gradient).
+int ksplit_of(int op, int64_t T, int64_t E, int64_t d_out, int64_t d_in, int num_sms) {
+  const int64_t M = op == G_DGRAD ? d_in : d_out, m_tiles = (M + GT_BM - 1) / GT_BM;
+  const int64_t most = op == G_WGRAD ? E * m_tiles * ((d_in + GT_BN - 1) / GT_BN) : m_tiles * ((E < T ? E : T) + T / GT_BN);
+  const int64_t kb = op == G_WGRAD ? T / (GT_BK * E) : ((op == G_FWD ? d_in : d_out) + GT_BK - 1) / GT_BK;
+  int64_t s = num_sms / 2 / (most < 1 ? 1 : most);
+  if (s > 8) s = 8;
+  return s > 1 && kb - kb / s >= GT_SPLIT_SAVES ? static_cast<int>(s) : 1;
+}
+int64_t out_elems(int op, int64_t T, int64_t E, int64_t d_out, int64_t d_in) {
+  return op == G_WGRAD ? E * d_out * d_in : T * (op == G_FWD ? d_out : d_in);
+}
+
 template <int OP>
 cudaError_t launch_op(const GroupedCall& g, const void* A, int64_t lda, const void* B, int64_t ldb) {
   using Cfg = GtCfg<OP>;
@@ -699,12 +763,16 @@ cudaError_t launch_op(const GroupedCall& g, const void* A, int64_t lda, const vo
   a.n_tiles = (a.N + GT_BN - 1) / GT_BN;
   a.n_width = ((a.N + a.n_tiles - 1) / a.n_tiles + 63) / 64 * 64;
   a.n_tiles = (a.N + a.n_width - 1) / a.n_width;
-  a.out_kind = g.out_kind;
+  a.ksplit = ksplit_of(OP, g.T, g.E, g.d_out, g.d_in, g.num_sms);
+  const int64_t n = out_elems(OP, g.T, g.E, g.d_out, g.d_in);
+  void* const result = a.ksplit > 1 ? g.parts : g.C;
+  a.out = result;
+  a.out_kind = a.ksplit > 1 ? static_cast<int>(EK_F32) : g.out_kind;
   a.idesc = idesc_f16(g.in_kind == EK_BF16, OP != G_FWD, OP == G_WGRAD, GT_BM, 0);
   a.timeout_ns = g.timeout_ns;
   a.status = g.status;
-  const int esz = elem_bytes(g.out_kind);
-  const uintptr_t out = reinterpret_cast<uintptr_t>(g.C);
+  const int esz = elem_bytes(a.out_kind);
+  const uintptr_t out = reinterpret_cast<uintptr_t>(result);
   a.wide = OP == G_WGRAD ? (a.N * esz) % 32 == 0 && out % 32 == 0 : a.M % 2 == 0 && out % 4 == 0;
 
   cudaLaunchConfig_t cfg = {};
@@ -733,7 +801,7 @@ cudaError_t launch_op(const GroupedCall& g, const void* A, int64_t lda, const vo
       ok = ok && encode_tmap_3d(&m.B[1], A, g.in_kind, dn, T, 1, pa, 0, 64, 16, 128) &&
            encode_tmap_3d(&m.B[2], B, g.in_kind, di, T, 1, pb, 0, 64, 16, 128);
       m.B[3] = m.B[0];
-      a.out = static_cast<char*>(g.C) + e0 * g.d_out * g.d_in * esz;
+      a.out = static_cast<char*>(result) + e0 * g.d_out * g.d_in * esz;
     } else {
       // A: the weights [E][d_out][pitch]; B: the rows
       const char* W = static_cast<const char*>(A) + e0 * dn * pa;
@@ -749,6 +817,7 @@ cudaError_t launch_op(const GroupedCall& g, const void* A, int64_t lda, const vo
     // no more pairs than there can be units
     int64_t most = OP == G_WGRAD ? ne * a.m_tiles * static_cast<int64_t>(a.n_tiles)
                                  : a.m_tiles * ((ne + 2 < g.T ? ne + 2 : g.T) + g.T / GT_BN);
+    most *= a.ksplit;
     int64_t pairs = g.num_sms / 2;
     if (pairs > most) pairs = most;
     if (pairs < 1) pairs = 1;
@@ -756,7 +825,13 @@ cudaError_t launch_op(const GroupedCall& g, const void* A, int64_t lda, const vo
     e = cudaLaunchKernelEx(&cfg, kern, m, a);
     if (e != cudaSuccess) return e;
   }
-  return cudaSuccess;
+  if (a.ksplit == 1) return cudaSuccess;
+  const int wide = n % 4 == 0 && reinterpret_cast<uintptr_t>(g.C) % 16 == 0;
+  int64_t blocks = ((wide ? n / 4 : n) + 255) / 256;
+  if (blocks > 8 * g.num_sms) blocks = 8 * g.num_sms;
+  grouped_sum_kernel<<<static_cast<unsigned>(blocks), 256, 0, g.stream>>>(static_cast<const float*>(g.parts), g.C, n,
+                                                                         a.ksplit, g.out_kind, wide);
+  return cudaGetLastError();
 }
 
 struct Operand {
@@ -766,23 +841,31 @@ struct Operand {
 
 }  // namespace
 
-// Staged copies: an operand whose rows are no multiple of 8 elements (or
-// whose base is not 16-byte aligned, when `any_base`).
-size_t grouped_ws_bytes(int op, int64_t T, int64_t E, int64_t d_out, int64_t d_in, bool any_base) {
+static size_t parts_bytes(int op, int64_t T, int64_t E, int64_t d_out, int64_t d_in, int num_sms) {
+  const int s = ksplit_of(op, T, E, d_out, d_in, num_sms);
+  return s > 1 ? up256(static_cast<size_t>(s) * out_elems(op, T, E, d_out, d_in) * 4) : 0;
+}
+
+// The sums of split reductions, then staged copies: an operand whose rows are
+// no multiple of 8 elements (or whose base is not 16-byte aligned, when `any_base`).
+size_t grouped_ws_bytes(int op, int64_t T, int64_t E, int64_t d_out, int64_t d_in, bool any_base, int num_sms) {
+  if (T <= 0 || E <= 0 || d_out <= 0 || d_in <= 0) return 0;
   const int64_t rows[2] = {op == G_WGRAD ? T : E * d_out, T};
   const int64_t cols[2] = {op == G_WGRAD ? d_out : d_in, op == G_DGRAD ? d_out : d_in};
-  size_t n = 0;
+  size_t n = parts_bytes(op, T, E, d_out, d_in, num_sms);
   for (int i = 0; i < 2; ++i)
     if (any_base || cols[i] % 8) n += up256(static_cast<size_t>(rows[i]) * up8(cols[i]) * 2);
   return n;
 }
 
-cudaError_t grouped_launch(const GroupedCall& g, size_t* need) {
+cudaError_t grouped_launch(const GroupedCall& call, size_t* need) {
+  GroupedCall g = call;
+  g.parts = g.ws;
   const Operand ops[2] = {{g.A, g.op == G_WGRAD ? g.T : g.E * g.d_out, g.op == G_WGRAD ? g.d_out : g.d_in},
                           {g.B, g.T, g.op == G_DGRAD ? g.d_out : g.d_in}};
   const void* p[2];
   int64_t pitch[2];
-  size_t used = 0;
+  size_t used = parts_bytes(g.op, g.T, g.E, g.d_out, g.d_in, g.num_sms);
   bool staged[2];
   for (int i = 0; i < 2; ++i) {
     pitch[i] = up8(ops[i].cols);

@@ -343,11 +343,14 @@ tg_status tg_bmm_attn(tg_attn_op op, const void* A, const void* B, void* C, int6
  * the tensors is read or written.
  * T < 2^31 - 1024.  Any widths and alignments run on the tensor cores: an
  * operand whose rows are no multiple of 8 elements, or whose base is not
- * 16-byte aligned, is first copied to rows that are, in `ws`: the size is
+ * 16-byte aligned, is first copied to rows that are, in `ws`.  Where there are
+ * few output tiles and long reductions, these are cut into ranges whose FP32
+ * sums, in `ws` too, are added in a fixed order.  Workspace:
  * tg_workspace_size(TG_OP_GROUPED_FWD / _DGRAD / _WGRAD, T, E, d_out, d_in),
- * or of TG_OP_GROUPED_UNALIGNED when a base is not 16-byte aligned (`ws`
- * 16-byte aligned).  Results are bitwise reproducible, and a row's result
- * does not depend on the other rows' values. */
+ * or of TG_OP_GROUPED_UNALIGNED when an operand's base is not 16-byte
+ * aligned; 16-byte aligned, its content does not matter.  Results are bitwise
+ * reproducible, and a row's result does not depend on the other rows'
+ * values. */
 tg_status tg_grouped_fwd(const void* X, const void* W, const int32_t* offsets, void* Y, int64_t T, int64_t E,
                          int64_t d_out, int64_t d_in, tg_dtype in, tg_dtype out, void* ws, size_t ws_bytes,
                          void* stream);

@@ -174,6 +174,36 @@ def test_grouped_layer_sizes(op):
         assert torch.equal(grouped(op, X, W, dY, off), got)
 
 
+@pytest.mark.parametrize("case", [
+    ("fwd", [5], 0, 0, 2304, 300), ("fwd", [0, 3, 40], 2, 5, 2312, 37), ("dgrad", [60, 1], 1, 0, 72, 3000),
+    ("wgrad", [3000, 17, 0], 3, 4, 64, 72), ("wgrad", [7000, 17, 0], 3, 4, 64, 72), ("wgrad", [4111], 0, 0, 33, 101), ("wgrad", [2600, 2500], 0, 9, 264, 300)],
+    ids=str)
+def test_grouped_long_reductions_of_few_tiles(case):
+    """Reductions that are cut into ranges and added afterwards: rows of no expert, empty experts, odd widths and
+    lengths, both output types; the same bits each time."""
+    op, sizes, lead, spare, d_in, d_out = case
+    X, W, dY, off = grouped_inputs(sizes, lead, spare, d_in, d_out, BF)
+    # an even share of 3,024 rows over three experts is too short to be cut
+    cut = tg.tg_workspace_size({"fwd": 13, "dgrad": 14, "wgrad": 15}[op], X.shape[0], len(sizes), d_out, d_in, BF, BF) > 0
+    assert cut == (sizes != [3000, 17, 0])
+    for out in (BF, F32):
+        got = grouped(op, X, W, dY, off, out_dtype=out)
+        check_grouped(op, got, X, W, dY, off, f"{case} {out}")
+        assert torch.equal(grouped(op, X, W, dY, off, out_dtype=out), got)
+
+
+def test_grouped_workspace_too_small():
+    X, W, dY, off = grouped_inputs([5], 0, 0, 2304, 300, BF)
+    o, Y = off.cuda(), torch.empty(5, 300, dtype=BF, device="cuda")
+    from gemms_linear_layers_gb300 import _binding as B
+    need = tg.tg_workspace_size(B.TG_OP_GROUPED_FWD, 5, 1, 300, 2304, BF, BF)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    call = lambda p, n: B.lib().tg_grouped_fwd(X.data_ptr(), W.data_ptr(), o.data_ptr(), Y.data_ptr(), 5, 1, 300, 2304,
+                                               B.TG_BF16, B.TG_BF16, p, n, torch.cuda.current_stream().cuda_stream)
+    assert call(0, 0) == 4 and call(ws.data_ptr(), need - 1) == 4 and call(ws.data_ptr(), need) == 0
+    check_grouped("fwd", Y, X, W, dY, off, "given workspace")
+
+
 def test_grouped_gradients_match_differences():
     """<G, Y> is linear in X and in W: its change along a direction is <dX, direction>, <dW, direction>."""
     X, W, G, off = grouped_inputs([20, 0, 33, 7], 1, 2, 64, 48, BF)
