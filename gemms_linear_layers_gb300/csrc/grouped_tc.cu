@@ -81,6 +81,7 @@ struct GtArgs {
   int first, last; // this launch holds the first / last experts: it zeroes the rows outside every group
   int out_kind;
   int wide;        // forward, input gradient: two 16-bit features in one store; weight gradient: 32-byte stores
+  int pair_out;    // weight gradient without `wide`: 16-bit, an even width, 4-byte aligned
   uint32_t idesc;  // without N
   unsigned long long timeout_ns;
   unsigned int* status;
@@ -647,11 +648,25 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
             __syncwarp();
             const int rows = min(32, args.M - row);
             char* at = p - (static_cast<long long>(lane) * args.N - lane) * esz;  // the warp's first row, column `lane`
-            if (lane < left)
-              for (int i = 0; i < rows; ++i, at += args.N * esz) {
-                if (kind == EK_F32) *reinterpret_cast<float*>(at) = t[i * 33 + lane];
-                else *reinterpret_cast<uint16_t*>(at) = to_16(t[i * 33 + lane], kind);
-              }
+            const long long pitch = args.N * esz;
+            if (args.pair_out) {  // two 16-bit columns a lane, two rows at a time
+              const int r2 = lane >> 4, c2 = 2 * (lane & 15);
+              char* at2 = p + (static_cast<long long>(r2 - lane) * args.N + c2) * 2;
+#pragma unroll 8
+              for (int i = 0; i < 32; i += 2)
+                if (i + r2 < rows && c2 < left)
+                  *reinterpret_cast<uint32_t*>(at2 + i * pitch) =
+                      pack_16(t[(i + r2) * 33 + c2], t[(i + r2) * 33 + c2 + 1], kind);
+            } else if (kind == EK_F32) {
+#pragma unroll 8
+              for (int i = 0; i < 32; ++i)
+                if (i < rows && lane < left) *reinterpret_cast<float*>(at + i * pitch) = t[i * 33 + lane];
+            } else {
+#pragma unroll 8
+              for (int i = 0; i < 32; ++i)
+                if (i < rows && lane < left)
+                  *reinterpret_cast<uint16_t*>(at + i * pitch) = to_16(t[i * 33 + lane], kind);
+            }
           }
         }
       }
@@ -774,6 +789,8 @@ cudaError_t launch_op(const GroupedCall& g, const void* A, int64_t lda, const vo
   const int esz = elem_bytes(a.out_kind);
   const uintptr_t out = reinterpret_cast<uintptr_t>(result);
   a.wide = OP == G_WGRAD ? (a.N * esz) % 32 == 0 && out % 32 == 0 : a.M % 2 == 0 && out % 4 == 0;
+
+  a.pair_out = esz == 2 && a.N % 2 == 0 && out % 4 == 0;
 
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
