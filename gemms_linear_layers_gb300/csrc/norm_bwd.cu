@@ -269,23 +269,27 @@ __global__ void __launch_bounds__(bwd_threads(EL, VPT), 1) norm_bwd_kernel(const
 }
 
 // Column sums of the CTAs' partials [ctas][3][d], a block of 32 columns per
-// CTA: 8 threads a column add every eighth partial in order, then each other.
-__global__ void __launch_bounds__(256) norm_cols_kernel(const float* part, int ctas, int d, int sums, void* dw_post,
-                                                        void* dw_pre, void* dgate, int kind) {
-  __shared__ float s[8][32];
+// CTA: 32 threads a column add every 32nd partial in order, then a warp the
+// 32 sums of a column (8 threads a column spent most of 8 us waiting for loads).
+__global__ void __launch_bounds__(1024) norm_cols_kernel(const float* part, int ctas, int d, int sums, void* dw_post,
+                                                         void* dw_pre, void* dgate, int kind) {
+  __shared__ float s[32][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int i = blockIdx.x * 32 + x;
+  int i = blockIdx.x * 32 + x;
   pdl_wait();
   pdl_trigger();
   float v = 0.f;
   if (i < sums * d) {
-#pragma unroll 4
-    for (int c = y; c < ctas; c += 8) v += part[static_cast<long long>(c) * 3 * d + i];
+#pragma unroll 5
+    for (int c = y; c < ctas; c += 32) v += part[static_cast<long long>(c) * 3 * d + i];
   }
   s[y][x] = v;
   __syncthreads();
-  if (y == 0 && i < sums * d) {
-    for (int k = 1; k < 8; ++k) v += s[k][x];
+  v = s[x][y];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  i = blockIdx.x * 32 + y;
+  if (x == 0 && i < sums * d) {
     const int which = i / d;
     put_kind(which == 0 ? dw_post : which == 1 ? dw_pre : dgate, i - which * d, v, kind);
   }
@@ -324,7 +328,7 @@ cudaError_t bwd_one(const NormResidual& n, const Geo& g) {
   e = launch_k(kern, dim3(g.ctas), dim3(g.team * g.teams), smem, n.stream, a);
   if (e != cudaSuccess) return e;
   const int sums = n.gate_kind == GATE_CHANNEL ? 3 : 2;
-  return launch_k(norm_cols_kernel, dim3(static_cast<unsigned>((sums * n.d + 31) / 32)), dim3(256), 0, n.stream,
+  return launch_k(norm_cols_kernel, dim3(static_cast<unsigned>((sums * n.d + 31) / 32)), dim3(1024), 0, n.stream,
                   static_cast<const float*>(n.ws), g.ctas, static_cast<int>(n.d), sums, n.dw_post, n.dw_pre, n.dgate,
                   n.out_kind);
 }
