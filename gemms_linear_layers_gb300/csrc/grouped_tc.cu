@@ -75,6 +75,7 @@ struct GtArgs {
   int N;           // weight gradient: d_in
   int K;           // forward: d_in; input gradient: d_out
   int m_tiles;     // of 256
+  float by_m, by_tiles;  // 1 / m_tiles, 1 / (m_tiles n_tiles)
   int n_tiles;     // weight gradient: column tiles
   int n_width;     // weight gradient: width of a column tile (a multiple of 64)
   int ksplit;      // every tile's reduction in so many ranges, FP32 sums of each to out [ksplit][..]
@@ -127,6 +128,17 @@ struct GtTab {
   int whole, cuts;  // units of the rounds before it
 };
 
+// n / d for 0 <= n < 2^24 (so many tiles of output are more than the GPU's
+// memory), by = 1 / d rounded: the integer divisions' dozens of dependent
+// instructions stood between a unit and its first copy (1,000 rows over 32 experts
+// 19.3 us with them, 17.3 without).
+__device__ __forceinline__ int quotient(int n, int d, float by) {
+  int q = __float2int_rd(__int2float_rn(n) * by);
+  const int r = n - q * d;
+  if (r < 0) --q;
+  if (r >= d) ++q;
+  return q;
+}
 __device__ __forceinline__ int tiles_of(int rows) { return (rows + GT_BN - 1) / GT_BN; }
 
 template <int OP>
@@ -177,8 +189,13 @@ __device__ void gt_build(const GtArgs& a, GtTab<OP>& t, int* s_plan) {
   if (lane == 0) {
     t.cum[G] = sum;
     // the last round
-    const int pairs = pairs_in_grid(), whole = sum / pairs * pairs, tail = sum - whole;
-    const int cuts = whole == 0 || tail == 0 || a.ksplit > 1 ? 1 : min(pairs / tail, GT_BN / 32);
+    const int pairs = pairs_in_grid();
+    int whole = 0, tail = sum, cuts = 1;
+    if (sum >= pairs) {
+      whole = sum / pairs * pairs;
+      tail = sum - whole;
+      if (tail > 0 && a.ksplit == 1) cuts = min(pairs / tail, GT_BN / 32);
+    }
     s_plan[0] = a.ksplit > 1 ? sum * a.ksplit : whole + tail * cuts;
     s_plan[1] = whole;
     s_plan[2] = cuts;
@@ -188,13 +205,17 @@ __device__ void gt_build(const GtArgs& a, GtTab<OP>& t, int* s_plan) {
 template <int OP>
 __device__ __forceinline__ GtUnit gt_unit(const GtArgs& a, const GtTab<OP>& t, int u) {
   GtUnit c;
-  c.s = u % a.ksplit;
-  u /= a.ksplit;
+  c.s = 0;
+  if (a.ksplit > 1) {
+    const int t = u / a.ksplit;
+    c.s = u - t * a.ksplit;
+    u = t;
+  }
   if (OP == G_WGRAD) {
     const int per = a.m_tiles * a.n_tiles;
-    c.e = u / per;
+    c.e = quotient(u, per, a.by_tiles);
     const int r = u - c.e * per;
-    const int nt = r / a.m_tiles;
+    const int nt = quotient(r, a.m_tiles, a.by_m);
     c.m0 = (r - nt * a.m_tiles) * GT_BM;
     c.n0 = nt * a.n_width;
     c.n = min(a.n_width, a.N - c.n0);
@@ -208,9 +229,9 @@ __device__ __forceinline__ GtUnit gt_unit(const GtArgs& a, const GtTab<OP>& t, i
   } else {
     int cut = 0;
     if (u >= t.whole) {
-      const int v = u - t.whole;
-      cut = v % t.cuts;
-      u = t.whole + v / t.cuts;
+      const int v = u - t.whole, w = t.cuts == 1 ? v : v / t.cuts;
+      cut = v - w * t.cuts;
+      u = t.whole + w;
     }
     int lo = 0, hi = a.E + 1;  // the last group whose units start at or before u
     while (lo < hi) {
@@ -220,9 +241,9 @@ __device__ __forceinline__ GtUnit gt_unit(const GtArgs& a, const GtTab<OP>& t, i
     }
     const int start = t.off[lo], rows = t.off[lo + 1] - start;
     const int r = u - t.cum[lo];
-    const int nt = r / a.m_tiles;
+    const int nt = quotient(r, a.m_tiles, a.by_m);
     const int tiles = tiles_of(rows);
-    const int width = ((rows + tiles - 1) / tiles + 31) / 32 * 32;
+    const int width = ((tiles <= 1 ? rows : (rows + tiles - 1) / tiles) + 31) / 32 * 32;
     c.m0 = (r - nt * a.m_tiles) * GT_BM;
     c.n0 = start + nt * width;
     c.n = min(width, rows - nt * width);
@@ -239,9 +260,13 @@ __device__ __forceinline__ GtUnit gt_unit(const GtArgs& a, const GtTab<OP>& t, i
     c.tail = (a.K - (c.kb - 1) * GT_BK + 15) >> 4;
     c.rest = 0;
   }
-  c.k0 = c.s * c.kb / a.ksplit;
-  c.k1 = (c.s + 1) * c.kb / a.ksplit;
-  if (c.s + 1 < a.ksplit) c.rest = 0;  // the last range's
+  c.k0 = 0;
+  c.k1 = c.kb;
+  if (a.ksplit > 1) {
+    c.k0 = c.s * c.kb / a.ksplit;
+    c.k1 = (c.s + 1) * c.kb / a.ksplit;
+    if (c.s + 1 < a.ksplit) c.rest = 0;  // the last range's
+  }
   return c;
 }
 
@@ -782,6 +807,8 @@ cudaError_t launch_op(const GroupedCall& g, const void* A, int64_t lda, const vo
   const int64_t n = out_elems(OP, g.T, g.E, g.d_out, g.d_in);
   void* const result = a.ksplit > 1 ? g.parts : g.C;
   a.out = result;
+  a.by_m = 1.f / static_cast<float>(a.m_tiles);
+  a.by_tiles = 1.f / (static_cast<float>(a.m_tiles) * static_cast<float>(a.n_tiles));
   a.out_kind = a.ksplit > 1 ? static_cast<int>(EK_F32) : g.out_kind;
   a.idesc = idesc_f16(g.in_kind == EK_BF16, OP != G_FWD, OP == G_WGRAD, GT_BM, 0);
   a.timeout_ns = g.timeout_ns;
