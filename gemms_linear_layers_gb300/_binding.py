@@ -494,17 +494,30 @@ def _raw_stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
-def _scratch(op, dims, din, dout, ws, device):
-    """(address, bytes, buffer allocated here or None) of a call's workspace."""
+# Workspaces of calls on the current stream, kept by (device, stream): an
+# allocation a call took a quarter of a small call's host time.  Calls on one
+# stream use theirs one after the other.  Not kept: large ones, those of a call
+# that is being captured (a graph outlives them) and of a caller's own stream.
+_kept = {}
+_KEEP_BYTES = 32 << 20
+
+
+def _scratch(op, dims, din, dout, ws, device, stream, raw):
+    """(address, bytes, buffer to hand to _keep or None) of a call's workspace; raw: the stream's handle."""
     n = (_lib or lib()).tg_workspace_size(op, *dims, din, dout)
-    if n == 0:
-        return 0, 0, None
-    if n == SIZE_MAX:  # sizes or types that the call itself will refuse
+    if n == 0 or n == SIZE_MAX:  # SIZE_MAX: sizes or types that the call itself will refuse
         return 0, 0, None
     if ws is not None and ws.numel() * ws.element_size() >= n:
         return ws.data_ptr(), ws.numel() * ws.element_size(), None
-    buf = torch.empty(n, dtype=torch.uint8, device=device)
-    return buf.data_ptr(), n, buf
+    if stream is not None or n > _KEEP_BYTES or torch.cuda.is_current_stream_capturing():
+        buf = torch.empty(n, dtype=torch.uint8, device=device)
+        return buf.data_ptr(), n, buf
+    key = (device.index, raw)
+    kept = _kept.get(key)
+    if kept is None or kept[1] < n:
+        buf = torch.empty(max(n, 1 << 20), dtype=torch.uint8, device=device)
+        kept = _kept[key] = (buf.data_ptr(), buf.numel(), buf)
+    return kept[0], kept[1], None
 
 
 def _like(t, name, shape, dtype, device):
@@ -530,9 +543,10 @@ def _grouped(name, op, A, B, W_shape, offsets, rows, out_arg, out_shape, out_nam
         c = _like(C, out_name, out_shape, out_dtype or getattr(C, "dtype", dt), dev)
     din, dout = _DT.get(dt, -1), _DT.get(C.dtype, -1)
     a, b = A.data_ptr(), B.data_ptr()
-    wp, wn, keep = _scratch(TG_OP_GROUPED_UNALIGNED if (a | b) & 15 else op, (rows, E, d_out, d_in), din, dout, ws, dev)
-    status = getattr(_lib or lib(), name)(a, b, off, c, rows, E, d_out, d_in, din, dout, wp, wn,
-                                          _raw_stream(stream, dev))
+    raw = _raw_stream(stream, dev)
+    wp, wn, keep = _scratch(TG_OP_GROUPED_UNALIGNED if (a | b) & 15 else op, (rows, E, d_out, d_in), din, dout, ws, dev,
+                            stream, raw)
+    status = getattr(_lib or lib(), name)(a, b, off, c, rows, E, d_out, d_in, din, dout, wp, wn, raw)
     if status:
         raise TGError(status, name)
     if keep is not None:
@@ -649,10 +663,10 @@ def tg_norm_residual_bwd(dH_out, dN, B, H_out, w_post, w_pre, rstd_b, rstd_h, ga
     dwq, dwp = _result(res, outs, "dw_post", (d,), ot, dev), _result(res, outs, "dw_pre", (d,), ot, dev)
     dg = 0 if kind == TG_GATE_NONE else _result(res, outs, "dgate", gshape, dt if kind == TG_GATE_FULL else ot, dev)
     din, dout = _DT.get(dt, -1), _DT.get(ot, -1)
-    wsp, wsn, keep = _scratch(TG_OP_NORM_RESIDUAL_BWD, (T, d, 0, 0), din, dout, ws, dev)
+    raw = _raw_stream(stream, dev)
+    wsp, wsn, keep = _scratch(TG_OP_NORM_RESIDUAL_BWD, (T, d, 0, 0), din, dout, ws, dev, stream, raw)
     status = (_lib or lib()).tg_norm_residual_bwd(dho, dn, B.data_ptr(), ho, wq, wp, g, kind, rb, rh, db, dh, dwq, dwp,
-                                                  dg, T, d, res_scale, din, _DT.get(rt, -1), dout, wsp, wsn,
-                                                  _raw_stream(stream, dev))
+                                                  dg, T, d, res_scale, din, _DT.get(rt, -1), dout, wsp, wsn, raw)
     if status:
         raise TGError(status, "tg_norm_residual_bwd")
     if keep is not None:
@@ -673,10 +687,11 @@ class TGTensorList:
                 raise ValueError("the tensors must be on one device")
         n = len(self.tensors)
         self.device = self.tensors[0].device if n else None
-        self.kinds = [(t.numel(), t.dtype) for t in self.tensors]
-        self.pointers = (ctypes.c_void_p * n)(*[t.data_ptr() if t.numel() else 0 for t in self.tensors])
-        self.numels = (ctypes.c_int64 * n)(*[t.numel() for t in self.tensors])
-        self.dtypes = (ctypes.c_int32 * n)(*[_DT[t.dtype] for t in self.tensors])
+        self._arrays = ((ctypes.c_void_p * n)(*[t.data_ptr() if t.numel() else 0 for t in self.tensors]),
+                        (ctypes.c_int64 * n)(*[t.numel() for t in self.tensors]),
+                        (ctypes.c_int32 * n)(*[_DT[t.dtype] for t in self.tensors]))
+        self.pointers, self.numels, self.dtypes = (ctypes.addressof(a) for a in self._arrays)
+        self.kinds = bytes(self._arrays[1]) + bytes(self._arrays[2])
 
     def __len__(self):
         return len(self.tensors)
@@ -699,8 +714,8 @@ def _grads(name, grads, outs, max_norm, norm, ws, stream):
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=dev)
     at = _like(norm, "norm", (1,), torch.float32, dev)
-    wp, wn, keep = _scratch(TG_OP_GRAD_CLIP, (n, 0, 0, 0), TG_F32, TG_F32, ws, dev)
     s = _raw_stream(stream, dev)
+    wp, wn, keep = _scratch(TG_OP_GRAD_CLIP, (n, 0, 0, 0), TG_F32, TG_F32, ws, dev, stream, s)
     if name == "tg_grad_norm":
         status = (_lib or lib()).tg_grad_norm(g.pointers, g.numels, g.dtypes, n, at, wp, wn, s)
     else:

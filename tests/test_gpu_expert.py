@@ -535,3 +535,34 @@ def test_clip_edges_graph_and_refusals():
         with pytest.raises(tg.TGError) as e:
             tg.tg_grad_clip(src, bad)
         assert e.value.status == 1
+
+
+def test_workspaces_kept_by_the_binding():
+    """Calls of all sizes in a row on one stream share its workspace; calls on two torch streams, and a graph
+    captured in between, have others: every result is that of the call alone."""
+    cases = [bwd_case(T, d, "channel", BF, BF, 0.75) for T, d in ((40, 576), (700, 4096), (3, 72))]
+    for got, ref in cases:
+        for n, (v, e) in ref.items():
+            R.check(got[n], v, e, n)
+    i = norm_inputs(200, 2304, "none", BF, BF)
+    rb, rh = (torch.ones(200, device="cuda") for _ in range(2))
+    call = lambda outs=None: tg.tg_norm_residual_bwd(i["H"], i["B"], i["B"], i["H"], i["w_post"], i["w_pre"], rb, rh,
+                                                     outs=outs)
+    want = call()
+    outs = {k: torch.empty_like(v) for k, v in want.items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(outs)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(call())
+        graph.replay()
+    bwd_case(900, 4096, "channel", BF, F32, 1.0)  # a larger workspace on the current stream
+    graph.replay()
+    torch.cuda.synchronize()
+    for g in got + [outs]:
+        assert all(torch.equal(g[k], want[k]) for k in want)
