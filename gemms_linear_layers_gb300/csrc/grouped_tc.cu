@@ -358,7 +358,6 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
     tc_fence_before();
   }
   pdl_wait();
-  pdl_trigger();
   if (warp == 2) gt_build<OP>(args, tab, s_plan);
   __syncthreads();
   // both CTAs' barriers are initialised before either signals the other's
@@ -704,6 +703,10 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
+  // Only now: a following kernel's CTAs could not run beside this one's shared
+  // memory anyway, and while they waited they would hold SMs that pairs of this
+  // launch may still have to be placed on.
+  pdl_trigger();
   // neither CTA leaves (or frees tensor memory) while the other may still
   // read its shared memory, write its tensor memory or arrive on its barriers
   cluster_sync_all();
