@@ -746,26 +746,37 @@ __global__ void __launch_bounds__(256) grouped_sum_kernel(const float* parts, vo
 
 // Rows of `cols` 16-bit elements copied to rows of `pitch` (a multiple of 8)
 // elements, the rest zero: what TMA needs of an operand whose rows are no
-// multiple of 16 bytes or whose base is not 16-byte aligned.
-__global__ void grouped_pitch_kernel(const uint16_t* src, uint16_t* dst, long long rows, int cols, int pitch) {
+// multiple of 16 bytes or whose base is not 16-byte aligned.  Both operands of
+// a call in one launch.
+struct PitchCopy {
+  const uint16_t* src;
+  uint16_t* dst;
+  long long words;  // of 16 bytes to write
+  int cols, pitch;
+};
+__global__ void __launch_bounds__(256) grouped_pitch_kernel(const PitchCopy a, const PitchCopy b) {
   pdl_wait();
   pdl_trigger();
-  const int per = pitch / 8;
-  const long long n = rows * per;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < a.words + b.words;
        i += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const long long r = i / per;
-    const int c = static_cast<int>(i - r * per) * 8;
-    const uint16_t* s = src + r * cols + c;
-    uint16_t v[8];
+    const PitchCopy& p = i < a.words ? a : b;
+    const long long k = i < a.words ? i : i - a.words;
+    const int per = p.pitch / 8;
+    const long long r = k / per;
+    const int c = static_cast<int>(k - r * per) * 8;
+    const uint16_t* s = p.src + r * p.cols + c;
+    uint32_t o[4];
+    if (c + 8 <= p.cols && (reinterpret_cast<uintptr_t>(s) & 3) == 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? s[j] : static_cast<uint16_t>(0);
-    uint4 o;
-    o.x = v[0] | static_cast<uint32_t>(v[1]) << 16;
-    o.y = v[2] | static_cast<uint32_t>(v[3]) << 16;
-    o.z = v[4] | static_cast<uint32_t>(v[5]) << 16;
-    o.w = v[6] | static_cast<uint32_t>(v[7]) << 16;
-    *reinterpret_cast<uint4*>(dst + r * pitch + c) = o;
+      for (int j = 0; j < 4; ++j) o[j] = reinterpret_cast<const uint32_t*>(s)[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = c + 2 * j < p.cols ? s[2 * j] : 0, hi = c + 2 * j + 1 < p.cols ? s[2 * j + 1] : 0;
+        o[j] = lo | hi << 16;
+      }
+    }
+    *reinterpret_cast<uint4*>(p.dst + r * p.pitch + c) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
@@ -775,13 +786,13 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // Ranges of every tile's reduction: more than one where the tiles are at most
 // half the pairs and the reduction is long enough that a pair saves more (0.33 us
 // a block) than the sums' second pass costs.  From sizes that the host knows: the
-// tiles there can be at most (forward, input gradient), the blocks of an even
-// share (weight gradient).
+// tiles and blocks of groups of equal size.
 int ksplit_of(int op, int64_t T, int64_t E, int64_t d_out, int64_t d_in, int num_sms) {
   const int64_t M = op == G_DGRAD ? d_in : d_out, m_tiles = (M + GT_BM - 1) / GT_BM;
-  const int64_t most = op == G_WGRAD ? E * m_tiles * ((d_in + GT_BN - 1) / GT_BN) : m_tiles * ((E < T ? E : T) + T / GT_BN);
+  const int64_t groups = E < T ? E : T, share = (T + groups - 1) / groups;
+  const int64_t tiles = m_tiles * (op == G_WGRAD ? E * ((d_in + GT_BN - 1) / GT_BN) : groups * ((share + GT_BN - 1) / GT_BN));
   const int64_t kb = op == G_WGRAD ? T / (GT_BK * E) : ((op == G_FWD ? d_in : d_out) + GT_BK - 1) / GT_BK;
-  int64_t s = num_sms / 2 / (most < 1 ? 1 : most);
+  int64_t s = num_sms / 2 / tiles;
   if (s > 8) s = 8;
   return s > 1 && kb - kb / s >= GT_SPLIT_SAVES ? static_cast<int>(s) : 1;
 }
@@ -926,15 +937,17 @@ cudaError_t grouped_launch(const GroupedCall& call, size_t* need) {
   *need = used;
   if (used > 0 && (g.ws == nullptr || g.ws_bytes < used || reinterpret_cast<uintptr_t>(g.ws) % 16)) return cudaSuccess;
   *need = 0;
-  for (int i = 0; i < 2; ++i) {
-    if (!staged[i]) continue;
-    const int64_t words = ops[i].rows * (pitch[i] / 8);
-    int64_t grid = (words + 255) / 256;
+  if (staged[0] || staged[1]) {
+    PitchCopy copy[2] = {};
+    for (int i = 0; i < 2; ++i)
+      if (staged[i])
+        copy[i] = {static_cast<const uint16_t*>(ops[i].p), static_cast<uint16_t*>(const_cast<void*>(p[i])),
+                   static_cast<long long>(ops[i].rows * (pitch[i] / 8)), static_cast<int>(ops[i].cols),
+                   static_cast<int>(pitch[i])};
+    int64_t grid = (copy[0].words + copy[1].words + 255) / 256;
     if (grid > 8 * g.num_sms) grid = 8 * g.num_sms;
-    const cudaError_t e = launch_k(grouped_pitch_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, g.stream,
-                                   static_cast<const uint16_t*>(ops[i].p), static_cast<uint16_t*>(const_cast<void*>(p[i])),
-                                   static_cast<long long>(ops[i].rows), static_cast<int>(ops[i].cols),
-                                   static_cast<int>(pitch[i]));
+    const cudaError_t e =
+        launch_k(grouped_pitch_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, g.stream, copy[0], copy[1]);
     if (e != cudaSuccess) return e;
   }
   switch (g.op) {
