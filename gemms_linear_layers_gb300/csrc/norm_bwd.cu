@@ -13,10 +13,10 @@
 // second mean is taken from sums that do not wait for the first (q and e
 // below), so a row costs one exchange between its threads, not two.
 //
-// Measured: 8,192 x 2,304 bf16 with an FP32 stream 76 us, 4.4 TB/s, with a bf16
-// one 57 us, 4.0 TB/s (53 % of the issue slots: what an element costs in
+// Measured: 8,192 x 2,304 bf16 with an FP32 stream 72 us, 4.7 TB/s, with a bf16
+// one 55 us, 4.1 TB/s (half of the issue slots: what an element costs in
 // conversions and FP32 arithmetic, and the chain of a row, stand before HBM);
-// 16,384 x 576 41 us; 8,192 x 2,300 81 us; 2,048 x 576 15 us.
+// 16,384 x 576 39 us; 8,192 x 2,300 77 us; 2,048 x 576 15 us.
 #include "norm_residual.cuh"
 
 namespace tg {
@@ -51,7 +51,9 @@ __global__ void __launch_bounds__(bwd_threads(EL, VPT), 1) norm_bwd_kernel(const
   const int d = a.d;
   const float inv_d = 1.f / static_cast<float>(d);
   const bool full = EL && a.gate_kind == GATE_FULL, channel = EL && a.gate_kind == GATE_CHANNEL;
-  const Ring ring = ring_of(ring_smem, VPT * (2 * Pack<RES>::WORDS + (full ? 3 : 2) * Pack<IN>::WORDS));
+  const int ring_words = VPT * (2 * Pack<RES>::WORDS + (full ? 3 : 2) * Pack<IN>::WORDS);
+  const Ring ring = ring_of(ring_smem, ring_words);
+  if (RING) ring_clear(ring, ring_words, D);
   pdl_wait();
   pdl_trigger();
   // rows: those congruent to `cls` modulo a.classes, dealt to the teams of the CTAs with that class in turn

@@ -32,7 +32,9 @@ __global__ void __launch_bounds__(fwd_threads(VPT)) norm_fwd_kernel(const Args a
   const int d = a.d;
   const float inv_d = 1.f / static_cast<float>(d);
   const bool full = a.gate_kind == GATE_FULL, channel = a.gate_kind == GATE_CHANNEL;
-  const Ring ring = ring_of(ring_smem, VPT * (Pack<RES>::WORDS + (full ? 2 : 1) * Pack<IN>::WORDS));
+  const int ring_words = VPT * (Pack<RES>::WORDS + (full ? 2 : 1) * Pack<IN>::WORDS);
+  const Ring ring = ring_of(ring_smem, ring_words);
+  if (RING) ring_clear(ring, ring_words, D);
   pdl_wait();
   pdl_trigger();
   // rows: those congruent to `cls` modulo a.classes, dealt to the teams of the CTAs with that class in turn

@@ -249,26 +249,31 @@ __device__ __forceinline__ uint4 read16(uint32_t at) {
                : "memory");
   return x;
 }
+// Words of columns past the row's end are never copied: they are made zeros
+// once, so that reading needs no test.
+__device__ __forceinline__ void ring_clear(const Ring& r, int words, int stages) {
+  for (int i = 0; i < words * stages; ++i)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(r.base + i * r.word), "r"(0) : "memory");
+  __syncthreads();
+}
 template <typename T, int FEED>
 __device__ __forceinline__ Pack<T> ring_read(const Ring& r, int stage, int& w, const Cols<FEED>& c, int d) {
-  Pack<T> v = zeros<T>();
+  Pack<T> v;
   const uint32_t at = r.base + stage * r.stage + w * r.word;
   uint4* x = reinterpret_cast<uint4*>(&v);
-  if (c.first < d) {
-    if constexpr (sizeof(T) == 2) {
-      x[0] = read16(at);
-    } else {
-      // words 2 lane and 2 lane + 1 of the warp's 64
-      const int lane = threadIdx.x & 31, k = 2 * lane & 31, flip = (k >> 3) & 1;
-      const uint32_t plane = at - 16 * lane + (lane >> 4) * r.word;
-      x[0] = read16(plane + 16 * (k ^ flip));
-      x[1] = read16(plane + 16 * ((k + 1) ^ flip));
-    }
-    if (c.edge(d)) {
+  if constexpr (sizeof(T) == 2) {
+    x[0] = read16(at);
+  } else {
+    // words 2 lane and 2 lane + 1 of the warp's 64
+    const int lane = threadIdx.x & 31, k = 2 * lane & 31, flip = (k >> 3) & 1;
+    const uint32_t plane = at - 16 * lane + (lane >> 4) * r.word;
+    x[0] = read16(plane + 16 * (k ^ flip));
+    x[1] = read16(plane + 16 * ((k + 1) ^ flip));
+  }
+  if (c.edge(d)) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c[j] < 0 || c[j] >= d) v.v[j] = from_f<T>(0.f);
-    }
+    for (int j = 0; j < 8; ++j)
+      if (c[j] < 0 || c[j] >= d) v.v[j] = from_f<T>(0.f);
   }
   w += Pack<T>::WORDS;
   return v;
