@@ -1631,11 +1631,27 @@ tg_status tg_attn_bwd(const void* Q, const void* K, const void* V, const void* d
 // rows stay below 2^31 with the kernels' tiles added
 static const int64_t kMaxRows = (int64_t(1) << 31) - 1024;
 
+// three sizes below 2^31 whose product may not fit 64 bits: at most 2^48 weights
+static bool grouped_sizes_ok(int64_t E, int64_t d_out, int64_t d_in) {
+  const int64_t most = int64_t(1) << 48;
+  return d_in == 0 || E * d_out <= most / d_in;
+}
+
+// the largest workspace of the products first..last
+static size_t grouped_workspace(int first, int last, int64_t T, int64_t E, int64_t d_out, int64_t d_in, bool any_base,
+                                int sms) {
+  if (T > kMaxRows || E > kMaxDim || d_out > kMaxDim || d_in > kMaxDim || !grouped_sizes_ok(E, d_out, d_in))
+    return SIZE_MAX;
+  size_t most = 0;
+  for (int op = first; op <= last; ++op) most = std::max(most, grouped_ws_bytes(op, T, E, d_out, d_in, any_base, sms));
+  return most;
+}
+
 static tg_status run_grouped(int op, const char* name, const void* A, const void* B, const int32_t* offsets, void* C,
                              int64_t T, int64_t E, int64_t d_out, int64_t d_in, tg_dtype in, tg_dtype out, void* ws,
                              size_t ws_bytes, void* stream) {
   TG_TRY(check_common(in, out, {T, E, d_out, d_in}));
-  if (T > kMaxRows) return TG_ERR_INVALID_ARG;
+  if (T > kMaxRows || !grouped_sizes_ok(E, d_out, d_in)) return TG_ERR_INVALID_ARG;
   const bool wgrad = op == 2;
   TG_TRY(check_ptr(A, wgrad ? T * d_out : E * d_out * d_in, 2));
   TG_TRY(check_ptr(B, T * (op == 1 ? d_out : d_in), 2));
@@ -1830,10 +1846,12 @@ tg_status tg_norm_residual_bwd(const void* dH_out, const void* dN, const void* B
 }
 
 // ------------------------------------------- global gradient norm and clipping
+static const int64_t kMaxTensors = 1 << 20;
+
 static tg_status run_grad(const char* name, const void* const* grads, void* const* outs, const int64_t* numels,
                           const int32_t* dtypes, int64_t n, float max_norm, float* norm, void* ws, size_t ws_bytes,
                           void* stream) {
-  if (n < 0 || n > (1 << 20) || std::isnan(max_norm) || max_norm < 0.f) return TG_ERR_INVALID_ARG;
+  if (n < 0 || n > kMaxTensors || std::isnan(max_norm) || max_norm < 0.f) return TG_ERR_INVALID_ARG;
   if (n > 0 && (grads == nullptr || numels == nullptr || dtypes == nullptr)) return TG_ERR_INVALID_ARG;
   TG_TRY(check_ptr(norm, 1, 4));
   for (int64_t i = 0; i < n; ++i) {
@@ -1904,16 +1922,13 @@ size_t tg_workspace_size(tg_op op, int64_t d0, int64_t d1, int64_t d2, int64_t d
     case TG_OP_ATTN_BWD: return d2 == 64 ? attn_bwd_ws_bytes(d0, d1) : SIZE_MAX;
     case TG_OP_GEMM_FWD_LORA: return layer_lora_ws(LAYOUT_NT, d0, d1, d2, d3, in, out, ctx->sms);
     case TG_OP_GEMM_DGRAD_LORA: return layer_lora_ws(LAYOUT_NN, d0, d2, d1, d3, in, out, ctx->sms);
-    case TG_OP_GROUPED_FWD: return grouped_ws_bytes(0, d0, d1, d2, d3, false, ctx->sms);
-    case TG_OP_GROUPED_DGRAD: return grouped_ws_bytes(1, d0, d1, d2, d3, false, ctx->sms);
-    case TG_OP_GROUPED_WGRAD: return grouped_ws_bytes(2, d0, d1, d2, d3, false, ctx->sms);
-    case TG_OP_GROUPED_UNALIGNED: {
-      size_t most = 0;
-      for (int k = 0; k < 3; ++k) most = std::max(most, grouped_ws_bytes(k, d0, d1, d2, d3, true, ctx->sms));
-      return most;
-    }
-    case TG_OP_NORM_RESIDUAL_BWD: return norm_residual_bwd_ws_bytes(d0, d1, ctx->sms);
-    case TG_OP_GRAD_CLIP: return grad_norm_ws_bytes(d0, ctx->sms);
+    case TG_OP_GROUPED_FWD: return grouped_workspace(0, 0, d0, d1, d2, d3, false, ctx->sms);
+    case TG_OP_GROUPED_DGRAD: return grouped_workspace(1, 1, d0, d1, d2, d3, false, ctx->sms);
+    case TG_OP_GROUPED_WGRAD: return grouped_workspace(2, 2, d0, d1, d2, d3, false, ctx->sms);
+    case TG_OP_GROUPED_UNALIGNED: return grouped_workspace(0, 2, d0, d1, d2, d3, true, ctx->sms);
+    case TG_OP_NORM_RESIDUAL_BWD:
+      return d0 <= kMaxDim && d1 <= NORM_MAX_D ? norm_residual_bwd_ws_bytes(d0, d1, ctx->sms) : SIZE_MAX;
+    case TG_OP_GRAD_CLIP: return d0 <= kMaxTensors ? grad_norm_ws_bytes(d0, ctx->sms) : SIZE_MAX;
     case TG_OP_BMM_ATTN: {
       GemmCall g;
       if (!attn_call(static_cast<tg_attn_op>(d0), nullptr, nullptr, nullptr, d1, d2, d3, in, out, nullptr, 0,

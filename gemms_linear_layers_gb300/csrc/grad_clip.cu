@@ -225,8 +225,7 @@ template <int N>
 __global__ void __launch_bounds__(GC_THREADS) grad_scale_kernel(const __grid_constant__ GradTable<N> t, const double* part,
                                                                 int parts, float max_norm, int in_place, float* norm) {
   __shared__ float factor;
-  pdl_wait();
-  pdl_trigger();
+  pdl_wait();  // no early trigger: there are more CTAs than fit at once
   if (threadIdx.x < 32) {
     const double total = norm_of(part, parts);
     if (threadIdx.x == 0) {

@@ -283,8 +283,7 @@ __global__ void __launch_bounds__(1024) norm_cols_kernel(const float* part, int 
   __shared__ float s[32][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   int i = blockIdx.x * 32 + x;
-  pdl_wait();
-  pdl_trigger();
+  pdl_wait();  // no early trigger: wide rows make more CTAs than fit at once
   float v = 0.f;
   if (i < sums * d) {
 #pragma unroll 5

@@ -25,7 +25,8 @@ def test_grouped_products_refuse(lib, fn):
     def call(a=EVEN, b=EVEN, off=EVEN, c=EVEN, T=8, E=2, o=8, i=8, din=B.TG_BF16, dout=B.TG_BF16):
         return f(a, b, off, c, T, E, o, i, din, dout, NULL, 0, NULL)
 
-    for bad in ({"T": -1}, {"E": -1}, {"o": -8}, {"i": 1 << 31}, {"T": (1 << 31) - 1}):
+    for bad in ({"T": -1}, {"E": -1}, {"o": -8}, {"i": 1 << 31}, {"T": (1 << 31) - 1},
+                {"E": 1 << 30, "o": 1 << 30, "i": 1 << 30}, {"E": 1 << 20, "o": 1 << 20, "i": 512}):
         assert call(**bad) == 1, bad
     for bad in ({"a": NULL}, {"b": NULL}, {"off": NULL}, {"c": NULL}):
         assert call(**bad) == 1, bad
