@@ -14,9 +14,9 @@
 // below), so a row costs one exchange between its threads, not two.
 //
 // Measured: 8,192 x 2,304 bf16 with an FP32 stream 72 us, 4.7 TB/s, with a bf16
-// one 55 us, 4.1 TB/s (half of the issue slots: what an element costs in
+// one 55 us, 4.1 TB/s (53 % of the issue slots, counted at 76 us: what an element costs in
 // conversions and FP32 arithmetic, and the chain of a row, stand before HBM);
-// 16,384 x 576 39 us; 8,192 x 2,300 77 us; 2,048 x 576 15 us.
+// 16,384 x 576 39 us; 8,192 x 2,300 with a bf16 stream 78 us; 2,048 x 576 15 us.
 #include "norm_residual.cuh"
 
 namespace tg {
