@@ -36,9 +36,9 @@
 // (weights, or the results of the weight gradient) below.  Measured: one group
 // of 4,096 rows, 5,760 -> 2,304: 1,830 / 1,790 / 1,760 TFLOP/s forward / input
 // gradient / weight gradient; 16,384 rows over 64 experts, 2,304 -> 5,760: 335
-// to 349 us, up to 1,300 TFLOP/s and 5.9 TB/s; 64 rows over 8 experts: 35 us, 6 TB/s; 8 uneven
+// to 349 us, up to 1,290 TFLOP/s and 5.9 TB/s; 64 rows over 8 experts: 35 us, 6 TB/s; 8 uneven
 // groups of 4,096 rows: 83 to 100 us input gradient (162 tiles for 76 pairs), 80 to 90 us
-// weight gradient (the power limit sets the clocks); one row of one small expert: 4.2 us.
+// weight gradient (ranges over GPUs and sessions); one row of one small expert: 4.2 us.
 #include <cuda.h>
 #include <stdio.h>
 
