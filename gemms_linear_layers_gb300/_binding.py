@@ -494,16 +494,22 @@ def _raw_stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
-# Workspaces of calls on the current stream, kept by (device, stream): an
-# allocation a call took a quarter of a small call's host time.  Calls on one
-# stream use theirs one after the other.  Not kept: large ones, those of a call
-# that is being captured (a graph outlives them) and of a caller's own stream.
-_kept = {}
+# Workspaces of calls on the current stream, kept by each host thread for each
+# (device, stream): an allocation a call took a quarter of a small call's host
+# time.  A thread's calls on one stream use its buffer one after the other.  Two
+# threads never share one: a call is several launches that pass data through its
+# workspace, and another thread's launches on the same stream may land between
+# them.  As with any memory of torch's allocator, work on a stream made outside
+# torch has to be finished before that stream is destroyed.  Not kept: large
+# ones, those of a call that is being captured (a graph outlives them) and of a
+# caller's own stream.
+_kept = threading.local()
 _KEEP_BYTES = 32 << 20
 
 
 def _scratch(op, dims, din, dout, ws, device, stream, raw):
-    """(address, bytes, buffer to hand to _keep or None) of a call's workspace; raw: the stream's handle."""
+    """(address, bytes, buffer) of a call's workspace; raw: the stream's handle.  The caller holds the buffer until
+    the call has returned (a kept one may be replaced meanwhile) and hands it to _keep."""
     n = (_lib or lib()).tg_workspace_size(op, *dims, din, dout)
     if n == 0 or n == SIZE_MAX:  # SIZE_MAX: sizes or types that the call itself will refuse
         return 0, 0, None
@@ -512,12 +518,13 @@ def _scratch(op, dims, din, dout, ws, device, stream, raw):
     if stream is not None or n > _KEEP_BYTES or torch.cuda.is_current_stream_capturing():
         buf = torch.empty(n, dtype=torch.uint8, device=device)
         return buf.data_ptr(), n, buf
+    kept = _kept.__dict__
     key = (device.index, raw)
-    kept = _kept.get(key)
-    if kept is None or kept[1] < n:
+    mine = kept.get(key)
+    if mine is None or mine[1] < n:
         buf = torch.empty(max(n, 1 << 20), dtype=torch.uint8, device=device)
-        kept = _kept[key] = (buf.data_ptr(), buf.numel(), buf)
-    return kept[0], kept[1], None
+        mine = kept[key] = (buf.data_ptr(), buf.numel(), buf)
+    return mine
 
 
 def _like(t, name, shape, dtype, device):
@@ -549,8 +556,7 @@ def _grouped(name, op, A, B, W_shape, offsets, rows, out_arg, out_shape, out_nam
     status = getattr(_lib or lib(), name)(a, b, off, c, rows, E, d_out, d_in, din, dout, wp, wn, raw)
     if status:
         raise TGError(status, name)
-    if keep is not None:
-        _keep(keep, stream)
+    _keep(keep, stream)
     return C
 
 
@@ -669,8 +675,7 @@ def tg_norm_residual_bwd(dH_out, dN, B, H_out, w_post, w_pre, rstd_b, rstd_h, ga
                                                   dg, T, d, res_scale, din, _DT.get(rt, -1), dout, wsp, wsn, raw)
     if status:
         raise TGError(status, "tg_norm_residual_bwd")
-    if keep is not None:
-        _keep(keep, stream)
+    _keep(keep, stream)
     return res
 
 
@@ -725,8 +730,7 @@ def _grads(name, grads, outs, max_norm, norm, ws, stream):
         status = (_lib or lib()).tg_grad_clip(g.pointers, o.pointers, g.numels, g.dtypes, n, max_norm, at, wp, wn, s)
     if status:
         raise TGError(status, name)
-    if keep is not None:
-        _keep(keep, stream)
+    _keep(keep, stream)
     return norm
 
 

@@ -1,6 +1,7 @@
 """Host-side checks of the expert-block operators (no GPU): arguments that the C entry points refuse before any
 device work, and the binding's own checks."""
 import ctypes
+import threading
 
 import pytest
 import torch
@@ -95,3 +96,41 @@ def test_exported():
     for n in B.SIGNATURES:
         if n.startswith(("tg_grouped", "tg_norm", "tg_grad")):
             assert n in pkg.__all__, n
+
+
+class Sizes:
+    """Stands for the library in `_scratch`: workspaces of the given sizes, one after the other."""
+
+    def __init__(self, *sizes):
+        self.sizes = list(sizes)
+
+    def tg_workspace_size(self, *_):
+        return self.sizes.pop(0) if len(self.sizes) > 1 else self.sizes[0]
+
+
+def scratch(monkeypatch, *sizes):
+    monkeypatch.setattr(B, "_lib", Sizes(*sizes))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    return lambda raw=7, stream=None: B._scratch(B.TG_OP_NORM_RESIDUAL_BWD, (1, 1, 0, 0), 0, 0, None, torch.device("cpu"),
+                                                 stream, raw)
+
+
+def test_threads_on_one_stream_have_workspaces_of_their_own(monkeypatch):
+    """A call's launches pass data through its workspace, and another thread's launches on the same stream may land
+    between them."""
+    take = scratch(monkeypatch, 4096)
+    here, there = take(), []
+    t = threading.Thread(target=lambda: there.append(take()))
+    t.start()
+    t.join()
+    assert here[0] != there[0][0]
+    assert take()[0] == here[0]  # the same thread's next call on the stream: the same buffer
+    assert take(raw=8)[0] != here[0]
+
+
+def test_a_workspace_outlives_its_replacement_by_a_larger_one(monkeypatch):
+    """The buffer goes with the call until its launches are queued, whatever replaces it among the kept ones."""
+    take = scratch(monkeypatch, 4096, 4 << 20)
+    address, size, buf = take()
+    assert size >= 4096 and buf.data_ptr() == address
+    assert take()[0] != address

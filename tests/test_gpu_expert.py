@@ -1,6 +1,7 @@
 """The expert-block operators against their 64-bit definitions: products grouped by expert, the norms with gate and
 residual scale, and the global gradient norm with clipping."""
 import math
+import threading
 
 import pytest
 import torch
@@ -566,3 +567,50 @@ def test_workspaces_kept_by_the_binding():
     torch.cuda.synchronize()
     for g in got + [outs]:
         assert all(torch.equal(g[k], want[k]) for k in want)
+
+
+def test_threads_on_one_stream():
+    """Host threads that call on one stream at once, with workspaces that grow on the way: every result is that of
+    the call alone, bit for bit."""
+    def clip(k, sizes):
+        grads = [randn((n,), 0.5, F32, f"{k}{n}") for n in sizes]
+        return lambda: (lambda outs: [tg.tg_grad_clip(grads, 0.1, outs=outs), *outs])([torch.empty_like(g) for g in grads])
+
+    def norm(T, d, tag):
+        i = norm_inputs(T, d, "channel", BF, BF, tag)
+        rb, rh = torch.ones(T, device="cuda"), torch.full((T,), 0.5, device="cuda")
+        return lambda: list(tg.tg_norm_residual_bwd(i["H"], i["B"], i["B"], i["H"], i["w_post"], i["w_pre"], rb, rh,
+                                                    gate=i["gate"]).values())
+
+    def product(op, sizes, d_in, d_out):
+        X, W, dY, off = grouped_inputs(sizes, 0, 0, d_in, d_out, BF)
+        o = off.cuda()
+        return lambda: [tg.tg_grouped_wgrad(dY, X, o) if op == "wgrad" else tg.tg_grouped_fwd(X, W, o)]
+
+    jobs = [[norm(40, 72, "a"), clip("a", (5000, 301)), product("wgrad", [4096], 72, 64), norm(300, 576, "b"),
+             product("fwd", [9, 30], 33, 101)],
+            [norm(41, 80, "c"), clip("b", (70000, 9)), product("wgrad", [5000], 576, 264), norm(700, 4096, "d"),
+             product("fwd", [70, 2], 101, 33)]]
+    want = [[f() for f in fs] for fs in jobs]
+    torch.cuda.synchronize()
+    got, failed, gate = [[], []], [], threading.Barrier(2)
+
+    def work(k):
+        try:
+            gate.wait()
+            for _ in range(60):
+                got[k].append([f() for f in jobs[k]])
+        except Exception as e:  # shown below: an exception in a thread is not the test's
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for k in range(2):
+        for run in got[k]:
+            for a, b in zip(run, want[k]):
+                assert all(torch.equal(x, y) for x, y in zip(a, b))
