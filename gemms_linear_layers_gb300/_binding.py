@@ -494,6 +494,23 @@ def _raw_stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory that a call on `stream` (None: the current one) writes.  It is taken from that stream's: the current
+    stream's may still be read by work queued there earlier, for which the other does not wait."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _new(shape, dtype, device, stream):
+    """An output of a call on `stream`, for the caller to go on with on the current one."""
+    t = _empty(shape, dtype, device, stream)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 # Workspaces of calls on the current stream, kept by each host thread for each
 # (device, stream): an allocation a call took a quarter of a small call's host
 # time.  A thread's calls on one stream use its buffer one after the other.  Two
@@ -509,14 +526,14 @@ _KEEP_BYTES = 32 << 20
 
 def _scratch(op, dims, din, dout, ws, device, stream, raw):
     """(address, bytes, buffer) of a call's workspace; raw: the stream's handle.  The caller holds the buffer until
-    the call has returned (a kept one may be replaced meanwhile) and hands it to _keep."""
+    the call has returned: a kept one may be replaced meanwhile."""
     n = (_lib or lib()).tg_workspace_size(op, *dims, din, dout)
     if n == 0 or n == SIZE_MAX:  # SIZE_MAX: sizes or types that the call itself will refuse
         return 0, 0, None
     if ws is not None and ws.numel() * ws.element_size() >= n:
         return ws.data_ptr(), ws.numel() * ws.element_size(), None
     if stream is not None or n > _KEEP_BYTES or torch.cuda.is_current_stream_capturing():
-        buf = torch.empty(n, dtype=torch.uint8, device=device)
+        buf = _empty(n, torch.uint8, device, stream)
         return buf.data_ptr(), n, buf
     kept = _kept.__dict__
     key = (device.index, raw)
@@ -543,7 +560,7 @@ def _grouped(name, op, A, B, W_shape, offsets, rows, out_arg, out_shape, out_nam
         raise ValueError("the operands must be on one device")
     off = _like(offsets, "offsets", (E + 1,), torch.int32, dev)
     if out_arg is None:
-        C = torch.empty(out_shape, dtype=out_dtype or dt, device=dev)
+        C = _new(out_shape, out_dtype or dt, dev, stream)
         c = C.data_ptr()
     else:
         C = out_arg
@@ -551,12 +568,11 @@ def _grouped(name, op, A, B, W_shape, offsets, rows, out_arg, out_shape, out_nam
     din, dout = _DT.get(dt, -1), _DT.get(C.dtype, -1)
     a, b = A.data_ptr(), B.data_ptr()
     raw = _raw_stream(stream, dev)
-    wp, wn, keep = _scratch(TG_OP_GROUPED_UNALIGNED if (a | b) & 15 else op, (rows, E, d_out, d_in), din, dout, ws, dev,
+    wp, wn, held = _scratch(TG_OP_GROUPED_UNALIGNED if (a | b) & 15 else op, (rows, E, d_out, d_in), din, dout, ws, dev,
                             stream, raw)
     status = getattr(_lib or lib(), name)(a, b, off, c, rows, E, d_out, d_in, din, dout, wp, wn, raw)
     if status:
         raise TGError(status, name)
-    _keep(keep, stream)
     return C
 
 
@@ -609,11 +625,11 @@ def _gate(gate, T, d, dtype, device):
     return kind, shape, _like(gate, "gate", shape, dtype, device)
 
 
-def _result(res, outs, name, shape, dtype, device):
+def _result(res, outs, name, shape, dtype, device, stream):
     """Address of an output: the caller's, or a new one; kept in res."""
     t = outs.get(name) if outs else None
     if t is None:
-        t = res[name] = torch.empty(shape, dtype=dtype, device=device)
+        t = res[name] = _new(shape, dtype, device, stream)
         return t.data_ptr()
     res[name] = t
     return _like(t, name, shape, dtype, device)
@@ -638,8 +654,8 @@ def tg_norm_residual_fwd(B, H, w_post, w_pre, gate=None, res_scale=1.0, eps=1e-6
     wq, wp = _like(w_post, "w_post", (d,), dt, dev), _like(w_pre, "w_pre", (d,), dt, dev)
     kind, _, g = _gate(gate, T, d, dt, dev)
     res = {}
-    ho, n = _result(res, outs, "H", shape, rt, dev), _result(res, outs, "N", shape, dt, dev)
-    rb, rh = (_result(res, outs, k, (T,), torch.float32, dev) for k in ("rstd_b", "rstd_h"))
+    ho, n = _result(res, outs, "H", shape, rt, dev, stream), _result(res, outs, "N", shape, dt, dev, stream)
+    rb, rh = (_result(res, outs, k, (T,), torch.float32, dev, stream) for k in ("rstd_b", "rstd_h"))
     status = (_lib or lib()).tg_norm_residual_fwd(B.data_ptr(), h, wq, wp, g, kind, ho, n, rb, rh, T, d, res_scale, eps,
                                                   _DT.get(dt, -1), _DT[rt] if rt in _DT else -1,
                                                   _raw_stream(stream, dev))
@@ -665,17 +681,17 @@ def tg_norm_residual_bwd(dH_out, dN, B, H_out, w_post, w_pre, rstd_b, rstd_h, ga
     kind, gshape, g = _gate(gate, T, d, dt, dev)
     ot = out_dtype or (outs["dw_post"].dtype if outs and "dw_post" in outs else dt)
     res = {}
-    db, dh = _result(res, outs, "dB", shape, dt, dev), _result(res, outs, "dH", shape, rt, dev)
-    dwq, dwp = _result(res, outs, "dw_post", (d,), ot, dev), _result(res, outs, "dw_pre", (d,), ot, dev)
-    dg = 0 if kind == TG_GATE_NONE else _result(res, outs, "dgate", gshape, dt if kind == TG_GATE_FULL else ot, dev)
+    db, dh = _result(res, outs, "dB", shape, dt, dev, stream), _result(res, outs, "dH", shape, rt, dev, stream)
+    dwq, dwp = (_result(res, outs, k, (d,), ot, dev, stream) for k in ("dw_post", "dw_pre"))
+    gt = dt if kind == TG_GATE_FULL else ot
+    dg = 0 if kind == TG_GATE_NONE else _result(res, outs, "dgate", gshape, gt, dev, stream)
     din, dout = _DT.get(dt, -1), _DT.get(ot, -1)
     raw = _raw_stream(stream, dev)
-    wsp, wsn, keep = _scratch(TG_OP_NORM_RESIDUAL_BWD, (T, d, 0, 0), din, dout, ws, dev, stream, raw)
+    wsp, wsn, held = _scratch(TG_OP_NORM_RESIDUAL_BWD, (T, d, 0, 0), din, dout, ws, dev, stream, raw)
     status = (_lib or lib()).tg_norm_residual_bwd(dho, dn, B.data_ptr(), ho, wq, wp, g, kind, rb, rh, db, dh, dwq, dwp,
                                                   dg, T, d, res_scale, din, _DT.get(rt, -1), dout, wsp, wsn, raw)
     if status:
         raise TGError(status, "tg_norm_residual_bwd")
-    _keep(keep, stream)
     return res
 
 
@@ -717,10 +733,10 @@ def _grads(name, grads, outs, max_norm, norm, ws, stream):
     if dev is None:
         dev = norm.device if norm is not None else torch.device("cuda", torch.cuda.current_device())
     if norm is None:
-        norm = torch.empty(1, dtype=torch.float32, device=dev)
+        norm = _new(1, torch.float32, dev, stream)
     at = _like(norm, "norm", (1,), torch.float32, dev)
     s = _raw_stream(stream, dev)
-    wp, wn, keep = _scratch(TG_OP_GRAD_CLIP, (n, 0, 0, 0), TG_F32, TG_F32, ws, dev, stream, s)
+    wp, wn, held = _scratch(TG_OP_GRAD_CLIP, (n, 0, 0, 0), TG_F32, TG_F32, ws, dev, stream, s)
     if name == "tg_grad_norm":
         status = (_lib or lib()).tg_grad_norm(g.pointers, g.numels, g.dtypes, n, at, wp, wn, s)
     else:
@@ -730,7 +746,6 @@ def _grads(name, grads, outs, max_norm, norm, ws, stream):
         status = (_lib or lib()).tg_grad_clip(g.pointers, o.pointers, g.numels, g.dtypes, n, max_norm, at, wp, wn, s)
     if status:
         raise TGError(status, name)
-    _keep(keep, stream)
     return norm
 
 

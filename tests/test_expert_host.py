@@ -1,5 +1,6 @@
 """Host-side checks of the expert-block operators (no GPU): arguments that the C entry points refuse before any
 device work, and the binding's own checks."""
+import contextlib
 import ctypes
 import threading
 
@@ -10,6 +11,7 @@ import gemms_linear_layers_gb300 as tg
 from gemms_linear_layers_gb300 import _binding as B
 from gemms_linear_layers_gb300 import build
 
+BF = torch.bfloat16
 NULL, EVEN, ODD, HALF = (ctypes.c_void_p(x) for x in (0, 0x1000, 0x1001, 0x1002))
 
 
@@ -134,3 +136,41 @@ def test_a_workspace_outlives_its_replacement_by_a_larger_one(monkeypatch):
     address, size, buf = take()
     assert size >= 4096 and buf.data_ptr() == address
     assert take()[0] != address
+
+
+def test_memory_of_a_call_on_a_given_stream_is_that_streams(monkeypatch):
+    """What a call on the caller's own stream allocates comes from that stream's memory: the current stream's may
+    still be read by work queued there, which the other stream does not wait for."""
+    current, taken = ["current"], []
+
+    class Buffer:
+        def __init__(self):
+            self.used_on = []
+
+        def data_ptr(self):
+            return 0x1000
+
+        def record_stream(self, s):
+            self.used_on.append(s)
+
+    @contextlib.contextmanager
+    def enter(s):
+        current.append(s)
+        yield
+        current.pop()
+
+    def empty(*_, **__):
+        taken.append(current[-1])
+        return Buffer()
+
+    monkeypatch.setattr(torch.cuda, "stream", enter)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: current[-1])
+    monkeypatch.setattr(torch, "empty", empty)
+    take = scratch(monkeypatch, 4096)
+    take(stream="side")
+    assert taken.pop() == "side"
+    res = {}
+    B._result(res, None, "dB", (2, 3), BF, torch.device("cpu"), "side")
+    assert taken.pop() == "side" and res["dB"].used_on == ["current"]  # where the caller may go on with it
+    B._result(res, None, "dH", (2, 3), BF, torch.device("cpu"), None)
+    assert taken.pop() == "current" and res["dH"].used_on == []

@@ -614,3 +614,26 @@ def test_threads_on_one_stream():
         for run in got[k]:
             for a, b in zip(run, want[k]):
                 assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_memory_of_a_call_on_a_given_stream():
+    """A call on a stream of the caller's, which does not wait for the current one, allocates nothing that work
+    queued on the current stream still reads."""
+    i = norm_inputs(300, 4096, "channel", BF, BF)
+    rb, rh = (torch.ones(300, device="cuda") for _ in range(2))
+    call = lambda **kw: tg.tg_norm_residual_bwd(i["H"], i["B"], i["B"], i["H"], i["w_post"], i["w_pre"], rb, rh,
+                                                gate=i["gate"], **kw)
+    want = call()
+    need = tg.tg_workspace_size(17, 300, 4096, 0, 0, BF, BF)
+    side, big = torch.cuda.Stream(), torch.ones(8192, 8192, dtype=BF, device="cuda")
+    torch.cuda.synchronize()
+    read = [torch.full((n,), 3, dtype=torch.uint8, device="cuda") for n in (need, want["dB"].numel() * 2, 8192, 1 << 22)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        big @ big
+    kept = [x + 1 for x in read]  # read when the products are done; freed now
+    del read
+    got = call(stream=side)
+    torch.cuda.synchronize()
+    assert all((k == 4).all() for k in kept)
+    assert all(torch.equal(got[k], want[k]) for k in want)
