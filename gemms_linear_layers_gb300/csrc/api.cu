@@ -1628,20 +1628,19 @@ tg_status tg_attn_bwd(const void* Q, const void* K, const void* V, const void* d
 }
 
 // ------------------------------------------------- products grouped by expert
-// rows stay below 2^31 with the kernels' tiles added
-static const int64_t kMaxRows = (int64_t(1) << 31) - 1024;
-
-// three sizes below 2^31 whose product may not fit 64 bits: at most 2^48 weights
-static bool grouped_sizes_ok(int64_t E, int64_t d_out, int64_t d_in) {
-  const int64_t most = int64_t(1) << 48;
-  return d_in == 0 || E * d_out <= most / d_in;
+// Rows and widths stay below 2^31 with the kernels' tiles added, and no tensor
+// has more than 2^38 elements (512 GiB in 16 bits): the tiles of a launch of 256
+// experts are then at most 2^30 and some, which the kernels count in 32 bits.
+static bool grouped_sizes_ok(int64_t T, int64_t E, int64_t d_out, int64_t d_in) {
+  const int64_t longest = (int64_t(1) << 31) - 1024, most = int64_t(1) << 38;
+  if (T > longest || E > kMaxDim || d_out > longest || d_in > longest) return false;
+  return T * d_out <= most && T * d_in <= most && (d_in == 0 || E * d_out <= most / d_in);
 }
 
 // the largest workspace of the products first..last
 static size_t grouped_workspace(int first, int last, int64_t T, int64_t E, int64_t d_out, int64_t d_in, bool any_base,
                                 int sms) {
-  if (T > kMaxRows || E > kMaxDim || d_out > kMaxDim || d_in > kMaxDim || !grouped_sizes_ok(E, d_out, d_in))
-    return SIZE_MAX;
+  if (!grouped_sizes_ok(T, E, d_out, d_in)) return SIZE_MAX;
   size_t most = 0;
   for (int op = first; op <= last; ++op) most = std::max(most, grouped_ws_bytes(op, T, E, d_out, d_in, any_base, sms));
   return most;
@@ -1651,7 +1650,7 @@ static tg_status run_grouped(int op, const char* name, const void* A, const void
                              int64_t T, int64_t E, int64_t d_out, int64_t d_in, tg_dtype in, tg_dtype out, void* ws,
                              size_t ws_bytes, void* stream) {
   TG_TRY(check_common(in, out, {T, E, d_out, d_in}));
-  if (T > kMaxRows || !grouped_sizes_ok(E, d_out, d_in)) return TG_ERR_INVALID_ARG;
+  if (!grouped_sizes_ok(T, E, d_out, d_in)) return TG_ERR_INVALID_ARG;
   const bool wgrad = op == 2;
   TG_TRY(check_ptr(A, wgrad ? T * d_out : E * d_out * d_in, 2));
   TG_TRY(check_ptr(B, T * (op == 1 ? d_out : d_in), 2));

@@ -136,10 +136,14 @@ struct GtTab {
   int whole, cuts;  // units of the rounds before it
 };
 
-// n / d for 0 <= n < 2^24 (so many tiles of output are more than the GPU's
-// memory), by = 1 / d rounded: the integer divisions' dozens of dependent
-// instructions stood between a unit and its first copy (1,000 rows over 32 experts
-// 19.3 us with them, 17.3 without).
+// n / d for 0 <= n < 2^31, by = 1 / d rounded: the integer divisions' dozens of
+// dependent instructions stood between a unit and its first copy (1,000 rows over 32
+// experts 19.3 us with them, 17.3 without).  The estimate is off by at most 2^-22 of
+// itself (four roundings), so while the quotient is at most 2^22 its floor is off by
+// one at most.  It is an expert of 256, or a tile along the rows or columns of a result:
+// more than 2^22 of these beside two or more feature tiles would be a tensor of more
+// than 2^38 elements, which the entry points refuse; beside one, d = 1 and n < 2^24:
+// exact.
 __device__ __forceinline__ int quotient(int n, int d, float by) {
   int q = __float2int_rd(__int2float_rn(n) * by);
   const int r = n - q * d;

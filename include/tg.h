@@ -341,8 +341,8 @@ tg_status tg_bmm_attn(tg_attn_op op, const void* A, const void* B, void* C, int6
  * what rows of other experts hold never reaches an expert's results.
  * Offsets that break the rules give unspecified results, but nothing outside
  * the tensors is read or written.
- * T < 2^31 - 1024, E d_out d_in <= 2^48.  Any widths and alignments run on the tensor cores: an
- * operand whose rows are no multiple of 8 elements, or whose base is not
+ * T, d_out and d_in are at most 2^31 - 1024, a tensor has at most 2^38
+ * elements.  Any widths and alignments run on the tensor cores: an operand whose rows are no multiple of 8 elements, or whose base is not
  * 16-byte aligned, is first copied to rows that are, in `ws`.  Where there are
  * few output tiles and long reductions, these are cut into ranges whose FP32
  * sums, in `ws` too, are added in a fixed order.  Workspace:

@@ -174,3 +174,20 @@ def test_memory_of_a_call_on_a_given_stream_is_that_streams(monkeypatch):
     assert taken.pop() == "side" and res["dB"].used_on == ["current"]  # where the caller may go on with it
     B._result(res, None, "dH", (2, 3), BF, torch.device("cpu"), None)
     assert taken.pop() == "current" and res["dH"].used_on == []
+
+
+@pytest.mark.parametrize("fn", ["tg_grouped_fwd", "tg_grouped_dgrad", "tg_grouped_wgrad"])
+def test_grouped_products_refuse_what_their_tiles_cannot_count(lib, fn):
+    """Widths within a tile of 2^31 (the tile counts are 32-bit) and tensors of more than 2^38 elements; sizes at
+    the limits pass the checks of sizes (and end at the missing device or at a tensor's address)."""
+    def call(T=1, E=1, o=8, i=8):
+        return getattr(lib, fn)(EVEN, EVEN, EVEN, ODD, T, E, o, i, B.TG_BF16, B.TG_BF16, NULL, 0, NULL)
+
+    top = (1 << 31) - 1024
+    for bad in ({"o": top + 1}, {"i": top + 1}, {"o": (1 << 31) - 1}, {"i": (1 << 31) - 1}, {"T": top + 1},
+                {"E": 1 << 20, "o": 1 << 10, "i": (1 << 8) + 1}, {"T": 1 << 20, "o": (1 << 18) + 1},
+                {"T": 1 << 20, "i": (1 << 18) + 1}):
+        assert call(**bad) == 1, bad
+    for good in ({"o": top}, {"i": top}, {"T": top}, {"E": 1 << 20, "o": 1 << 10, "i": 1 << 8}, {"T": 1 << 20, "o": 1 << 18},
+                 {"T": 1 << 20, "i": 1 << 18}):
+        assert call(**good) == 3, good
