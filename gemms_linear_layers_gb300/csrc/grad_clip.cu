@@ -83,7 +83,7 @@ __device__ __forceinline__ double square_d(T v) {
   return x * x;
 }
 
-// The squares of one chunk: 16-byte words [chunk * 2048, ..) after the head;
+// The squares of one chunk: 16-byte words [chunk * 4096, ..) after the head;
 // the first chunk also takes the head and the tail.
 template <typename T>
 __device__ __forceinline__ double chunk_squares(const void* base, long long n, long long chunk) {
@@ -107,8 +107,8 @@ __device__ __forceinline__ double chunk_squares(const void* base, long long n, l
 #pragma unroll
     for (int j = 0; j < V; ++j) sum[i & 1] = fmaf(gc_f(e[j]), gc_f(e[j]), sum[i & 1]);
   }
-  const float s = sum[0] + sum[1];
-  double d = static_cast<double>(s);
+  const float s = sum[0] + sum[1];  // for the range test alone: each group goes into FP64 by itself
+  double d = static_cast<double>(sum[0]) + static_cast<double>(sum[1]);
   if (!(s >= 0x1p-90f && s <= 0x1p120f) && any != 0) {
     d = 0.0;
 #pragma unroll 1

@@ -637,3 +637,16 @@ def test_memory_of_a_call_on_a_given_stream():
     torch.cuda.synchronize()
     assert all((k == 4).all() for k in kept)
     assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=str)
+def test_clip_adds_each_group_of_squares_in_64_bits(dtype):
+    """Groups of at most 32 squares in FP32, 64 bits beyond.  The groups here are exact, 4,096^2 and 1 by turns, so
+    the norm is the correctly rounded root; were two groups joined in FP32, the ones would vanish beside 2^24 and the
+    root would fall below the middle of two FP32 values."""
+    words = torch.zeros(4096, 16 // dtype.itemsize, dtype=dtype, device="cuda")  # 64 KB, 16 bytes a row
+    words[:512, 0], words[512:1024, 0] = 4096.0, 1.0
+    total = 512 * (4096 ** 2 + 1) + 14 ** 2
+    want = torch.tensor(math.sqrt(total), dtype=F32)
+    assert want > torch.tensor(math.sqrt(total - 512), dtype=F32)
+    assert float(tg.tg_grad_norm([words, torch.full((1,), 14.0, device="cuda")])) == float(want)
