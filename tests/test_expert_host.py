@@ -6,6 +6,7 @@ import threading
 
 import pytest
 import torch
+from torch.multiprocessing.reductions import StorageWeakRef
 
 import gemms_linear_layers_gb300 as tg
 from gemms_linear_layers_gb300 import _binding as B
@@ -191,3 +192,20 @@ def test_grouped_products_refuse_what_their_tiles_cannot_count(lib, fn):
     for good in ({"o": top}, {"i": top}, {"T": top}, {"E": 1 << 20, "o": 1 << 10, "i": 1 << 8}, {"T": 1 << 20, "o": 1 << 18},
                  {"T": 1 << 20, "i": 1 << 18}):
         assert call(**good) == 3, good
+
+
+def test_a_list_whose_tensors_moved_is_refused():
+    """A laid-out list holds addresses: a tensor that was given other memory since is an error, not a write to where
+    it used to be, and that memory is held meanwhile."""
+    class OnDevice(torch.Tensor):
+        is_cuda = True
+
+    a, b = (torch.zeros(n).as_subclass(OnDevice) for n in (5, 3))
+    laid_out = tg.tg_tensor_list([a, b])
+    memory = StorageWeakRef(b.untyped_storage())
+    b.data = torch.ones(3).as_subclass(OnDevice)
+    assert not memory.expired()
+    for call in (lambda: tg.tg_grad_norm(laid_out), lambda: tg.tg_grad_clip(laid_out, 1.0),
+                 lambda: tg.tg_grad_clip(tg.tg_tensor_list([a, b]), 1.0, outs=laid_out)):
+        with pytest.raises(ValueError, match="tensor 1 "):
+            call()
