@@ -667,8 +667,8 @@ def tg_norm_residual_fwd(B, H, w_post, w_pre, gate=None, res_scale=1.0, eps=1e-6
 def tg_norm_residual_bwd(dH_out, dN, B, H_out, w_post, w_pre, rstd_b, rstd_h, gate=None, res_scale=1.0, out_dtype=None,
                          outs=None, ws=None, stream=None):
     """Gradients of <dH_out, H_out> + <dN, N> for the forward of tg_norm_residual_fwd: {"dB", "dH", "dw_post",
-    "dw_pre"} and "dgate" when there is a gate.  out_dtype (B's dtype or FP32): dw_post, dw_pre and the gradient
-    of a broadcast gate.  outs may give any of them."""
+    "dw_pre"} and "dgate" when there is a gate.  out_dtype (B's dtype or FP32; by default that of those in outs):
+    dw_post, dw_pre and the gradient of a broadcast gate.  outs may give any of them."""
     _need(B, "B", 2)
     T, d = shape = tuple(B.shape)
     dev, dt = B.device, B.dtype
@@ -679,7 +679,10 @@ def tg_norm_residual_bwd(dH_out, dN, B, H_out, w_post, w_pre, rstd_b, rstd_h, ga
     wq, wp = _like(w_post, "w_post", (d,), dt, dev), _like(w_pre, "w_pre", (d,), dt, dev)
     rb, rh = _like(rstd_b, "rstd_b", (T,), f32, dev), _like(rstd_h, "rstd_h", (T,), f32, dev)
     kind, gshape, g = _gate(gate, T, d, dt, dev)
-    ot = out_dtype or (outs["dw_post"].dtype if outs and "dw_post" in outs else dt)
+    ot = out_dtype
+    if ot is None:  # that of any output of this type that is given
+        summed = ("dw_post", "dw_pre") if kind in (TG_GATE_NONE, TG_GATE_FULL) else ("dw_post", "dw_pre", "dgate")
+        ot = next((outs[k].dtype for k in summed if outs.get(k) is not None), dt) if outs else dt
     res = {}
     db, dh = _result(res, outs, "dB", shape, dt, dev, stream), _result(res, outs, "dH", shape, rt, dev, stream)
     dwq, dwp = (_result(res, outs, k, (d,), ot, dev, stream) for k in ("dw_post", "dw_pre"))

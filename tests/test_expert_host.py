@@ -101,6 +101,10 @@ def test_exported():
             assert n in pkg.__all__, n
 
 
+class OnDevice(torch.Tensor):
+    is_cuda = True
+
+
 class Sizes:
     """Stands for the library in `_scratch`: workspaces of the given sizes, one after the other."""
 
@@ -197,9 +201,6 @@ def test_grouped_products_refuse_what_their_tiles_cannot_count(lib, fn):
 def test_a_list_whose_tensors_moved_is_refused():
     """A laid-out list holds addresses: a tensor that was given other memory since is an error, not a write to where
     it used to be, and that memory is held meanwhile."""
-    class OnDevice(torch.Tensor):
-        is_cuda = True
-
     a, b = (torch.zeros(n).as_subclass(OnDevice) for n in (5, 3))
     laid_out = tg.tg_tensor_list([a, b])
     memory = StorageWeakRef(b.untyped_storage())
@@ -209,3 +210,29 @@ def test_a_list_whose_tensors_moved_is_refused():
                  lambda: tg.tg_grad_clip(tg.tg_tensor_list([a, b]), 1.0, outs=laid_out)):
         with pytest.raises(ValueError, match="tensor 1 "):
             call()
+
+
+@pytest.mark.parametrize("given", ["dw_post", "dw_pre", "dgate"])
+def test_the_type_of_summed_gradients_follows_any_given_output(monkeypatch, given):
+    """One FP32 output given among those summed over rows: the others come in FP32 too; one that is None is new."""
+    class Library:
+        def tg_workspace_size(self, *_):
+            return 0
+
+        def tg_norm_residual_bwd(self, *args):
+            self.out_type = args[20]  # after dtypes in, res
+            return 0
+
+    library = Library()
+    monkeypatch.setattr(B, "_lib", library)
+    monkeypatch.setattr(B, "_raw_stream", lambda *_: 0)
+    dev = lambda *shape, dtype=BF: torch.zeros(shape, dtype=dtype).as_subclass(OnDevice)
+    x, w, r = dev(4, 8), dev(8), dev(4, dtype=torch.float32)
+    outs = {"dw_post": None, "dw_pre": None, "dgate": None, given: dev(8, dtype=torch.float32)}
+    got = tg.tg_norm_residual_bwd(x, x, x, x, w, w, r, r, gate=w, outs=outs)
+    assert library.out_type == B.TG_F32 and got[given] is outs[given]
+    assert all(got[k].dtype == torch.float32 for k in ("dw_post", "dw_pre", "dgate")) and got["dB"].dtype == BF
+    full = tg.tg_norm_residual_bwd(x, x, x, x, w, w, r, r, gate=x, outs={"dgate": dev(4, 8)})  # of B's type
+    assert full["dw_pre"].dtype == BF
+    with pytest.raises(ValueError):
+        tg.tg_norm_residual_bwd(x, x, x, x, w, w, r, r, gate=w, outs={**outs, "dw_post": dev(8), "dw_pre": r[:0]})
