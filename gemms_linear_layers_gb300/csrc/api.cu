@@ -1770,8 +1770,10 @@ tg_status tg_norm_residual_fwd(const void* B, const void* H, const void* w_post,
   a.res_kind = ek_of(res);
   a.num_sms = ctx->sms;
   a.stream = static_cast<cudaStream_t>(stream);
+  const char* rows = "";
+  a.rows = &rows;
   const cudaError_t e = norm_residual_fwd_launch(a);
-  record("norm_residual_fwd T=" + std::to_string(T) + " d=" + std::to_string(d) + " " +
+  record("norm_residual_fwd T=" + std::to_string(T) + " d=" + std::to_string(d) + " rows by " + rows + " " +
          (e == cudaSuccess ? "ok" : cudaGetErrorString(e)));
   return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
 }
@@ -1838,8 +1840,10 @@ tg_status tg_norm_residual_bwd(const void* dH_out, const void* dN, const void* B
   a.ws = static_cast<float*>(ws);
   a.num_sms = ctx->sms;
   a.stream = st;
+  const char* rows = "";
+  a.rows = &rows;
   const cudaError_t e = norm_residual_bwd_launch(a);
-  record("norm_residual_bwd T=" + std::to_string(T) + " d=" + std::to_string(d) + " " +
+  record("norm_residual_bwd T=" + std::to_string(T) + " d=" + std::to_string(d) + " rows by " + rows + " " +
          (e == cudaSuccess ? "ok" : cudaGetErrorString(e)));
   return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
 }

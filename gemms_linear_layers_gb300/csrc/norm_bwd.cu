@@ -327,6 +327,7 @@ int bwd_smem(const NormResidual& n, const Geo& g, int feed) {
 template <typename IN, typename RES, int VPT, int FEED, bool EL>
 cudaError_t bwd_one(const NormResidual& n, const Geo& g) {
   const Args a = to_args(n, g);
+  *n.rows = FEED_NAMES[FEED];
   auto kern = norm_bwd_kernel<IN, RES, VPT, FEED, EL>;
   const int smem = bwd_smem<IN, RES>(n, g, FEED);
   cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), smem);
@@ -356,10 +357,17 @@ cudaError_t bwd_gate(const NormResidual& n) {
   if (fit(false, FEED_RING, &g))
     return g.vpt == 1 ? bwd_one<IN, RES, 1, FEED_RING, EL>(n, g) : bwd_one<IN, RES, MANY, FEED_RING, EL>(n, g);
   g = bwd_geometry(n.T, n.d, false, n.num_sms, EL);
+  // aligned rows of one group a thread always fit the ring (216 KB at most)
   if (g.vpt == 1) return bwd_one<IN, RES, 1, FEED_SCALAR, EL>(n, g);
+  // Wider ones that do not: words of 16 bytes all the same (4,096 x 10,240 with an FP32
+  // stream 174 us, element by element 509; 4,096 x 8,192 in FP32 208 and 463).  16-bit
+  // streams always fit, and FP32 ones beside an element-wise gate on 16-bit values.
+  const bool vec = words && n.d % 8 == 0;
+  if constexpr (sizeof(RES) == 4 && (sizeof(IN) == 4 || !EL)) {
+    if (g.vpt == MANY && vec) return bwd_one<IN, RES, MANY, FEED_VEC, EL>(n, g);
+  }
   if (g.vpt == MANY) return bwd_one<IN, RES, MANY, FEED_SCALAR, EL>(n, g);
-  return words && n.d % 8 == 0 ? bwd_one<IN, RES, BWD_WIDEST, FEED_VEC, EL>(n, g)
-                               : bwd_one<IN, RES, BWD_WIDEST, FEED_SCALAR, EL>(n, g);
+  return vec ? bwd_one<IN, RES, BWD_WIDEST, FEED_VEC, EL>(n, g) : bwd_one<IN, RES, BWD_WIDEST, FEED_SCALAR, EL>(n, g);
 }
 template <typename IN, typename RES>
 cudaError_t bwd_types(const NormResidual& n) {

@@ -166,6 +166,7 @@ int fwd_smem(const NormResidual& n, const Geo& g, int feed) {
 template <typename IN, typename RES, int VPT, int FEED>
 cudaError_t fwd_one(const NormResidual& n, const Geo& g) {
   const Args a = to_args(n, g);
+  *n.rows = FEED_NAMES[FEED];
   auto kern = norm_fwd_kernel<IN, RES, VPT, FEED>;
   const int smem = fwd_smem<IN, RES>(n, g, FEED);
   if (smem > 0) {

@@ -36,6 +36,8 @@ namespace nr {
 //   FEED_SCALAR: bases off 16 bytes, and wide rows with such a d: element by element.
 enum Feed : int { FEED_SCALAR = 0, FEED_VEC = 1, FEED_RING = 2, FEED_SHIFT = 3 };
 
+constexpr const char* FEED_NAMES[] = {"element", "vector", "ring", "shifted ring"};
+
 constexpr int MAX_TEAMS = 15;     // named barriers 1..15
 constexpr int SMEM_BYTES = 224 * 1024;  // dynamic, beside 1 KB of the warps' slots
 

@@ -21,6 +21,7 @@ struct NormResidual {
   float* ws;
   int num_sms;
   cudaStream_t stream;
+  const char** rows;  // set to how the kernel takes its rows
 };
 
 cudaError_t norm_residual_fwd_launch(const NormResidual& a);

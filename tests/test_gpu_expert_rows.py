@@ -101,3 +101,28 @@ def test_norms_off_16_bytes(shape, gate):
         assert c.B.data_ptr() % 16 and c.dHo.data_ptr() % 16
         c.check_forward(f"{gate} {dtype} {res}")
         c.check_backward(f"{gate} {dtype} {res}")
+
+
+# aligned rows of which two do not fit shared memory: straight into registers, in words of 16 bytes
+PAST_THE_RING = [("none", BF, F32, 10240), ("token", HF, F32, 12288), ("none", BF, F32, 9224), ("none", F32, F32, 6920),
+                 ("token", F32, F32, 12288), ("channel", F32, F32, 7176), ("channel", F32, F32, 8192), ("full", F32, F32, 5640),
+                 ("full", F32, F32, 8192), ("none", BF, BF, 12296), ("full", BF, BF, 8200)]
+
+
+@pytest.mark.parametrize("gate,dtype,res,d", PAST_THE_RING, ids=str)
+@pytest.mark.parametrize("T", [3, 1000])
+def test_wide_aligned_rows_are_taken_by_words(T, gate, dtype, res, d):
+    c = Case(T, d, gate, dtype, res)
+    c.check_backward(f"{gate} {dtype} {res}")
+    assert "rows by vector" in tg.tg_last_call()
+    c = Case(T, d, gate, dtype, res, off=1)
+    c.check_backward(f"{gate} {dtype} {res} off 16 bytes")
+    assert "rows by element" in tg.tg_last_call()
+
+
+def test_how_rows_are_taken():
+    for d, want in ((2304, "ring"), (2301, "shifted ring")):
+        c = Case(40, d, "full", BF, BF)
+        for call in (c.forward, c.backward):
+            call()
+            assert f"rows by {want} ok" in tg.tg_last_call()
