@@ -30,7 +30,10 @@
 // rows (2,304 x 5,760) took 92 us; with all sizes multiples of 16, 78.
 //
 // Roles of a CTA (7 warps): 0 producer (TMA), 1 MMA issuer (rank 0 of the
-// pair), 2-5 epilogue, 6 mender (weight gradient).  Every wait is bounded.
+// pair), 2-5 epilogue, 6 mender (weight gradient).  Every wait is bounded.  Two last
+// as long as reductions do, the epilogue's for an accumulator and the mender's for the
+// next slice: their bound grows with the blocks in between (10^9 rows of one expert in
+// a unit take 3 to 4 s, the plain bound is 2).
 //
 // Bound by the MMA rate and L2 while groups have hundreds of rows, by HBM
 // (weights, or the results of the weight gradient) below.  Measured: one group
@@ -62,6 +65,7 @@ constexpr int GT_SLICES = 2;      // weight gradient: buffers of a group's last 
 constexpr int GT_SLICE_BYTES = 4 * 16 * 128;  // two 64-column chunks of each operand
 constexpr int GT_MAXG = GROUPED_PER_LAUNCH + 2;   // experts of a launch, rows before and after them
 constexpr int GT_BAR_BYTES = 384;
+constexpr unsigned long long GT_BLOCK_NS = 8000;  // most that a block of a reduction may take (0.2 to 0.3 us measured)
 constexpr int GT_SPLIT_SAVES = 20;  // blocks that splitting reductions has to save a pair
 
 template <int OP>
@@ -553,10 +557,16 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
     if (OP == G_WGRAD) {
       int slice = 0;
       uint32_t phase = 0;
+      unsigned long long blocks = 0;  // that the producer goes through before it requests the slice
       for (int u = pair; u < tab.units; u += pairs_in_grid()) {
         const GtUnit c = gt_unit<OP>(args, tab, u);
-        if (c.rest == 0) continue;
-        if (!mbar_wait(smem_u32(&landed[slice]), phase, tmo, abort_flag, args.status, 0x46)) break;
+        const int own = c.k1 - c.k0;  // after the slice
+        if (c.rest == 0) {
+          blocks += own;
+          continue;
+        }
+        if (!mbar_wait(smem_u32(&landed[slice]), phase, tmo + blocks * GT_BLOCK_NS, abort_flag, args.status, 0x46)) break;
+        blocks = own;
         // rows rest..15 of each chunk of 16 rows of 128 bytes
         const int words = (16 - c.rest) * 8;  // of 16 bytes
         const int chunks = (c.nmma / 2 + 63) / 64;
@@ -585,7 +595,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
       if (c.n <= 0) continue;
       const bool sum = !c.zero();
       if (sum &&
-          !mbar_wait<true>(smem_u32(&tfull[acc]), acc_phase, tmo, abort_flag, args.status, 0x47))
+          !mbar_wait<true>(smem_u32(&tfull[acc]), acc_phase, tmo + (c.k1 - c.k0) * GT_BLOCK_NS, abort_flag, args.status, 0x47))
         break;
       tc_fence_after();
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256);

@@ -1,5 +1,9 @@
 """The expert-block operators on tensors of more than 2^31 elements: values far beyond the 32-bit range of an index,
 checked at sampled rows against the 64-bit definitions."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -87,3 +91,37 @@ def test_clip_beyond_32_bits():
     want = torch.tensor([0.3, 0.4, 1.2, 8.4], dtype=torch.float64, device="cuda")
     assert ((g[at].double() - want).abs() <= want * 2.0 ** -8).all() and float(small) == pytest.approx(13.2, rel=1e-6)
     assert int((g != 0).sum()) == 4
+
+
+LONG = """
+import torch
+import gemms_linear_layers_gb300 as tg
+E, d, T = 78, 8, 1 << 26
+off = torch.full((E + 1,), T, dtype=torch.int32)
+off[0], off[E - 1] = 0, T + 5  # the first expert: T rows; the last but one, which the same pair takes next: 5
+off[E] = T + 5
+dY, X = (torch.zeros(T + 5, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+g = torch.Generator(device="cuda")
+g.manual_seed(9)
+for t in (dY, X):  # whole numbers whose sums FP32 holds
+    t[::16] = torch.randint(0, 2, t[::16].shape, generator=g, device="cuda").to(t.dtype)
+    t[-5:] = 1
+got = tg.tg_grouped_wgrad(dY, X, off.cuda(), out_dtype=torch.float32)
+a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+a.record()
+tg.tg_grouped_wgrad(dY, X, off.cuda(), dW=got)
+b.record()
+torch.cuda.synchronize()
+assert tg.tg_stream_status() == 0
+assert torch.equal(got[0].double(), dY[:T:16].double().T @ X[:T:16].double())
+assert (got[E - 2] == 5).all() and (got[1:E - 2] == 0).all() and (got[E - 1] == 0).all()
+assert a.elapsed_time(b) > 100, a.elapsed_time(b)  # longer than twice the bound
+"""
+
+
+def test_a_reduction_longer_than_the_bound_on_waits():
+    """The bound on a wait is 50 ms here; the waits for one long unit, and for the slice after it, last longer."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", LONG], env={**os.environ, "TG_WAIT_TIMEOUT_MS": "50"}, cwd=root,
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
