@@ -88,6 +88,13 @@ class ExpertBlock:
         return norm
 
 
+def loss_and_gradient(out, target):
+    """The squared distance of a token's output from its target, averaged over the tokens, and its gradient for
+    `out` in out's type."""
+    diff = out.float() - target.float()
+    return diff.square().sum(1).mean(), (diff * (2.0 / out.shape[0])).to(out.dtype)
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--tokens", type=int, default=2048)
@@ -106,9 +113,8 @@ def main(argv=None):
     losses = []
     for k in range(a.steps):
         _, out = block.forward(N, H)
-        diff = out.float() - target.float()
-        loss = diff.square().mean()
-        block.backward(zero, (diff * (2.0 / a.tokens)).to(H.dtype))
+        loss, dN = loss_and_gradient(out, target)
+        block.backward(zero, dN)
         norm = block.step(a.lr, a.max_norm)
         losses.append((loss, norm))
     for k, (loss, norm) in enumerate(losses):

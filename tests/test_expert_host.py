@@ -10,7 +10,7 @@ from torch.multiprocessing.reductions import StorageWeakRef
 
 import gemms_linear_layers_gb300 as tg
 from gemms_linear_layers_gb300 import _binding as B
-from gemms_linear_layers_gb300 import build
+from gemms_linear_layers_gb300 import build, expert_step
 
 BF = torch.bfloat16
 NULL, EVEN, ODD, HALF = (ctypes.c_void_p(x) for x in (0, 0x1000, 0x1001, 0x1002))
@@ -236,3 +236,15 @@ def test_the_type_of_summed_gradients_follows_any_given_output(monkeypatch, give
     assert full["dw_pre"].dtype == BF
     with pytest.raises(ValueError):
         tg.tg_norm_residual_bwd(x, x, x, x, w, w, r, r, gate=w, outs={**outs, "dw_post": dev(8), "dw_pre": r[:0]})
+
+
+def test_the_examples_gradient_is_that_of_its_loss():
+    g = torch.Generator().manual_seed(3)
+    out, target = torch.randn(7, 24, generator=g, dtype=torch.float64), torch.randn(7, 24, generator=g, dtype=torch.float64)
+    loss, grad = expert_step.loss_and_gradient(out, target)
+    assert grad.dtype == out.dtype
+    for k in range(3):  # quadratic: its central difference is the derivative, but for roundings
+        D = torch.randn(7, 24, generator=g, dtype=torch.float64)
+        up, down = (expert_step.loss_and_gradient(out + s * D, target)[0] for s in (0.5, -0.5))
+        assert float((grad * D).sum()) == pytest.approx(float(up - down), rel=1e-4)  # FP32: sums of 168 terms
+    assert float(loss) > 0
