@@ -681,11 +681,15 @@ def tg_norm_residual_bwd(dH_out, dN, B, H_out, w_post, w_pre, rstd_b, rstd_h, ga
     kind, gshape, g = _gate(gate, T, d, dt, dev)
     ot = out_dtype
     if ot is None:  # that of any output of this type that is given
-        summed = ("dw_post", "dw_pre") if kind in (TG_GATE_NONE, TG_GATE_FULL) else ("dw_post", "dw_pre", "dgate")
-        ot = next((outs[k].dtype for k in summed if outs.get(k) is not None), dt) if outs else dt
+        ot = dt
+        for k in ("dw_post", "dw_pre", "dgate") if outs else ():
+            t = outs.get(k)
+            if t is not None and (k != "dgate" or kind in (TG_GATE_CHANNEL, TG_GATE_TOKEN)):
+                ot = t.dtype
+                break
     res = {}
     db, dh = _result(res, outs, "dB", shape, dt, dev, stream), _result(res, outs, "dH", shape, rt, dev, stream)
-    dwq, dwp = (_result(res, outs, k, (d,), ot, dev, stream) for k in ("dw_post", "dw_pre"))
+    dwq, dwp = _result(res, outs, "dw_post", (d,), ot, dev, stream), _result(res, outs, "dw_pre", (d,), ot, dev, stream)
     gt = dt if kind == TG_GATE_FULL else ot
     dg = 0 if kind == TG_GATE_NONE else _result(res, outs, "dgate", gshape, gt, dev, stream)
     din, dout = _DT.get(dt, -1), _DT.get(ot, -1)
