@@ -372,8 +372,10 @@ tg_status tg_grouped_wgrad(const void* dY, const void* X, const int32_t* offsets
  * (bf16, fp16 or FP32); H and H_out have type `res` (FP32 or `in`); N and
  * rstd_h are taken from H_out before its rounding.  H_out may be H.  rstd_b
  * and rstd_h ([T], FP32; what the backward takes) may be NULL.
- * FP32 arithmetic, each output rounded once.  d <= 16384.  res_scale finite,
- * eps finite and >= 0 (a zero row with eps = 0 gives NaN). */
+ * FP32 arithmetic, squares included (a row whose sum of squares leaves FP32's
+ * range has rstd 0), each output rounded once.  d <= 16384.  res_scale finite,
+ * eps finite and >= 0 (a row whose squares sum to zero gives NaN with eps =
+ * 0). */
 tg_status tg_norm_residual_fwd(const void* B, const void* H, const void* w_post, const void* w_pre, const void* gate,
                                tg_gate gate_kind, void* H_out, void* N, float* rstd_b, float* rstd_h, int64_t T,
                                int64_t d, float res_scale, float eps, tg_dtype in, tg_dtype res, void* stream);
@@ -403,9 +405,11 @@ tg_status tg_norm_residual_bwd(const void* dH_out, const void* dN, const void* B
  * zero; outs[i] has grads[i]'s type and may be grads[i].  norm: one FP32
  * value on the device.  Squares are summed in FP32 groups of at most 32 and
  * FP64 beyond; magnitudes whose square leaves FP32's range are handled.  A
- * norm that is infinite gives c = 0, one that is not a number stays so.  When
- * every output is in place and c = 1 nothing is written to them.  max_norm >=
- * 0 (may be infinite).  n <= 2^20.  Workspace: tg_workspace_size(
+ * norm that is infinite gives c = 0 (not a number when max_norm is infinite
+ * too), one that is not a number stays so.  When every output is in place and
+ * c = 1 nothing is written to them.  A tensor given twice counts twice in the
+ * norm; outputs must not overlap one another, nor another entry's gradient.
+ * max_norm >= 0 (may be infinite).  n <= 2^20.  Workspace: tg_workspace_size(
  * TG_OP_GRAD_CLIP, n, 0, 0, 0, TG_F32, TG_F32), 16-byte aligned.  Results are
  * bitwise reproducible. */
 tg_status tg_grad_norm(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int64_t n, float* norm,
