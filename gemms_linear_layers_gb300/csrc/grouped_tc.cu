@@ -36,12 +36,14 @@
 // a unit take 3 to 4 s, the plain bound is 2).
 //
 // Bound by the MMA rate and L2 while groups have hundreds of rows, by HBM
-// (weights, or the results of the weight gradient) below.  Measured: one group
-// of 4,096 rows, 5,760 -> 2,304: 1,830 / 1,790 / 1,760 TFLOP/s forward / input
-// gradient / weight gradient; 16,384 rows over 64 experts, 2,304 -> 5,760: 335
-// to 349 us, up to 1,290 TFLOP/s and 5.9 TB/s; 64 rows over 8 experts: 35 us, 6 TB/s; 8 uneven
-// groups of 4,096 rows: 83 to 100 us input gradient (162 tiles for 76 pairs), 80 to 90 us
-// weight gradient (ranges over GPUs and sessions); one row of one small expert: 4.2 us.
+// (weights) below; the weight gradient of small groups by its epilogue's stores.
+// Measured: one group of 4,096 rows, 5,760 -> 2,304: 1,830 / 1,790 / 1,760 TFLOP/s
+// forward / input gradient / weight gradient; 16,384 rows over 64 experts, 2,304 ->
+// 5,760: 335 to 349 us at full clocks (1,240 to 1,290 TFLOP/s, 5.6 to 5.9 TB/s), 363 to
+// 383 in rows of hundreds of calls and more, where the power limit lowers the clocks;
+// 64 rows over 8 experts: 35 us, 6 TB/s; 8 uneven groups of 4,096 rows: 82 to 100 us
+// input gradient (162 tiles for 76 pairs), 81 to 90 us weight gradient (ranges over GPUs
+// and sessions); one row of one small expert: 4.2 us.
 #include <cuda.h>
 #include <stdio.h>
 

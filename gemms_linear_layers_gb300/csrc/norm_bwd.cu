@@ -14,9 +14,11 @@
 // below), so a row costs one exchange between its threads, not two.
 //
 // Measured: 8,192 x 2,304 bf16 with an FP32 stream 72 us, 4.7 TB/s, with a bf16
-// one 55 us, 4.1 TB/s (53 % of the issue slots, counted at 76 us: what an element costs in
-// conversions and FP32 arithmetic, and the chain of a row, stand before HBM);
-// 16,384 x 576 39 us; 8,192 x 2,300 with a bf16 stream 78 us; 2,048 x 576 15 us.
+// one 55 us, 4.1 TB/s; with a channel gate 82 and 61, with a full one 87 and 63.  What
+// stands before HBM is latency: neither issue (53 % of the slots) nor DRAM (52 %) is
+// saturated, counted at 76 us; waiting for loads is the first stall (3.9 an issue), then
+// the teams' barriers (2.5).  16,384 x 576 39 us; 8,192 x 2,300 with a bf16 stream 77 us;
+// 2,048 x 576 15 us.
 #include "norm_residual.cuh"
 
 namespace tg {

@@ -33,7 +33,7 @@ namespace nr {
 //     (the rows congruent to its index modulo 8 / gcd(8, d)), so columns stay
 //     with their thread here too; the weights are laid out with the same shift
 //     in shared memory.
-//   FEED_SCALAR: bases off 16 bytes, and wide rows with such a d: element by element.
+//   FEED_SCALAR: bases off 16 bytes, and rows with such a d that do not fit: element by element.
 enum Feed : int { FEED_SCALAR = 0, FEED_VEC = 1, FEED_RING = 2, FEED_SHIFT = 3 };
 
 constexpr const char* FEED_NAMES[] = {"element", "vector", "ring", "shifted ring"};
