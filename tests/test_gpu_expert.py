@@ -650,3 +650,25 @@ def test_clip_adds_each_group_of_squares_in_64_bits(dtype):
     want = torch.tensor(math.sqrt(total), dtype=F32)
     assert want > torch.tensor(math.sqrt(total - 512), dtype=F32)
     assert float(tg.tg_grad_norm([words, torch.full((1,), 14.0, device="cuda")])) == float(want)
+
+
+def test_a_captured_call_on_a_forked_stream_allocates_for_the_graph():
+    """A call with stream= inside a capture, on a stream forked from the captured one: outputs and workspace are the
+    graph's, and replays give the bits of the eager call."""
+    i = norm_inputs(300, 576, "channel", BF, BF)
+    rb, rh = (torch.ones(300, device="cuda") for _ in range(2))
+    call = lambda **kw: tg.tg_norm_residual_bwd(i["H"], i["B"], i["B"], i["H"], i["w_post"], i["w_pre"], rb, rh,
+                                                gate=i["gate"], **kw)
+    want = call()
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        for t in got.values():
+            t.zero_()
+        torch.cuda.empty_cache()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[k], want[k]) for k in want)
