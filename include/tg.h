@@ -342,9 +342,10 @@ tg_status tg_bmm_attn(tg_attn_op op, const void* A, const void* B, void* C, int6
  * Offsets that break the rules give unspecified results, but nothing outside
  * the tensors is read or written.
  * T, d_out and d_in are at most 2^31 - 1024, a tensor has at most 2^38
- * elements.  Any widths and alignments run on the tensor cores: an operand whose rows are no multiple of 8 elements, or whose base is not
- * 16-byte aligned, is first copied to rows that are, in `ws`.  Where there are
- * few output tiles and long reductions, these are cut into ranges whose FP32
+ * elements.  Any widths and alignments run on the tensor cores: an operand
+ * whose rows are no multiple of 8 elements, or whose base is not 16-byte
+ * aligned, is first copied to rows that are, in `ws`.  Where there are few
+ * output tiles and long reductions, these are cut into ranges whose FP32
  * sums, in `ws` too, are added in a fixed order.  Workspace:
  * tg_workspace_size(TG_OP_GROUPED_FWD / _DGRAD / _WGRAD, T, E, d_out, d_in),
  * or of TG_OP_GROUPED_UNALIGNED when an operand's base is not 16-byte
