@@ -14,6 +14,7 @@ __all__ = [
     "tg_lora_down", "tg_lora_up", "tg_lora_grad", "tg_lora_up_add", "tg_lora_grad_add",
     "tg_lora_down_f32w", "tg_lora_up_f32w", "tg_lora_grad_f32w", "tg_bmm_attn", "tg_attn_fwd", "tg_attn_bwd",
     "tg_grouped_fwd", "tg_grouped_dgrad", "tg_grouped_wgrad", "tg_norm_residual_fwd", "tg_norm_residual_bwd",
+    "tg_layer_norm_fwd", "tg_layer_norm_bwd", "tg_gated_fwd", "tg_gated_bwd", "tg_orthogonalize",
     "tg_grad_norm", "tg_grad_clip", "tg_tensor_list", "TGTensorList",
     "tg_workspace_size", "tg_plan_describe", "tg_stream_status",
     "tg_status_string", "tg_load_table", "tg_version", "tg_last_call", "tg_wait_probe", "lib",

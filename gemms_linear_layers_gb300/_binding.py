@@ -9,6 +9,7 @@ the library's kernels.  If libtg.so has not been built the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -31,7 +32,9 @@ TG_OP_ATTN_BWD = 10
 TG_OP_GEMM_FWD_LORA, TG_OP_GEMM_DGRAD_LORA = 11, 12
 TG_OP_GROUPED_FWD, TG_OP_GROUPED_DGRAD, TG_OP_GROUPED_WGRAD, TG_OP_GROUPED_UNALIGNED = 13, 14, 15, 16
 TG_OP_NORM_RESIDUAL_BWD, TG_OP_GRAD_CLIP = 17, 18
+TG_OP_LAYER_NORM_BWD, TG_OP_GATED_FWD, TG_OP_GATED_BWD, TG_OP_GATED_UNALIGNED, TG_OP_ORTHOGONALIZE = 19, 20, 21, 22, 23
 TG_GATE_NONE, TG_GATE_CHANNEL, TG_GATE_TOKEN, TG_GATE_FULL = 0, 1, 2, 3
+ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 ATTN_OPS = {"qk": 0, "pv": 1, "do_vt": 2, "pt_do": 3, "ds_k": 4, "dst_q": 5}
 SIZE_MAX = (1 << 64) - 1
 
@@ -69,6 +72,12 @@ SIGNATURES = {
                                   ctypes.c_float, _i, _i, _i, _vp, _sz, _vp]),
     "tg_grad_norm": (_i, [_vp, _vp, _vp, _i64, _vp, _vp, _sz, _vp]),
     "tg_grad_clip": (_i, [_vp, _vp, _vp, _vp, _i64, ctypes.c_float, _vp, _vp, _sz, _vp]),
+    "tg_layer_norm_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, ctypes.c_float, _i, _vp]),
+    "tg_layer_norm_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i, _i, _vp, _sz, _vp]),
+    "tg_gated_fwd": (_i, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i, _i, _vp, _sz, _vp]),
+    "tg_gated_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i, _i, _vp, _sz, _vp]),
+    "tg_orthogonalize": (_i, [_vp, _vp, _i64, _i64, _i64, _vp, _i64, ctypes.c_float, ctypes.c_float, _i, _i, _vp, _sz,
+                              _vp]),
     "tg_workspace_size": (_sz, [_i, _i64, _i64, _i64, _i64, _i, _i]),
     "tg_stream_status": (_i, [_vp]),
     "tg_status_string": (ctypes.c_char_p, [_i]),
@@ -782,6 +791,156 @@ def tg_grad_clip(grads, max_norm, outs=None, norm=None, ws=None, stream=None):
     in place, or into outs (tensors of the same types and sizes).  grads and outs: tensors, or lists laid out
     once with tg_tensor_list.  Returns the norm (before scaling), one FP32 value on the device ([1])."""
     return _grads("tg_grad_clip", grads, outs, max_norm, norm, ws, stream)
+
+
+def _on_current(t, name, ndim):
+    """A contiguous CUDA tensor on the current device; returns its device and type."""
+    _need(t, name, ndim)
+    dev = t.device
+    if dev.index != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be on the current device")
+    return dev, t.dtype
+
+
+def tg_layer_norm_fwd(X, w, b=None, eps=1e-5, outs=None, stream=None):
+    """Y = (X - mean) rstd w + b over the rows of X [T, d], rstd = (variance + eps)^-1/2; w, b [d].
+    Returns {"Y", "mean", "rstd"} (outs may give any of them; outs["Y"] may be X)."""
+    dev, dt = _on_current(X, "X", 2)
+    T, d = shape = tuple(X.shape)
+    wp = _like(w, "w", (d,), dt, dev)
+    bp = 0 if b is None else _like(b, "b", (d,), dt, dev)
+    res = {}
+    y = _result(res, outs, "Y", shape, dt, dev, stream)
+    m, r = (_result(res, outs, k, (T,), torch.float32, dev, stream) for k in ("mean", "rstd"))
+    status = (_lib or lib()).tg_layer_norm_fwd(X.data_ptr(), wp, bp, y, m, r, T, d, eps, _DT.get(dt, -1),
+                                               _raw_stream(stream, dev))
+    if status:
+        raise TGError(status, "tg_layer_norm_fwd")
+    return res
+
+
+def tg_layer_norm_bwd(dY, X, w, mean, rstd, dR=None, bias=True, out_dtype=None, outs=None, ws=None, stream=None):
+    """Gradients of <dY, Y> for the forward of tg_layer_norm_fwd: {"dX", "dw"} and, with `bias`, "db".  dR [T, d]: a
+    gradient to add to dX.  out_dtype (X's dtype or FP32; by default that of those in outs): dw and db."""
+    dev, dt = _on_current(X, "X", 2)
+    T, d = shape = tuple(X.shape)
+    dy, wp = _like(dY, "dY", shape, dt, dev), _like(w, "w", (d,), dt, dev)
+    m, r = _like(mean, "mean", (T,), torch.float32, dev), _like(rstd, "rstd", (T,), torch.float32, dev)
+    rp = 0 if dR is None else _like(dR, "dR", shape, dt, dev)
+    ot = out_dtype
+    if ot is None:  # that of either output that is given
+        given = [outs[k].dtype for k in ("dw", "db") if outs and outs.get(k) is not None and (bias or k == "dw")]
+        ot = given[0] if given else dt
+    res = {}
+    dx, dw = _result(res, outs, "dX", shape, dt, dev, stream), _result(res, outs, "dw", (d,), ot, dev, stream)
+    db = _result(res, outs, "db", (d,), ot, dev, stream) if bias else 0
+    din, dout = _DT.get(dt, -1), _DT.get(ot, -1)
+    raw = _raw_stream(stream, dev)
+    wsp, wsn, held = _scratch(TG_OP_LAYER_NORM_BWD, (T, d, 0, 0), din, dout, ws, dev, stream, raw)
+    status = (_lib or lib()).tg_layer_norm_bwd(dy, X.data_ptr(), wp, m, r, rp, dx, dw, db, T, d, din, dout, wsp, wsn, raw)
+    if status:
+        raise TGError(status, "tg_layer_norm_bwd")
+    return res
+
+
+def _act(act):
+    code = ACTS.get(act) if isinstance(act, str) else act
+    if code not in (0, 1, 2, 3):
+        raise ValueError(f"act must be one of {', '.join(ACTS)}")
+    return code
+
+
+def tg_gated_fwd(X, W, act="silu", keep=False, outs=None, ws=None, stream=None):
+    """[G U] = X W^T and H = act(G) U in one kernel: X [T, d], W [2 f, d] (gate rows, then up rows).  Returns {"H"}
+    and, with `keep`, "GU" [T, 2 f], which the backward takes.  act: silu, gelu, gelu_tanh or relu."""
+    dev, dt = _on_current(X, "X", 2)
+    T, d = X.shape
+    rows = W.shape[0] if isinstance(W, torch.Tensor) and W.dim() == 2 else 0
+    if rows % 2:
+        raise ValueError("W must have an even number of rows: the gate's, then the up projection's")
+    f = rows // 2
+    wp = _like(W, "W", (rows, d), dt, dev)
+    a = _act(act)
+    res = {}
+    h = _result(res, outs, "H", (T, f), dt, dev, stream)
+    gu = _result(res, outs, "GU", (T, rows), dt, dev, stream) if keep else 0
+    din = _DT.get(dt, -1)
+    x = X.data_ptr()
+    raw = _raw_stream(stream, dev)
+    wsp, wsn, held = _scratch(TG_OP_GATED_UNALIGNED if (x | wp) & 15 else TG_OP_GATED_FWD, (T, f, d, 0), din, din, ws, dev,
+                              stream, raw)
+    status = (_lib or lib()).tg_gated_fwd(x, wp, h, gu, T, f, d, a, din, wsp, wsn, raw)
+    if status:
+        raise TGError(status, "tg_gated_fwd")
+    return res
+
+
+def tg_gated_bwd(dY, W_down, GU, act="silu", keep=False, outs=None, ws=None, stream=None):
+    """Through the down projection and the gate: with dH = dY W_down (never stored), dGU = [dH U act'(G), dH act(G)];
+    dY [T, d], W_down [d, f], GU [T, 2 f] of the forward.  Returns {"dGU"} and, with `keep`, "H" = act(G) U for the
+    down projection's weight gradient (outs may give them; outs["dGU"] may be GU)."""
+    dev, dt = _on_current(dY, "dY", 2)
+    T, d = dY.shape
+    f = W_down.shape[1] if isinstance(W_down, torch.Tensor) and W_down.dim() == 2 else 0
+    wp = _like(W_down, "W_down", (d, f), dt, dev)
+    gp = _like(GU, "GU", (T, 2 * f), dt, dev)
+    a = _act(act)
+    res = {}
+    dgu = _result(res, outs, "dGU", (T, 2 * f), dt, dev, stream)
+    h = _result(res, outs, "H", (T, f), dt, dev, stream) if keep else 0
+    din = _DT.get(dt, -1)
+    y = dY.data_ptr()
+    raw = _raw_stream(stream, dev)
+    wsp, wsn, held = _scratch(TG_OP_GATED_UNALIGNED if (y | wp) & 15 else TG_OP_GATED_BWD, (T, f, d, 0), din, din, ws, dev,
+                              stream, raw)
+    status = (_lib or lib()).tg_gated_bwd(y, wp, gp, dgu, h, T, f, d, a, din, wsp, wsn, raw)
+    if status:
+        raise TGError(status, "tg_gated_bwd")
+    return res
+
+
+# (a, b, c) of s -> a s + b s^3 + c s^5: five of them take every singular value into about [0.7, 1.2]
+ORTH_QUINTIC = (3.4445, -4.7750, 2.0315)
+
+
+@functools.lru_cache(maxsize=64)
+def _orth_coeffs(coeffs, steps):
+    """(host array, steps) of one triple for all steps or of a triple for each."""
+    flat = [float(x) for c in coeffs for x in (c if isinstance(c, tuple) else (c,))]
+    one = not isinstance(coeffs[0], tuple)
+    n = (5 if one else len(coeffs)) if steps is None else steps
+    if len(flat) != 3 * (1 if one else n):
+        raise ValueError("coeffs must be (a, b, c), or such a triple for each step")
+    flat = flat * n if one else flat
+    return (ctypes.c_double * len(flat))(*flat), n
+
+
+def tg_orthogonalize(G, O=None, out_dtype=None, steps=None, coeffs=ORTH_QUINTIC, scale=1.0, eps=1e-7, ws=None, stream=None):
+    """scale times the matrix (or each of a batch: G [rows, cols] or [batch, rows, cols]) that Newton-Schulz steps
+    X <- a X + (b A + c A A) X, A = X X^T, make of X = G / (|G| + eps): close to the nearest one with orthonormal rows
+    or columns.  coeffs: (a, b, c) for all steps (5 by default) or a triple for each.  G may be FP32; O is bf16 or
+    fp16 (by default G's dtype, bf16 for FP32) and may be G."""
+    if not isinstance(G, torch.Tensor) or G.dim() not in (2, 3):
+        raise ValueError("G must be [rows, cols] or [batch, rows, cols]")
+    dev, dt = _on_current(G, "G", G.dim())
+    shape = tuple(G.shape)
+    batch, rows, cols = shape if len(shape) == 3 else (1, *shape)
+    key = tuple(tuple(c) if isinstance(c, (list, tuple)) else c for c in coeffs)
+    array, n = _orth_coeffs(key, steps)
+    ot = out_dtype or (O.dtype if O is not None else torch.bfloat16 if dt is torch.float32 else dt)
+    if O is None:
+        O = _new(shape, ot, dev, stream)
+        o = O.data_ptr()
+    else:
+        o = _like(O, "O", shape, ot, dev)
+    din, dout = _DT.get(dt, -1), _DT.get(ot, -1)
+    raw = _raw_stream(stream, dev)
+    wsp, wsn, held = _scratch(TG_OP_ORTHOGONALIZE, (batch, rows, cols, 0), din, dout, ws, dev, stream, raw)
+    status = (_lib or lib()).tg_orthogonalize(G.data_ptr(), o, batch, rows, cols, ctypes.addressof(array), n, scale, eps,
+                                              din, dout, wsp, wsn, raw)
+    if status:
+        raise TGError(status, "tg_orthogonalize")
+    return O
 
 
 def tg_workspace_size(op, d0, d1, d2, d3, din, dout) -> int:

@@ -19,9 +19,12 @@
 #include <unordered_map>
 
 #include "attn.h"
+#include "gated.h"
 #include "grad_clip.h"
 #include "grouped.h"
+#include "layer_norm.h"
 #include "norm_residual.h"
+#include "orth.h"
 #include "ptx.cuh"
 #include "tg.h"
 #include "tg_internal.h"
@@ -1899,10 +1902,226 @@ tg_status tg_grad_clip(const void* const* grads, void* const* outs, const int64_
   return run_grad("grad_clip", grads, outs, numels, dtypes, n, max_norm, norm, ws, ws_bytes, stream);
 }
 
+// ------------------------------------------- the dense feed-forward block
+tg_status tg_layer_norm_fwd(const void* X, const void* w, const void* b, void* Y, float* mean, float* rstd, int64_t T,
+                            int64_t d, float eps, tg_dtype in, void* stream) {
+  if (!dtype_in_ok_layer(in)) return TG_ERR_UNSUPPORTED_DTYPE;
+  if (T < 0 || T > kMaxDim || d < 0 || d > NORM_MAX_D || !std::isfinite(eps) || eps < 0.f) return TG_ERR_INVALID_ARG;
+  const int64_t n = T * d;
+  TG_TRY(check_ptr(X, n, dt_bytes(in)));
+  TG_TRY(check_ptr(w, n > 0 ? d : 0, dt_bytes(in)));
+  TG_TRY(check_ptr(Y, n, dt_bytes(in)));
+  if (!aligned(b, dt_bytes(in)) || !aligned(mean, 4) || !aligned(rstd, 4)) return TG_ERR_MISALIGNED;
+  DevCtx* ctx = nullptr;
+  TG_TRY(device_ctx(&ctx));
+  if (n == 0) {
+    record("layer_norm_fwd empty: nothing to do");
+    return TG_OK;
+  }
+  LayerNorm a{};
+  a.X = X;
+  a.w = w;
+  a.b = b;
+  a.Y = Y;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.T = T;
+  a.d = d;
+  a.eps = eps;
+  a.in_kind = ek_of(in);
+  a.num_sms = ctx->sms;
+  a.stream = static_cast<cudaStream_t>(stream);
+  const char* rows = "";
+  a.rows = &rows;
+  const cudaError_t e = layer_norm_fwd_launch(a);
+  record("layer_norm_fwd T=" + std::to_string(T) + " d=" + std::to_string(d) + " rows by " + rows + " " +
+         (e == cudaSuccess ? "ok" : cudaGetErrorString(e)));
+  return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
+}
+
+tg_status tg_layer_norm_bwd(const void* dY, const void* X, const void* w, const float* mean, const float* rstd,
+                            const void* dR, void* dX, void* dw, void* db, int64_t T, int64_t d, tg_dtype in,
+                            tg_dtype out, void* ws, size_t ws_bytes, void* stream) {
+  if (!dtype_in_ok_layer(in) || !dtype_out_ok(in, out)) return TG_ERR_UNSUPPORTED_DTYPE;
+  if (T < 0 || T > kMaxDim || d < 0 || d > NORM_MAX_D) return TG_ERR_INVALID_ARG;
+  const int64_t n = T * d;
+  TG_TRY(check_ptr(dY, n, dt_bytes(in)));
+  TG_TRY(check_ptr(X, n, dt_bytes(in)));
+  TG_TRY(check_ptr(w, n > 0 ? d : 0, dt_bytes(in)));
+  TG_TRY(check_ptr(mean, n > 0 ? T : 0, 4));
+  TG_TRY(check_ptr(rstd, n > 0 ? T : 0, 4));
+  TG_TRY(check_ptr(dX, n, dt_bytes(in)));
+  TG_TRY(check_ptr(dw, d, dt_bytes(out)));
+  if (!aligned(dR, dt_bytes(in)) || !aligned(db, dt_bytes(out))) return TG_ERR_MISALIGNED;
+  DevCtx* ctx = nullptr;
+  TG_TRY(device_ctx(&ctx));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (n == 0) {  // sums over nothing
+    record("layer_norm_bwd empty: zero fill");
+    if (d > 0 && (cudaMemsetAsync(dw, 0, d * dt_bytes(out), st) != cudaSuccess ||
+                  (db && cudaMemsetAsync(db, 0, d * dt_bytes(out), st) != cudaSuccess)))
+      return TG_ERR_CUDA;
+    return TG_OK;
+  }
+  const size_t need = layer_norm_bwd_ws_bytes(T, d, ctx->sms);
+  if (ws == nullptr || ws_bytes < need) return TG_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(ws, 16)) return TG_ERR_MISALIGNED;
+  LayerNorm a{};
+  a.X = X;
+  a.w = w;
+  a.dY = dY;
+  a.dR = dR;
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.dX = dX;
+  a.dw = dw;
+  a.db = db;
+  a.T = T;
+  a.d = d;
+  a.in_kind = ek_of(in);
+  a.out_kind = ek_of(out);
+  a.ws = static_cast<float*>(ws);
+  a.num_sms = ctx->sms;
+  a.stream = st;
+  const char* rows = "";
+  a.rows = &rows;
+  const cudaError_t e = layer_norm_bwd_launch(a);
+  record("layer_norm_bwd T=" + std::to_string(T) + " d=" + std::to_string(d) + " rows by " + rows + " " +
+         (e == cudaSuccess ? "ok" : cudaGetErrorString(e)));
+  return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
+}
+
+// as grouped_sizes_ok: [2 f, d] and [T, 2 f] are the largest tensors
+static bool gated_sizes_ok(int64_t T, int64_t f, int64_t d) {
+  const int64_t longest = (int64_t(1) << 31) - 1024, most = int64_t(1) << 38;
+  return T <= longest && f <= longest && d <= longest && T * d <= most && f * d <= most / 2 && T * f <= most / 2;
+}
+
+static tg_status run_gated(bool bwd, const char* name, const void* A, const void* W, const void* GU, void* H, void* out,
+                           int64_t T, int64_t f, int64_t d, tg_act act, tg_dtype in, void* ws, size_t ws_bytes,
+                           void* stream) {
+  TG_TRY(check_common(in, in, {T, f, d}));
+  if (!gated_sizes_ok(T, f, d) || act < TG_ACT_SILU || act > TG_ACT_RELU) return TG_ERR_INVALID_ARG;
+  TG_TRY(check_ptr(A, T > 0 && f > 0 ? T * d : 0, 2));
+  TG_TRY(check_ptr(W, T > 0 ? (bwd ? 1 : 2) * f * d : 0, 2));
+  const int64_t n = T * f;
+  if (bwd) {
+    TG_TRY(check_ptr(GU, 2 * n, 2));
+    TG_TRY(check_ptr(out, 2 * n, 2));
+    if (!aligned(H, 2)) return TG_ERR_MISALIGNED;
+  } else {
+    TG_TRY(check_ptr(H, n, 2));
+    if (!aligned(out, 2)) return TG_ERR_MISALIGNED;
+  }
+  DevCtx* ctx = nullptr;
+  TG_TRY(device_ctx(&ctx));
+  if (n == 0) {
+    record(std::string(name) + " empty output: nothing to do");
+    return TG_OK;
+  }
+  GatedCall g{};
+  g.bwd = bwd;
+  g.A = A;
+  g.W = W;
+  g.GU = GU;
+  g.H = H;
+  g.out = out;
+  g.T = T;
+  g.f = f;
+  g.d = d;
+  static_assert(TG_ACT_SILU == static_cast<int>(ACT_SILU) && TG_ACT_GELU == static_cast<int>(ACT_GELU) &&
+                    TG_ACT_GELU_TANH == static_cast<int>(ACT_GELU_TANH) && TG_ACT_RELU == static_cast<int>(ACT_RELU),
+                "activations");
+  g.act = act;
+  g.in_kind = ek_of(in);
+  g.ws = ws;
+  g.ws_bytes = ws_bytes;
+  g.num_sms = ctx->sms;
+  g.status = ctx->status;
+  g.timeout_ns = ctx->timeout_ns;
+  g.stream = static_cast<cudaStream_t>(stream);
+  size_t need = 0;
+  const char* path = "";
+  g.path = &path;
+  const cudaError_t e = gated_launch(g, &need);
+  if (need > 0) {
+    record(std::string(name) + ": workspace " + std::to_string(need) + " bytes needed (16-byte aligned), " +
+           std::to_string(ws ? ws_bytes : 0) + " given");
+    return TG_ERR_WORKSPACE_TOO_SMALL;
+  }
+  record(std::string(name) + " tc " + path + " T=" + std::to_string(T) + " f=" + std::to_string(f) + " d=" +
+         std::to_string(d) + " " + (e == cudaSuccess ? "ok" : cudaGetErrorString(e)));
+  return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
+}
+
+tg_status tg_gated_fwd(const void* X, const void* W, void* H, void* GU, int64_t T, int64_t f, int64_t d, tg_act act,
+                       tg_dtype in, void* ws, size_t ws_bytes, void* stream) {
+  return run_gated(false, "gated_fwd", X, W, nullptr, H, GU, T, f, d, act, in, ws, ws_bytes, stream);
+}
+
+tg_status tg_gated_bwd(const void* dY, const void* W_down, const void* GU, void* dGU, void* H, int64_t T, int64_t f,
+                       int64_t d, tg_act act, tg_dtype in, void* ws, size_t ws_bytes, void* stream) {
+  return run_gated(true, "gated_bwd", dY, W_down, GU, H, dGU, T, f, d, act, in, ws, ws_bytes, stream);
+}
+
+static const int64_t kMaxOrth = int64_t(1) << 20;
+static bool orth_sizes_ok(int64_t batch, int64_t rows, int64_t cols) {
+  const int64_t most = int64_t(1) << 38;
+  const int64_t m = std::min(rows, cols);
+  return batch <= kMaxOrth && rows <= kMaxOrth && cols <= kMaxOrth &&
+         (batch == 0 || (rows * (cols + 7) <= most / batch && m * (m + 7) <= most / batch));
+}
+
+tg_status tg_orthogonalize(const void* G, void* O, int64_t batch, int64_t rows, int64_t cols, const double* coeffs,
+                           int64_t steps, float scale, float eps, tg_dtype in, tg_dtype out, void* ws, size_t ws_bytes,
+                           void* stream) {
+  if (!dtype_in_ok_layer(in) || !dtype_in_ok(out)) return TG_ERR_UNSUPPORTED_DTYPE;
+  if (batch < 0 || rows < 0 || cols < 0 || !orth_sizes_ok(batch, rows, cols)) return TG_ERR_INVALID_ARG;
+  if (steps < 1 || steps > 64 || coeffs == nullptr || !std::isfinite(scale) || !std::isfinite(eps) || eps < 0.f)
+    return TG_ERR_INVALID_ARG;
+  for (int64_t i = 0; i < 3 * steps; ++i)
+    if (!std::isfinite(static_cast<float>(coeffs[i]))) return TG_ERR_INVALID_ARG;
+  const int64_t n = batch * rows * cols;
+  TG_TRY(check_ptr(G, n, dt_bytes(in)));
+  TG_TRY(check_ptr(O, n, dt_bytes(out)));
+  DevCtx* ctx = nullptr;
+  TG_TRY(device_ctx(&ctx));
+  if (n == 0) {
+    record("orthogonalize empty output: nothing to do");
+    return TG_OK;
+  }
+  const size_t need = orth_ws_bytes(batch, rows, cols);
+  if (ws == nullptr || ws_bytes < need) return TG_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(ws, 16)) return TG_ERR_MISALIGNED;
+  OrthCall g{};
+  g.G = G;
+  g.O = O;
+  g.batch = batch;
+  g.rows = rows;
+  g.cols = cols;
+  g.coeffs = coeffs;
+  g.steps = steps;
+  g.scale = scale;
+  g.eps = eps;
+  g.in_kind = ek_of(in);
+  g.out_kind = ek_of(out);
+  g.ws = ws;
+  g.num_sms = ctx->sms;
+  g.status = ctx->status;
+  g.timeout_ns = ctx->timeout_ns;
+  g.stream = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = orth_launch(g);
+  record("orthogonalize tc batch=" + std::to_string(batch) + " rows=" + std::to_string(rows) + " cols=" +
+         std::to_string(cols) + " steps=" + std::to_string(steps) + " " + (e == cudaSuccess ? "ok" : cudaGetErrorString(e)));
+  return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
+}
+
 size_t tg_workspace_size(tg_op op, int64_t d0, int64_t d1, int64_t d2, int64_t d3, tg_dtype in, tg_dtype out) {
   const bool layer = op == TG_OP_GEMM_FWD || op == TG_OP_GEMM_DGRAD || op == TG_OP_GEMM_WGRAD ||
-                     op == TG_OP_NORM_RESIDUAL_BWD || op == TG_OP_GRAD_CLIP;  // these take FP32 too
-  if (!(layer ? dtype_in_ok_layer(in) : dtype_in_ok(in)) || !dtype_out_ok(in, out)) return SIZE_MAX;
+                     op == TG_OP_NORM_RESIDUAL_BWD || op == TG_OP_GRAD_CLIP || op == TG_OP_LAYER_NORM_BWD ||
+                     op == TG_OP_ORTHOGONALIZE;  // these take FP32 too
+  if (!(layer ? dtype_in_ok_layer(in) : dtype_in_ok(in))) return SIZE_MAX;
+  if (!(op == TG_OP_ORTHOGONALIZE ? dtype_in_ok(out) : dtype_out_ok(in, out))) return SIZE_MAX;
   if (d0 < 0 || d1 < 0 || d2 < 0 || d3 < 0) return SIZE_MAX;
   DevCtx* ctx = nullptr;
   if (device_ctx(&ctx) != TG_OK) return SIZE_MAX;
@@ -1931,6 +2150,14 @@ size_t tg_workspace_size(tg_op op, int64_t d0, int64_t d1, int64_t d2, int64_t d
     case TG_OP_GROUPED_UNALIGNED: return grouped_workspace(0, 2, d0, d1, d2, d3, true, ctx->sms);
     case TG_OP_NORM_RESIDUAL_BWD:
       return d0 <= kMaxDim && d1 <= NORM_MAX_D ? norm_residual_bwd_ws_bytes(d0, d1, ctx->sms) : SIZE_MAX;
+    case TG_OP_LAYER_NORM_BWD:
+      return d0 <= kMaxDim && d1 <= NORM_MAX_D ? layer_norm_bwd_ws_bytes(d0, d1, ctx->sms) : SIZE_MAX;
+    case TG_OP_GATED_FWD: return gated_sizes_ok(d0, d1, d2) ? gated_ws_bytes(false, d0, d1, d2, false, ctx->sms) : SIZE_MAX;
+    case TG_OP_GATED_BWD: return gated_sizes_ok(d0, d1, d2) ? gated_ws_bytes(true, d0, d1, d2, false, ctx->sms) : SIZE_MAX;
+    case TG_OP_GATED_UNALIGNED:
+      if (!gated_sizes_ok(d0, d1, d2)) return SIZE_MAX;
+      return std::max(gated_ws_bytes(false, d0, d1, d2, true, ctx->sms), gated_ws_bytes(true, d0, d1, d2, true, ctx->sms));
+    case TG_OP_ORTHOGONALIZE: return orth_sizes_ok(d0, d1, d2) ? orth_ws_bytes(d0, d1, d2) : SIZE_MAX;
     case TG_OP_GRAD_CLIP: return d0 <= kMaxTensors ? grad_norm_ws_bytes(d0, ctx->sms) : SIZE_MAX;
     case TG_OP_BMM_ATTN: {
       GemmCall g;

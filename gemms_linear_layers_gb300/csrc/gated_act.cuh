@@ -1,0 +1,47 @@
+// gated_act.cuh -- the gate's activations and their derivatives, in FP32.
+#pragma once
+#include "gated.h"
+#include "ptx.cuh"
+
+namespace tg {
+
+// 1 / (1 + e^-x): 0 and 1 at the ends (the divide gives 0 for a denominator of 2^126 or more)
+__device__ __forceinline__ float logistic(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// The normal distribution's function: erfc keeps its relative accuracy where 1 + erf cancels.
+__device__ __forceinline__ float normal_cdf(float x) { return 0.5f * erfcf(x * -0.70710678118654752f); }
+
+// The tanh form of GELU is x s(y), s the logistic function, y = 2 sqrt(2/pi) (x + 0.044715 x^3)
+constexpr float GELU_K = 1.5957691216057308f, GELU_C = 0.044715f;
+
+template <int ACT>
+__device__ __forceinline__ float activation(float x) {
+  if constexpr (ACT == ACT_SILU) return x * logistic(x);
+  else if constexpr (ACT == ACT_GELU) return x * normal_cdf(x);
+  else if constexpr (ACT == ACT_GELU_TANH) return x * logistic(GELU_K * fmaf(GELU_C * x * x, x, x));
+  else return x < 0.f ? 0.f : x;  // not fmaxf: a value that is not a number stays one
+}
+
+template <int ACT>
+__device__ __forceinline__ float activation_grad(float x, float* value) {
+  if constexpr (ACT == ACT_SILU) {
+    const float p = logistic(x);
+    *value = x * p;
+    return p * fmaf(x, 1.f - p, 1.f);
+  } else if constexpr (ACT == ACT_GELU) {
+    const float p = normal_cdf(x);
+    *value = x * p;
+    return fmaf(x, 0.39894228040143268f * __expf(-0.5f * x * x), p);
+  } else if constexpr (ACT == ACT_GELU_TANH) {
+    const float p = logistic(GELU_K * fmaf(GELU_C * x * x, x, x));
+    *value = x * p;
+    // beyond 12 the factor p (1 - p) is 0 in FP32, and x^2 of the largest x must not make it 0 inf
+    const float z = fminf(fmaxf(x, -12.f), 12.f);
+    return fmaf(z * p * (1.f - p), GELU_K * fmaf(3.f * GELU_C * z, z, 1.f), p);
+  } else {
+    *value = x < 0.f ? 0.f : x;
+    return x > 0.f ? 1.f : 0.f;
+  }
+}
+
+}  // namespace tg

@@ -1,0 +1,345 @@
+// gated_tc.cu -- the gated feed-forward block on tcgen05 CTA pairs.
+//
+// Forward:   G = X Wg^T, U = X Wu^T, H = act(G) U, in one product over the weight
+//            [Wg; Wu]: a pair's tile takes `width` gate rows into rank 0's half of B
+//            and the same up rows into rank 1's, so that columns j and width + j of
+//            each CTA's accumulator are G and U of one element and H needs no exchange.
+// Backward:  dH = dY Wd (the down projection's input gradient), then in the epilogue
+//            dG = dH U act'(G), dU = dH act(G), and H = act(G) U again for the down
+//            projection's weight gradient.  dH never reaches memory.
+// Everything of an element is FP32 until its one rounding.  The blocks of G and U that
+// a backward epilogue needs are asked for before its accumulator is waited for.
+#include "gated.h"
+
+#include <type_traits>
+
+#include "gated_act.cuh"
+#include "pair_tc.cuh"
+#include "pitch_copy.cuh"
+
+namespace tg {
+namespace {
+
+struct GatedMaps {
+  CUtensorMap A, B, H, GU;
+};
+struct GatedArgs {
+  const uint16_t* gu_in;  // backward: G and U [T, 2 f]
+  uint16_t *h, *gu;       // outputs (h, or forward gu, may be null)
+  long long T, f;
+  int kb, units, m_tiles, width;  // width: columns of H of a tile
+  int act;
+  int wide;  // outputs through TMA, G and U by 16-byte words
+  uint32_t idesc;
+  unsigned long long timeout_ns;
+  unsigned int* status;
+};
+struct GatedUnit {
+  int m0, f0, kb, nmma;
+};
+
+__device__ __forceinline__ bool gated_unit(const GatedArgs& a, int u, GatedUnit& c, int per) {
+  const int nt = u / a.m_tiles;
+  c.m0 = (u - nt * a.m_tiles) * 256;
+  c.f0 = nt * a.width;
+  c.kb = a.kb;
+  c.nmma = per * a.width;
+  return true;
+}
+
+// The block's `cols` columns from f on, rows from row0 on, to plane z of `map` or to `to`.
+__device__ __forceinline__ void gated_put(const CUtensorMap* map, uint8_t* block, uint16_t* to, long long pitch, int f,
+                                          int row0, int z, int rows, int cols, int lane, bool wide) {
+  if (wide) {
+    if (lane == 0) tma_store_3d(map, smem_u32(block), f, row0, z);
+  } else {
+    pt::block_store(block, to + static_cast<long long>(row0) * pitch + f, pitch, rows, cols, lane);
+  }
+}
+
+template <bool F16>
+struct GatedFwd {
+  using Maps = GatedMaps;
+  using Args = GatedArgs;
+  using Unit = GatedUnit;
+  static constexpr int STAGES = 5, EPI_WARP = 3 * pt::BLOCK;
+  static constexpr bool A_MN = false, B_MN = false;
+  static constexpr unsigned SITE = 0x50;
+  static __device__ __forceinline__ void prefetch(const Maps& m, const Args& a) {
+    if (a.kb > 0) {
+      prefetch_tmap(&m.A);
+      prefetch_tmap(&m.B);
+    }
+  }
+  static __device__ __forceinline__ bool unit(const Args& a, int u, Unit& c) { return gated_unit(a, u, c, 2); }
+  static __device__ __forceinline__ uint32_t bytes(const Args& a, const Unit&) { return pt::A_BYTES + a.width * pt::BK * 2; }
+  static __device__ __forceinline__ void load(const Maps& m, const Args&, const Unit& c, int kb, int rank, uint32_t a_dst,
+                                              uint32_t b_dst, uint32_t bar) {
+    tma_load_3d_pair(a_dst, &m.A, bar, kb * pt::BK, c.m0 + rank * 128, 0);
+    tma_load_3d_pair(b_dst, &m.B, bar, kb * pt::BK, c.f0, rank);  // rank 0: gate rows, rank 1: up rows
+  }
+  template <class Wait, class Release>
+  static __device__ __forceinline__ void epilogue(const Maps& m, const Args& a, const Unit& c, int ew, int rank,
+                                                  uint32_t taddr, uint8_t* slot, Wait wait, Release release) {
+    const int lane = threadIdx.x & 31;
+    const int row0 = c.m0 + rank * 128 + ((ew + 2) & 3) * 32;
+    const int rows = static_cast<int>(min(32ll, a.T - row0));
+    const int half = a.width / 2, chunks = half / 32;
+    if (!wait()) return;
+#pragma unroll 1
+    for (int ch = 0; ch < chunks; ++ch) {
+      const int col = (ew >> 2) * half + ch * 32;
+      float g[32], u[32];
+      if (c.kb > 0) {
+        tmem_ld_32x32b_x32(taddr + col, reinterpret_cast<uint32_t*>(g));
+        tmem_ld_32x32b_x32(taddr + a.width + col, reinterpret_cast<uint32_t*>(u));
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) g[j] = u[j] = 0.f;
+      }
+      if (ch == chunks - 1) release();
+      const int cols = static_cast<int>(min(32ll, a.f - c.f0 - col));
+      if (rows <= 0 || cols <= 0) continue;
+      if (lane == 0) bulk_wait_read<0>();
+      __syncwarp();
+      if (a.gu) {
+        pt::put_row<F16>(slot + pt::BLOCK, lane, g);
+        pt::put_row<F16>(slot + 2 * pt::BLOCK, lane, u);
+      }
+      auto apply = [&](auto kind) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) g[j] = activation<decltype(kind)::value>(g[j]) * u[j];
+      };
+      switch (a.act) {
+        case ACT_SILU: apply(std::integral_constant<int, ACT_SILU>()); break;
+        case ACT_GELU: apply(std::integral_constant<int, ACT_GELU>()); break;
+        case ACT_GELU_TANH: apply(std::integral_constant<int, ACT_GELU_TANH>()); break;
+        default: apply(std::integral_constant<int, ACT_RELU>()); break;
+      }
+      pt::put_row<F16>(slot, lane, g);
+      fence_async_smem();
+      __syncwarp();
+      const int f = c.f0 + col;
+      gated_put(&m.H, slot, a.h, a.f, f, row0, 0, rows, cols, lane, a.wide);
+      if (a.gu) {
+        gated_put(&m.GU, slot + pt::BLOCK, a.gu, 2 * a.f, f, row0, 0, rows, cols, lane, a.wide);
+        gated_put(&m.GU, slot + 2 * pt::BLOCK, a.gu + a.f, 2 * a.f, f, row0, 1, rows, cols, lane, a.wide);
+      }
+      if (lane == 0) bulk_commit();
+      __syncwarp();
+    }
+  }
+};
+
+template <bool F16>
+struct GatedBwd {
+  using Maps = GatedMaps;
+  using Args = GatedArgs;
+  using Unit = GatedUnit;
+  static constexpr int STAGES = 5, EPI_WARP = 3 * pt::BLOCK;
+  static constexpr bool A_MN = false, B_MN = true;
+  static constexpr unsigned SITE = 0x58;
+  static __device__ __forceinline__ void prefetch(const Maps& m, const Args& a) { GatedFwd<F16>::prefetch(m, a); }
+  static __device__ __forceinline__ bool unit(const Args& a, int u, Unit& c) { return gated_unit(a, u, c, 1); }
+  static __device__ __forceinline__ int chunks64(const Args& a) { return (a.width / 2 + 63) / 64; }
+  static __device__ __forceinline__ uint32_t bytes(const Args& a, const Unit&) {
+    return pt::A_BYTES + chunks64(a) * 64 * pt::BK * 2;
+  }
+  static __device__ __forceinline__ void load(const Maps& m, const Args& a, const Unit& c, int kb, int rank,
+                                              uint32_t a_dst, uint32_t b_dst, uint32_t bar) {
+    tma_load_3d_pair(a_dst, &m.A, bar, kb * pt::BK, c.m0 + rank * 128, 0);
+    const int n = c.f0 + rank * (a.width / 2);
+    for (int j = 0; j < chunks64(a); ++j) tma_load_3d_pair(b_dst + j * 8192, &m.B, bar, n + 64 * j, kb * pt::BK, 0);
+  }
+  template <class Wait, class Release>
+  static __device__ __forceinline__ void epilogue(const Maps& m, const Args& a, const Unit& c, int ew, int rank,
+                                                  uint32_t taddr, uint8_t* slot, Wait wait, Release release) {
+    const int lane = threadIdx.x & 31;
+    const int row0 = c.m0 + rank * 128 + ((ew + 2) & 3) * 32;
+    const int rows = static_cast<int>(min(32ll, a.T - row0));
+    const int half = a.width / 2, chunks = half / 32;
+    const int col0 = (ew >> 2) * half;
+    pt::BlockRegs g, u;
+    auto fetch = [&](int ch) {
+      const int f = c.f0 + col0 + ch * 32;
+      const int cols = static_cast<int>(min(32ll, a.f - f));
+      if (rows <= 0 || cols <= 0) return;
+      const uint16_t* p = a.gu_in + static_cast<long long>(row0) * 2 * a.f + f;
+      pt::block_fetch(g, p, 2 * a.f, rows, cols, lane, a.wide);
+      pt::block_fetch(u, p + a.f, 2 * a.f, rows, cols, lane, a.wide);
+    };
+    fetch(0);
+    if (!wait()) return;
+#pragma unroll 1
+    for (int ch = 0; ch < chunks; ++ch) {
+      const int f = c.f0 + col0 + ch * 32;
+      const int cols = static_cast<int>(min(32ll, a.f - f));
+      const bool live = rows > 0 && cols > 0;
+      if (live) {
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+        pt::block_put(g, slot, lane);
+        pt::block_put(u, slot + pt::BLOCK, lane);
+        __syncwarp();
+      }
+      if (ch + 1 < chunks) fetch(ch + 1);
+      float dh[32];
+      if (c.kb > 0) {
+        tmem_ld_32x32b_x32(taddr + col0 + ch * 32, reinterpret_cast<uint32_t*>(dh));
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) dh[j] = 0.f;
+      }
+      if (ch == chunks - 1) release();
+      if (!live) continue;
+      // eight elements at a time, from the lane's rows of G and U into the same places
+      auto apply = [&](auto kind) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint4* pg = reinterpret_cast<uint4*>(pt::block_word(slot, lane, j));
+          uint4* pu = reinterpret_cast<uint4*>(pt::block_word(slot + pt::BLOCK, lane, j));
+          const uint4 wg = *pg, wu = *pu;
+          uint32_t og[4], ou[4], oh[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 x = pt::unpack16<F16>(reinterpret_cast<const uint32_t*>(&wg)[k]);
+            const float2 y = pt::unpack16<F16>(reinterpret_cast<const uint32_t*>(&wu)[k]);
+            const float d0 = dh[8 * j + 2 * k], d1 = dh[8 * j + 2 * k + 1];
+            float a0, a1;
+            const float b0 = activation_grad<decltype(kind)::value>(x.x, &a0);
+            const float b1 = activation_grad<decltype(kind)::value>(x.y, &a1);
+            og[k] = pt::pack16<F16>(d0 * y.x * b0, d1 * y.y * b1);
+            ou[k] = pt::pack16<F16>(d0 * a0, d1 * a1);
+            oh[k] = pt::pack16<F16>(a0 * y.x, a1 * y.y);
+          }
+          *pg = make_uint4(og[0], og[1], og[2], og[3]);
+          *pu = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+          if (a.h)
+            *reinterpret_cast<uint4*>(pt::block_word(slot + 2 * pt::BLOCK, lane, j)) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+        }
+      };
+      switch (a.act) {
+        case ACT_SILU: apply(std::integral_constant<int, ACT_SILU>()); break;
+        case ACT_GELU: apply(std::integral_constant<int, ACT_GELU>()); break;
+        case ACT_GELU_TANH: apply(std::integral_constant<int, ACT_GELU_TANH>()); break;
+        default: apply(std::integral_constant<int, ACT_RELU>()); break;
+      }
+      fence_async_smem();
+      __syncwarp();
+      gated_put(&m.GU, slot, a.gu, 2 * a.f, f, row0, 0, rows, cols, lane, a.wide);
+      gated_put(&m.GU, slot + pt::BLOCK, a.gu + a.f, 2 * a.f, f, row0, 1, rows, cols, lane, a.wide);
+      if (a.h) gated_put(&m.H, slot + 2 * pt::BLOCK, a.h, a.f, f, row0, 0, rows, cols, lane, a.wide);
+      if (lane == 0) bulk_commit();
+      __syncwarp();
+    }
+  }
+};
+
+// Operands as TMA takes them, and the copies that make them so.
+struct Staged {
+  const void* p[2];
+  int64_t pitch[2];
+  size_t bytes;
+  bool copy[2];
+};
+struct Operand {
+  const void* p;
+  int64_t rows, cols;
+};
+Staged staged(const Operand* op, void* ws) {
+  Staged s = {};
+  for (int i = 0; i < 2; ++i) {
+    s.p[i] = op[i].p;
+    s.pitch[i] = up8(op[i].cols);
+    s.copy[i] = op[i].cols > 0 && (op[i].cols % 8 != 0 || reinterpret_cast<uintptr_t>(op[i].p) % 16 != 0);
+    if (s.copy[i]) {
+      s.p[i] = static_cast<char*>(ws) + s.bytes;
+      s.bytes += up256(static_cast<size_t>(op[i].rows) * s.pitch[i] * 2);
+    }
+  }
+  return s;
+}
+
+template <class P>
+cudaError_t launch_one(const GatedCall& g, const Staged& s) {
+  const bool bwd = g.bwd;
+  GatedMaps m = {};
+  GatedArgs a = {};
+  a.gu_in = static_cast<const uint16_t*>(g.GU);
+  a.h = static_cast<uint16_t*>(g.H);
+  a.gu = static_cast<uint16_t*>(g.out);
+  a.T = g.T;
+  a.f = g.f;
+  a.kb = static_cast<int>((g.d + pt::BK - 1) / pt::BK);
+  a.m_tiles = static_cast<int>((g.T + 255) / 256);
+  a.act = g.act;
+  a.idesc = idesc_f16(g.in_kind == EK_BF16, P::A_MN, P::B_MN, 256, 0);
+  a.timeout_ns = g.timeout_ns;
+  a.status = g.status;
+  // whole tiles while they occupy more than half of the pairs, narrower ones below
+  a.width = bwd ? 256 : 128;
+  auto tiles = [&](int w) { return a.m_tiles * ((g.f + w - 1) / w); };
+  while (a.width > 64 && tiles(a.width) <= g.num_sms / 4) a.width /= 2;
+  a.units = static_cast<int>(tiles(a.width));
+  const uint64_t f = g.f, T = g.T, d = g.d;
+  a.wide = g.f % 8 == 0 && reinterpret_cast<uintptr_t>(g.H) % 16 == 0 && reinterpret_cast<uintptr_t>(g.out) % 16 == 0 &&
+           reinterpret_cast<uintptr_t>(g.GU) % 16 == 0;
+  bool ok = true;
+  if (d > 0) {
+    const uint64_t pa = s.pitch[0] * 2, pb = s.pitch[1] * 2;
+    ok = encode_tmap_3d(&m.A, s.p[0], g.in_kind, d, T, 1, pa, 0, 64, 128, 128);
+    ok = ok && (bwd ? encode_tmap_3d(&m.B, s.p[1], g.in_kind, f, d, 1, pb, 0, 64, 64, 128)
+                    : encode_tmap_3d(&m.B, s.p[1], g.in_kind, d, f, 2, pb, f * pb, 64, a.width, 128));
+  }
+  if (a.wide && g.H) ok = ok && encode_tmap_3d(&m.H, g.H, g.in_kind, f, T, 1, f * 2, 0, 32, 32, 64);
+  if (a.wide && g.out) ok = ok && encode_tmap_3d(&m.GU, g.out, g.in_kind, f, T, 2, 4 * f, 2 * f, 32, 32, 64);
+  if (!ok) return cudaErrorInvalidValue;
+  return pt::pair_launch<P>(m, a, g.num_sms, g.stream);
+}
+
+void operands(bool bwd, const void* A, const void* W, int64_t T, int64_t f, int64_t d, Operand* op) {
+  op[0] = {A, T, d};
+  op[1] = bwd ? Operand{W, d, f} : Operand{W, 2 * f, d};
+}
+
+}  // namespace
+
+size_t gated_ws_bytes(bool bwd, int64_t T, int64_t f, int64_t d, bool any_base, int) {
+  if (T <= 0 || f <= 0 || d <= 0) return 0;
+  Operand op[2];
+  operands(bwd, nullptr, nullptr, T, f, d, op);
+  if (any_base)
+    for (Operand& o : op) o.p = reinterpret_cast<const void*>(2);
+  return staged(op, nullptr).bytes;
+}
+
+cudaError_t gated_launch(const GatedCall& g, size_t* need) {
+  Operand op[2];
+  operands(g.bwd, g.A, g.W, g.T, g.f, g.d, op);
+  const Staged s = staged(op, g.ws);
+  *need = s.bytes;
+  if (s.bytes > 0 && (g.ws == nullptr || g.ws_bytes < s.bytes || reinterpret_cast<uintptr_t>(g.ws) % 16))
+    return cudaSuccess;
+  *need = 0;
+  if (s.bytes > 0) {
+    PitchCopy copy[2] = {};
+    int64_t words = 0;
+    for (int i = 0; i < 2; ++i)
+      if (s.copy[i]) {
+        copy[i] = {static_cast<const uint16_t*>(op[i].p), static_cast<uint16_t*>(const_cast<void*>(s.p[i])),
+                   static_cast<long long>(op[i].rows), static_cast<int>(op[i].cols), static_cast<int>(s.pitch[i])};
+        words += op[i].rows * (s.pitch[i] / 8);
+      }
+    int64_t grid = (words + 255) / 256;
+    if (grid > 8 * g.num_sms) grid = 8 * g.num_sms;
+    const cudaError_t e = launch_k(pitch_copy_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, g.stream, copy[0], copy[1]);
+    if (e != cudaSuccess) return e;
+  }
+  *g.path = "pairs";
+  if (g.in_kind == EK_F16) return g.bwd ? launch_one<GatedBwd<true>>(g, s) : launch_one<GatedFwd<true>>(g, s);
+  return g.bwd ? launch_one<GatedBwd<false>>(g, s) : launch_one<GatedFwd<false>>(g, s);
+}
+
+}  // namespace tg

@@ -48,6 +48,7 @@
 #include <stdio.h>
 
 #include "grouped.h"
+#include "pitch_copy.cuh"
 #include "ptx.cuh"
 #include "smem_attr.h"
 
@@ -768,45 +769,6 @@ __global__ void __launch_bounds__(256) grouped_sum_kernel(const float* parts, vo
   }
 }
 
-// Rows of `cols` 16-bit elements copied to rows of `pitch` (a multiple of 8)
-// elements, the rest zero: what TMA needs of an operand whose rows are no
-// multiple of 16 bytes or whose base is not 16-byte aligned.  Both operands of
-// a call in one launch.
-struct PitchCopy {
-  const uint16_t* src;
-  uint16_t* dst;
-  long long rows;
-  int cols, pitch;
-};
-// eight elements from column c of row r
-__device__ __forceinline__ void pitch_word(const PitchCopy& p, long long r, int c) {
-  const uint16_t* s = p.src + r * p.cols + c;
-  uint32_t o[4];
-  if (c + 8 <= p.cols && (reinterpret_cast<uintptr_t>(s) & 3) == 0) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = reinterpret_cast<const uint32_t*>(s)[j];
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = c + 2 * j < p.cols ? s[2 * j] : 0, hi = c + 2 * j + 1 < p.cols ? s[2 * j + 1] : 0;
-      o[j] = lo | hi << 16;
-    }
-  }
-  *reinterpret_cast<uint4*>(p.dst + r * p.pitch + c) = make_uint4(o[0], o[1], o[2], o[3]);
-}
-__global__ void __launch_bounds__(256) grouped_pitch_kernel(const PitchCopy a, const PitchCopy b) {
-  pdl_wait();
-  pdl_trigger();
-  const long long first = a.rows * (a.pitch / 8), all = first + b.rows * (b.pitch / 8);
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < all;
-       i += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const PitchCopy& p = i < first ? a : b;
-    const long long k = i < first ? i : i - first;
-    const int per = p.pitch / 8;
-    const long long r = k / per;
-    pitch_word(p, r, static_cast<int>(k - r * per) * 8);
-  }
-}
 // The same with the weights `a` of experts without rows left out, a warp a row:
 // for calls with fewer rows than experts (20 rows, 40 experts of 999 x 1,001: 17 us
 // instead of 42; where all experts have rows it is slower, 5,000 rows over 20
@@ -827,9 +789,6 @@ __global__ void __launch_bounds__(256) grouped_pitch_rows_kernel(const PitchCopy
     for (int c = (threadIdx.x & 31) * 8; c < p.cols; c += 256) pitch_word(p, r, c);
   }
 }
-
-int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
-size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Ranges of every tile's reduction: more than one where the tiles are at most
 // half the pairs and the reduction is long enough that a pair saves more (0.33 us
@@ -998,7 +957,7 @@ cudaError_t grouped_launch(const GroupedCall& call, size_t* need) {
     const dim3 ctas(static_cast<unsigned>(grid));
     const cudaError_t e = sparse ? launch_k(grouped_pitch_rows_kernel, ctas, dim3(256), 0, g.stream, copy[0], copy[1],
                                             g.offsets, static_cast<int>(g.d_out))
-                                 : launch_k(grouped_pitch_kernel, ctas, dim3(256), 0, g.stream, copy[0], copy[1]);
+                                 : launch_k(pitch_copy_kernel, ctas, dim3(256), 0, g.stream, copy[0], copy[1]);
     if (e != cudaSuccess) return e;
   }
   switch (g.op) {

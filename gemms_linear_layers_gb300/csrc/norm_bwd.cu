@@ -34,12 +34,6 @@ constexpr int BWD_WIDEST = 4;
 constexpr int bwd_threads(bool el, int vpt) { return vpt > 1 ? 512 : el ? 576 : 864; }
 constexpr int BWD_DEPTH = 2;      // rows in the ring
 
-__device__ __forceinline__ void put_kind(void* p, long long i, float v, int kind) {
-  if (kind == EK_F32) static_cast<float*>(p)[i] = v;
-  else if (kind == EK_F16) static_cast<__half*>(p)[i] = __float2half_rn(v);
-  else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-}
-
 // EL: the gate differs from element to element (full or channel); otherwise
 // it is one value a row, or 1
 template <typename IN, typename RES, int VPT, int FEED, bool EL>
@@ -277,32 +271,6 @@ __global__ void __launch_bounds__(bwd_threads(EL, VPT), 1) norm_bwd_kernel(const
   for (int i = threadIdx.x; i < sums * d; i += blockDim.x) out[i] = col[i];
 }
 
-// Column sums of the CTAs' partials [ctas][3][d], a block of 32 columns per
-// CTA: 32 threads a column add every 32nd partial in order, then a warp the
-// 32 sums of a column (8 threads a column spent most of 8 us waiting for loads).
-__global__ void __launch_bounds__(1024) norm_cols_kernel(const float* part, int ctas, int d, int sums, void* dw_post,
-                                                         void* dw_pre, void* dgate, int kind) {
-  __shared__ float s[32][33];
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  int i = blockIdx.x * 32 + x;
-  pdl_wait();  // no early trigger: wide rows make more CTAs than fit at once
-  float v = 0.f;
-  if (i < sums * d) {
-#pragma unroll 5
-    for (int c = y; c < ctas; c += 32) v += part[static_cast<long long>(c) * 3 * d + i];
-  }
-  s[y][x] = v;
-  __syncthreads();
-  v = s[x][y];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  i = blockIdx.x * 32 + y;
-  if (x == 0 && i < sums * d) {
-    const int which = i / d;
-    put_kind(which == 0 ? dw_post : which == 1 ? dw_pre : dgate, i - which * d, v, kind);
-  }
-}
-
 Geo bwd_geometry(int64_t T, int64_t d, bool shift, int sms, bool el) {
   int vpt = 1;
   for (const int v : {bwd_many(el), BWD_WIDEST})
@@ -338,7 +306,7 @@ cudaError_t bwd_one(const NormResidual& n, const Geo& g) {
   if (e != cudaSuccess) return e;
   const int sums = n.gate_kind == GATE_CHANNEL ? 3 : 2;
   return launch_k(norm_cols_kernel, dim3(static_cast<unsigned>((sums * n.d + 31) / 32)), dim3(1024), 0, n.stream,
-                  static_cast<const float*>(n.ws), g.ctas, static_cast<int>(n.d), sums, n.dw_post, n.dw_pre, n.dgate,
+                  static_cast<const float*>(n.ws), g.ctas, static_cast<int>(n.d), 3, sums, n.dw_post, n.dw_pre, n.dgate,
                   n.out_kind);
 }
 template <typename IN, typename RES, bool EL>

@@ -346,6 +346,39 @@ __device__ __forceinline__ void prefetch_row(const void* base, long long row, in
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i) : "memory");
 }
 
+__device__ __forceinline__ void put_kind(void* p, long long i, float v, int kind) {
+  if (kind == EK_F32) static_cast<float*>(p)[i] = v;
+  else if (kind == EK_F16) static_cast<__half*>(p)[i] = __float2half_rn(v);
+  else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+
+// Column sums of the CTAs' partials [ctas][planes][d], a block of 32 columns per
+// CTA: 32 threads a column add every 32nd partial in order, then a warp the
+// 32 sums of a column (8 threads a column spent most of 8 us waiting for loads).
+static __global__ void __launch_bounds__(1024) norm_cols_kernel(const float* part, int ctas, int d, int planes, int sums,
+                                                                void* dw_post, void* dw_pre, void* dgate, int kind) {
+  __shared__ float s[32][33];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  int i = blockIdx.x * 32 + x;
+  pdl_wait();  // no early trigger: wide rows make more CTAs than fit at once
+  float v = 0.f;
+  if (i < sums * d) {
+#pragma unroll 5
+    for (int c = y; c < ctas; c += 32) v += part[static_cast<long long>(c) * planes * d + i];
+  }
+  s[y][x] = v;
+  __syncthreads();
+  v = s[x][y];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  i = blockIdx.x * 32 + y;
+  if (x == 0 && i < sums * d) {
+    const int which = i / d;
+    put_kind(which == 0 ? dw_post : which == 1 ? dw_pre : dgate, i - which * d, v, kind);
+  }
+}
+
 // ----------------------------------------------------------------- host side
 struct Geo {
   int vpt, team, teams, ctas, classes;

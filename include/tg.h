@@ -96,6 +96,14 @@ typedef enum {
   TG_GATE_FULL = 3     /* [T, d] */
 } tg_gate;
 
+/* The gate's activation in tg_gated_*. */
+typedef enum {
+  TG_ACT_SILU = 0,      /* x / (1 + e^-x) */
+  TG_ACT_GELU = 1,      /* x Phi(x), Phi the normal distribution's function */
+  TG_ACT_GELU_TANH = 2, /* x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2 */
+  TG_ACT_RELU = 3       /* max(x, 0) */
+} tg_act;
+
 /* Operation ids for tg_workspace_size. */
 typedef enum {
   TG_OP_GEMM_FWD = 0,   /* d0=T, d1=d_out, d2=d_in */
@@ -116,7 +124,12 @@ typedef enum {
   TG_OP_GROUPED_WGRAD = 15,   /* d0=T, d1=E, d2=d_out, d3=d_in */
   TG_OP_GROUPED_UNALIGNED = 16, /* the same, when an operand's base is not 16-byte aligned */
   TG_OP_NORM_RESIDUAL_BWD = 17, /* d0=T, d1=d */
-  TG_OP_GRAD_CLIP = 18        /* d0=number of tensors (tg_grad_norm too) */
+  TG_OP_GRAD_CLIP = 18,       /* d0=number of tensors (tg_grad_norm too) */
+  TG_OP_LAYER_NORM_BWD = 19,  /* d0=T, d1=d */
+  TG_OP_GATED_FWD = 20,       /* d0=T, d1=f, d2=d */
+  TG_OP_GATED_BWD = 21,       /* d0=T, d1=f, d2=d */
+  TG_OP_GATED_UNALIGNED = 22, /* the same, when an operand's base is not 16-byte aligned */
+  TG_OP_ORTHOGONALIZE = 23    /* d0=batch, d1=rows, d2=cols */
 } tg_op;
 
 /* Forward product of a linear layer ("Where the time went"):
@@ -417,6 +430,88 @@ tg_status tg_grad_norm(const void* const* grads, const int64_t* numels, const in
                        void* ws, size_t ws_bytes, void* stream);
 tg_status tg_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels, const int32_t* dtypes,
                        int64_t n, float max_norm, float* norm, void* ws, size_t ws_bytes, void* stream);
+
+/* Layer norm over the rows of X [T, d]:
+ *   mean[t] = sum_c X[t,c] / d,  rstd[t] = (sum_c (X[t,c] - mean[t])^2 / d + eps)^-1/2
+ *   Y = (X - mean) . rstd . w + b
+ * w, b are [d]; b may be NULL (no bias).  X, w, b and Y have type `in` (bf16,
+ * fp16 or FP32).  mean and rstd ([T], FP32; what the backward takes) may be
+ * NULL.  Y may be X.  FP32 arithmetic, each output rounded once; the squares
+ * are of distances from a mean, so a row far from zero keeps its variance (a
+ * row whose sum of squares leaves FP32's range has rstd 0).  d <= 16384.  eps
+ * finite and >= 0 (a row of equal values gives NaN with eps = 0). */
+tg_status tg_layer_norm_fwd(const void* X, const void* w, const void* b, void* Y, float* mean, float* rstd, int64_t T,
+                            int64_t d, float eps, tg_dtype in, void* stream);
+
+/* Backward of tg_layer_norm_fwd: the gradients of <dY, Y> for X, w and b, given
+ * X, w and the forward's mean and rstd (means over the row):
+ *   n  = (X - mean) . rstd,  q = dY . w
+ *   dX = rstd . (q - mean(q) - n . mean(q . n)) + dR
+ *   dw = sum over the rows of dY . n,  db = sum over the rows of dY
+ * dR (may be NULL) is a gradient that reached X by another way, such as the
+ * residual stream's.  X, w, dY, dR and dX have type `in`; dw, db ([d]; db may
+ * be NULL) have type `out` (FP32 or `in`).  dX may be dY, dR or X.  Sums over
+ * rows are FP32 partials added in a fixed order: results are bitwise
+ * reproducible.  Workspace: tg_workspace_size(TG_OP_LAYER_NORM_BWD, T, d, 0, 0,
+ * in, out), 16-byte aligned; its content on entry does not matter. */
+tg_status tg_layer_norm_bwd(const void* dY, const void* X, const void* w, const float* mean, const float* rstd,
+                            const void* dR, void* dX, void* dw, void* db, int64_t T, int64_t d, tg_dtype in,
+                            tg_dtype out, void* ws, size_t ws_bytes, void* stream);
+
+/* A gated feed-forward block's projections, activation and product, in one
+ * kernel: with W[2 f, d] (f gate rows, then f up rows)
+ *   [G U][T, 2 f] = X[T, d] . W^T,   H[T, f] = act(G) . U
+ * X, W, H and GU have type `in` (bf16 or fp16); G and U enter act(G) . U as FP32
+ * sums, and each output is rounded once.  GU [T, 2 f] (G's columns, then U's) is
+ * what the backward takes; NULL when it is not wanted.  Any widths and
+ * alignments run on the tensor cores: an operand whose rows are no multiple of
+ * 8 elements, or whose base is not 16-byte aligned, is first copied to rows
+ * that are, in `ws`.  Workspace: tg_workspace_size(TG_OP_GATED_FWD, T, f, d, 0,
+ * in, in), or of TG_OP_GATED_UNALIGNED when an operand's base is not 16-byte
+ * aligned; 16-byte aligned, its content does not matter.  T, f and d are at most
+ * 2^31 - 1024, a tensor has at most 2^38 elements.  Results are bitwise
+ * reproducible, and a row's result does not depend on the other rows' values. */
+tg_status tg_gated_fwd(const void* X, const void* W, void* H, void* GU, int64_t T, int64_t f, int64_t d, tg_act act,
+                       tg_dtype in, void* ws, size_t ws_bytes, void* stream);
+
+/* Backward of tg_gated_fwd, together with the input gradient of the down
+ * projection Y = H . W_down^T that follows the block, W_down[d, f]: given
+ * dY[T, d] and the forward's GU,
+ *   dH = dY . W_down                        (FP32, never stored)
+ *   dG = dH . U . act'(G),  dU = dH . act(G),  H = act(G) . U
+ * dGU[T, 2 f] (dG's columns, then dU's) and H[T, f] have type `in`, rounded
+ * once.  H (NULL when it is not wanted) is computed again from GU, so that the
+ * forward's need not be kept for the down projection's weight gradient.  dGU
+ * may be GU.  The rest of the backward are the layer products:
+ *   tg_gemm_dgrad(dGU, W) = dX,  tg_gemm_wgrad(dGU, X) = dW,
+ *   tg_gemm_wgrad(dY, H)  = dW_down.
+ * Sizes, alignment, workspace (TG_OP_GATED_BWD) and reproducibility as
+ * tg_gated_fwd. */
+tg_status tg_gated_bwd(const void* dY, const void* W_down, const void* GU, void* dGU, void* H, int64_t T, int64_t f,
+                       int64_t d, tg_act act, tg_dtype in, void* ws, size_t ws_bytes, void* stream);
+
+/* Orthogonalised updates from gradients (or their momentum) by Newton-Schulz
+ * products, for `batch` matrices G[batch, rows, cols], each by itself: with
+ * X = G / (|G| + eps), |G| the Frobenius norm, and for i = 0 .. steps - 1
+ * (a, b, c) = coeffs[3 i .. 3 i + 2],
+ *   A = X . X^T,  X <- a X + (b A + c A . A) . X
+ * (for rows > cols the same of the transpose), and O = scale . X.  Each singular
+ * value s of X becomes a s + b s^3 + c s^5 in a step; (3.4445, -4.7750, 2.0315)
+ * takes all of them into about [0.7, 1.2] in five.  coeffs is a HOST array of
+ * 3 steps values, read before the call returns.  G has type `in` (bf16, fp16 or
+ * FP32), O type `out`, bf16 or fp16 (whatever `in`: the iterates are held as two
+ * bf16 parts, 2^-17, and their products summed in FP32, which is less than FP32
+ * outputs would promise).  O may be G when the types agree.  The norm's squares
+ * are summed in FP64 beyond groups of 8; a matrix of zeros gives zeros (not
+ * numbers with eps = 0), one that holds values that are not finite gives values
+ * that are not numbers, in that matrix only.  rows, cols and batch are at most
+ * 2^20, a tensor has at most 2^38 elements; 1 <= steps <= 64; scale and coeffs
+ * finite, eps finite and >= 0.  Workspace: tg_workspace_size(
+ * TG_OP_ORTHOGONALIZE, batch, rows, cols, 0, in, out), 16-byte aligned; its
+ * content does not matter.  Results are bitwise reproducible. */
+tg_status tg_orthogonalize(const void* G, void* O, int64_t batch, int64_t rows, int64_t cols, const double* coeffs,
+                           int64_t steps, float scale, float eps, tg_dtype in, tg_dtype out, void* ws, size_t ws_bytes,
+                           void* stream);
 
 /* Bytes of `ws` the call with these sizes needs on the current device
  * (0 when none).  Returns SIZE_MAX for invalid arguments. */
