@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libtg.so")
 
 SOURCES = ["api.cu", "gemm_tc_nt.cu", "gemm_tc_nn.cu", "gemm_tc_tn.cu", "gemm_simt.cu", "gemm_ffma.cu", "lora.cu", "lora_block.cu",
            "attn_tc.cu", "attn_bwd_tc.cu", "grouped_tc.cu", "norm_fwd.cu", "norm_bwd.cu", "grad_clip.cu", "layer_norm_fwd.cu",
-           "layer_norm_bwd.cu", "gated_tc.cu", "orth_tc.cu", "noalloc.cu", "tmap.cpp", "smem_attr.cpp"]
+           "layer_norm_bwd.cu", "gated_tc.cu", "gated_few.cu", "orth_tc.cu", "noalloc.cu", "tmap.cpp", "smem_attr.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC,-O2",
          f"-I{INCLUDE}", f"-I{CSRC}"]

@@ -14,6 +14,7 @@
 #include <type_traits>
 
 #include "gated_act.cuh"
+#include "gated_few.h"
 #include "pair_tc.cuh"
 #include "pitch_copy.cuh"
 
@@ -336,6 +337,12 @@ cudaError_t gated_launch(const GatedCall& g, size_t* need) {
     if (grid > 8 * g.num_sms) grid = 8 * g.num_sms;
     const cudaError_t e = launch_k(pitch_copy_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, g.stream, copy[0], copy[1]);
     if (e != cudaSuccess) return e;
+  }
+  if (g.T <= GATED_FEW && g.d > 0) {  // both sides measured in gated_few.cu
+    *g.path = "few rows";
+    const GatedFew f = {g.bwd, s.p[0], s.p[1], g.GU, g.H, g.out, g.T, g.f, g.d, s.pitch[0], s.pitch[1], g.act, g.in_kind, g.num_sms,
+                        g.status, g.timeout_ns, g.stream};
+    return gated_few_launch(f);
   }
   *g.path = "pairs";
   if (g.in_kind == EK_F16) return g.bwd ? launch_one<GatedBwd<true>>(g, s) : launch_one<GatedFwd<true>>(g, s);

@@ -142,7 +142,8 @@ def test_layer_norm_gradient_by_differences():
 
 
 # ----------------------------------------------------------- the gated block
-GATED_SIZES = [(1, 8, 8), (1, 64, 576), (3, 7, 5), (16, 1536, 576), (31, 33, 65), (127, 200, 72), (128, 128, 64),
+GATED_SIZES = [(1, 8, 8), (1, 64, 576), (3, 7, 5), (16, 1536, 576), (5, 200, 2304), (33, 130, 1501), (64, 1000, 3000),
+               (100, 5760, 2304), (31, 33, 65), (127, 200, 72), (128, 128, 64),
                (129, 130, 129), (256, 256, 128), (257, 1000, 999), (300, 1536, 576), (1001, 321, 200), (513, 5760, 2304)]
 
 
