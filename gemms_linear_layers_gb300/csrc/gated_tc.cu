@@ -48,13 +48,19 @@ __device__ __forceinline__ bool gated_unit(const GatedArgs& a, int u, GatedUnit&
   return true;
 }
 
-// The block's `cols` columns from f on, rows from row0 on, to plane z of `map` or to `to`.
-__device__ __forceinline__ void gated_put(const CUtensorMap* map, uint8_t* block, uint16_t* to, long long pitch, int f,
-                                          int row0, int z, int rows, int cols, int lane, bool wide) {
-  if (wide) {
-    if (lane == 0) tma_store_3d(map, smem_u32(block), f, row0, z);
-  } else {
-    pt::block_store(block, to + static_cast<long long>(row0) * pitch + f, pitch, rows, cols, lane);
+// Half a block's `cols` columns from f on to `to`, element by element.
+__device__ __forceinline__ void gated_put(uint8_t* block, int h, uint16_t* to, long long pitch, int f, int row0, int rows,
+                                          int cols, int lane) {
+  pt::half_store(block, h, to + static_cast<long long>(row0) * pitch + f, pitch, rows, cols, lane);
+}
+
+template <class F>
+__device__ __forceinline__ void with_act(int act, F apply) {
+  switch (act) {
+    case ACT_SILU: apply(std::integral_constant<int, ACT_SILU>()); break;
+    case ACT_GELU: apply(std::integral_constant<int, ACT_GELU>()); break;
+    case ACT_GELU_TANH: apply(std::integral_constant<int, ACT_GELU_TANH>()); break;
+    default: apply(std::integral_constant<int, ACT_RELU>()); break;
   }
 }
 
@@ -63,9 +69,10 @@ struct GatedFwd {
   using Maps = GatedMaps;
   using Args = GatedArgs;
   using Unit = GatedUnit;
-  static constexpr int STAGES = 5, EPI_WARP = 3 * pt::BLOCK;
-  static constexpr bool A_MN = false, B_MN = false;
+  static constexpr int PARTS = 1, STAGES = 5, EPI_BLOCKS = 3;
   static constexpr unsigned SITE = 0x50;
+  static __device__ __forceinline__ bool a_mn(const Args&, const Unit&, int) { return false; }
+  static __device__ __forceinline__ bool b_mn(const Args&, const Unit&, int) { return false; }
   static __device__ __forceinline__ void prefetch(const Maps& m, const Args& a) {
     if (a.kb > 0) {
       prefetch_tmap(&m.A);
@@ -80,55 +87,54 @@ struct GatedFwd {
     tma_load_3d_pair(b_dst, &m.B, bar, kb * pt::BK, c.f0, rank);  // rank 0: gate rows, rank 1: up rows
   }
   template <class Wait, class Release>
-  static __device__ __forceinline__ void epilogue(const Maps& m, const Args& a, const Unit& c, int ew, int rank,
-                                                  uint32_t taddr, uint8_t* slot, Wait wait, Release release) {
+  static __device__ __forceinline__ void epilogue(const Maps& m, const Args& a, const Unit& c, const pt::EpiWarp& at,
+                                                  Wait wait, Release release) {
     const int lane = threadIdx.x & 31;
-    const int row0 = c.m0 + rank * 128 + ((ew + 2) & 3) * 32;
+    const int row0 = c.m0 + at.rank * 128 + at.q * 32;
     const int rows = static_cast<int>(min(32ll, a.T - row0));
-    const int half = a.width / 2, chunks = half / 32;
+    uint8_t *bh = at.blocks, *bg = bh + pt::BLOCK, *bu = bg + pt::BLOCK;
     if (!wait()) return;
 #pragma unroll 1
-    for (int ch = 0; ch < chunks; ++ch) {
-      const int col = (ew >> 2) * half + ch * 32;
+    for (int col = 0; col < a.width; col += 64) {
+      const int mine = col + 32 * at.h;
       float g[32], u[32];
       if (c.kb > 0) {
-        tmem_ld_32x32b_x32(taddr + col, reinterpret_cast<uint32_t*>(g));
-        tmem_ld_32x32b_x32(taddr + a.width + col, reinterpret_cast<uint32_t*>(u));
+        tmem_ld_32x32b_x32(at.taddr + mine, reinterpret_cast<uint32_t*>(g));
+        tmem_ld_32x32b_x32(at.taddr + a.width + mine, reinterpret_cast<uint32_t*>(u));
         tmem_ld_wait();
       } else {
 #pragma unroll
         for (int j = 0; j < 32; ++j) g[j] = u[j] = 0.f;
       }
-      if (ch == chunks - 1) release();
-      const int cols = static_cast<int>(min(32ll, a.f - c.f0 - col));
-      if (rows <= 0 || cols <= 0) continue;
-      if (lane == 0) bulk_wait_read<0>();
-      __syncwarp();
+      if (col + 64 >= a.width) release();
+      if (rows <= 0 || c.f0 + col >= a.f) continue;
+      pt::blocks_free(at, lane);
       if (a.gu) {
-        pt::put_row<F16>(slot + pt::BLOCK, lane, g);
-        pt::put_row<F16>(slot + 2 * pt::BLOCK, lane, u);
+        pt::put_row<F16>(bg, lane, at.h, g);
+        pt::put_row<F16>(bu, lane, at.h, u);
       }
-      auto apply = [&](auto kind) {
+      with_act(a.act, [&](auto kind) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) g[j] = activation<decltype(kind)::value>(g[j]) * u[j];
-      };
-      switch (a.act) {
-        case ACT_SILU: apply(std::integral_constant<int, ACT_SILU>()); break;
-        case ACT_GELU: apply(std::integral_constant<int, ACT_GELU>()); break;
-        case ACT_GELU_TANH: apply(std::integral_constant<int, ACT_GELU_TANH>()); break;
-        default: apply(std::integral_constant<int, ACT_RELU>()); break;
+      });
+      pt::put_row<F16>(bh, lane, at.h, g);
+      if (a.wide) {
+        if (pt::blocks_full(at, lane)) {
+          tma_store_3d(&m.H, smem_u32(bh), c.f0 + col, row0, 0);
+          if (a.gu) {
+            tma_store_3d(&m.GU, smem_u32(bg), c.f0 + col, row0, 0);
+            tma_store_3d(&m.GU, smem_u32(bu), c.f0 + col, row0, 1);
+          }
+          bulk_commit();
+        }
+      } else {
+        const int f = c.f0 + mine, cols = static_cast<int>(min(32ll, a.f - f));
+        gated_put(bh, at.h, a.h, a.f, f, row0, rows, cols, lane);
+        if (a.gu) {
+          gated_put(bg, at.h, a.gu, 2 * a.f, f, row0, rows, cols, lane);
+          gated_put(bu, at.h, a.gu + a.f, 2 * a.f, f, row0, rows, cols, lane);
+        }
       }
-      pt::put_row<F16>(slot, lane, g);
-      fence_async_smem();
-      __syncwarp();
-      const int f = c.f0 + col;
-      gated_put(&m.H, slot, a.h, a.f, f, row0, 0, rows, cols, lane, a.wide);
-      if (a.gu) {
-        gated_put(&m.GU, slot + pt::BLOCK, a.gu, 2 * a.f, f, row0, 0, rows, cols, lane, a.wide);
-        gated_put(&m.GU, slot + 2 * pt::BLOCK, a.gu + a.f, 2 * a.f, f, row0, 1, rows, cols, lane, a.wide);
-      }
-      if (lane == 0) bulk_commit();
-      __syncwarp();
     }
   }
 };
@@ -138,9 +144,10 @@ struct GatedBwd {
   using Maps = GatedMaps;
   using Args = GatedArgs;
   using Unit = GatedUnit;
-  static constexpr int STAGES = 5, EPI_WARP = 3 * pt::BLOCK;
-  static constexpr bool A_MN = false, B_MN = true;
+  static constexpr int PARTS = 1, STAGES = 5, EPI_BLOCKS = 3;
   static constexpr unsigned SITE = 0x58;
+  static __device__ __forceinline__ bool a_mn(const Args&, const Unit&, int) { return false; }
+  static __device__ __forceinline__ bool b_mn(const Args&, const Unit&, int) { return true; }
   static __device__ __forceinline__ void prefetch(const Maps& m, const Args& a) { GatedFwd<F16>::prefetch(m, a); }
   static __device__ __forceinline__ bool unit(const Args& a, int u, Unit& c) { return gated_unit(a, u, c, 1); }
   static __device__ __forceinline__ int chunks64(const Args& a) { return (a.width / 2 + 63) / 64; }
@@ -154,53 +161,48 @@ struct GatedBwd {
     for (int j = 0; j < chunks64(a); ++j) tma_load_3d_pair(b_dst + j * 8192, &m.B, bar, n + 64 * j, kb * pt::BK, 0);
   }
   template <class Wait, class Release>
-  static __device__ __forceinline__ void epilogue(const Maps& m, const Args& a, const Unit& c, int ew, int rank,
-                                                  uint32_t taddr, uint8_t* slot, Wait wait, Release release) {
+  static __device__ __forceinline__ void epilogue(const Maps& m, const Args& a, const Unit& c, const pt::EpiWarp& at,
+                                                  Wait wait, Release release) {
     const int lane = threadIdx.x & 31;
-    const int row0 = c.m0 + rank * 128 + ((ew + 2) & 3) * 32;
+    const int row0 = c.m0 + at.rank * 128 + at.q * 32;
     const int rows = static_cast<int>(min(32ll, a.T - row0));
-    const int half = a.width / 2, chunks = half / 32;
-    const int col0 = (ew >> 2) * half;
-    pt::BlockRegs g, u;
-    auto fetch = [&](int ch) {
-      const int f = c.f0 + col0 + ch * 32;
-      const int cols = static_cast<int>(min(32ll, a.f - f));
-      if (rows <= 0 || cols <= 0) return;
+    uint8_t *bg = at.blocks, *bu = bg + pt::BLOCK, *bh = bu + pt::BLOCK;
+    pt::HalfRegs g, u;
+    auto fetch = [&](int col) {
+      const int f = c.f0 + col + 32 * at.h, cols = static_cast<int>(min(32ll, a.f - f));
       const uint16_t* p = a.gu_in + static_cast<long long>(row0) * 2 * a.f + f;
-      pt::block_fetch(g, p, 2 * a.f, rows, cols, lane, a.wide);
-      pt::block_fetch(u, p + a.f, 2 * a.f, rows, cols, lane, a.wide);
+      pt::half_fetch(g, p, 2 * a.f, rows, cols, lane, a.wide);
+      pt::half_fetch(u, p + a.f, 2 * a.f, rows, cols, lane, a.wide);
     };
     fetch(0);
     if (!wait()) return;
 #pragma unroll 1
-    for (int ch = 0; ch < chunks; ++ch) {
-      const int f = c.f0 + col0 + ch * 32;
-      const int cols = static_cast<int>(min(32ll, a.f - f));
-      const bool live = rows > 0 && cols > 0;
+    for (int col = 0; col < a.width; col += 64) {
+      const int mine = col + 32 * at.h;
+      const bool live = rows > 0 && c.f0 + col < a.f;
       if (live) {
-        if (lane == 0) bulk_wait_read<0>();
-        __syncwarp();
-        pt::block_put(g, slot, lane);
-        pt::block_put(u, slot + pt::BLOCK, lane);
+        pt::blocks_free(at, lane);
+        pt::half_put(g, bg, at.h, lane);
+        pt::half_put(u, bu, at.h, lane);
         __syncwarp();
       }
-      if (ch + 1 < chunks) fetch(ch + 1);
+      if (col + 64 < a.width) fetch(col + 64);
       float dh[32];
       if (c.kb > 0) {
-        tmem_ld_32x32b_x32(taddr + col0 + ch * 32, reinterpret_cast<uint32_t*>(dh));
+        tmem_ld_32x32b_x32(at.taddr + mine, reinterpret_cast<uint32_t*>(dh));
         tmem_ld_wait();
       } else {
 #pragma unroll
         for (int j = 0; j < 32; ++j) dh[j] = 0.f;
       }
-      if (ch == chunks - 1) release();
+      if (col + 64 >= a.width) release();
       if (!live) continue;
       // eight elements at a time, from the lane's rows of G and U into the same places
-      auto apply = [&](auto kind) {
+      with_act(a.act, [&](auto kind) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint4* pg = reinterpret_cast<uint4*>(pt::block_word(slot, lane, j));
-          uint4* pu = reinterpret_cast<uint4*>(pt::block_word(slot + pt::BLOCK, lane, j));
+          uint4* pg = reinterpret_cast<uint4*>(pt::block_word(bg, lane, 4 * at.h + j));
+          uint4* pu = reinterpret_cast<uint4*>(pt::block_word(bu, lane, 4 * at.h + j));
           const uint4 wg = *pg, wu = *pu;
           uint32_t og[4], ou[4], oh[4];
 #pragma unroll
@@ -218,22 +220,22 @@ struct GatedBwd {
           *pg = make_uint4(og[0], og[1], og[2], og[3]);
           *pu = make_uint4(ou[0], ou[1], ou[2], ou[3]);
           if (a.h)
-            *reinterpret_cast<uint4*>(pt::block_word(slot + 2 * pt::BLOCK, lane, j)) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+            *reinterpret_cast<uint4*>(pt::block_word(bh, lane, 4 * at.h + j)) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
         }
-      };
-      switch (a.act) {
-        case ACT_SILU: apply(std::integral_constant<int, ACT_SILU>()); break;
-        case ACT_GELU: apply(std::integral_constant<int, ACT_GELU>()); break;
-        case ACT_GELU_TANH: apply(std::integral_constant<int, ACT_GELU_TANH>()); break;
-        default: apply(std::integral_constant<int, ACT_RELU>()); break;
+      });
+      if (a.wide) {
+        if (pt::blocks_full(at, lane)) {
+          tma_store_3d(&m.GU, smem_u32(bg), c.f0 + col, row0, 0);
+          tma_store_3d(&m.GU, smem_u32(bu), c.f0 + col, row0, 1);
+          if (a.h) tma_store_3d(&m.H, smem_u32(bh), c.f0 + col, row0, 0);
+          bulk_commit();
+        }
+      } else {
+        const int f = c.f0 + mine, cols = static_cast<int>(min(32ll, a.f - f));
+        gated_put(bg, at.h, a.gu, 2 * a.f, f, row0, rows, cols, lane);
+        gated_put(bu, at.h, a.gu + a.f, 2 * a.f, f, row0, rows, cols, lane);
+        if (a.h) gated_put(bh, at.h, a.h, a.f, f, row0, rows, cols, lane);
       }
-      fence_async_smem();
-      __syncwarp();
-      gated_put(&m.GU, slot, a.gu, 2 * a.f, f, row0, 0, rows, cols, lane, a.wide);
-      gated_put(&m.GU, slot + pt::BLOCK, a.gu + a.f, 2 * a.f, f, row0, 1, rows, cols, lane, a.wide);
-      if (a.h) gated_put(&m.H, slot + 2 * pt::BLOCK, a.h, a.f, f, row0, 0, rows, cols, lane, a.wide);
-      if (lane == 0) bulk_commit();
-      __syncwarp();
     }
   }
 };
@@ -276,7 +278,7 @@ cudaError_t launch_one(const GatedCall& g, const Staged& s) {
   a.kb = static_cast<int>((g.d + pt::BK - 1) / pt::BK);
   a.m_tiles = static_cast<int>((g.T + 255) / 256);
   a.act = g.act;
-  a.idesc = idesc_f16(g.in_kind == EK_BF16, P::A_MN, P::B_MN, 256, 0);
+  a.idesc = idesc_f16(g.in_kind == EK_BF16, false, false, 256, 0);
   a.timeout_ns = g.timeout_ns;
   a.status = g.status;
   // whole tiles while they occupy more than half of the pairs, narrower ones below
@@ -294,8 +296,8 @@ cudaError_t launch_one(const GatedCall& g, const Staged& s) {
     ok = ok && (bwd ? encode_tmap_3d(&m.B, s.p[1], g.in_kind, f, d, 1, pb, 0, 64, 64, 128)
                     : encode_tmap_3d(&m.B, s.p[1], g.in_kind, d, f, 2, pb, f * pb, 64, a.width, 128));
   }
-  if (a.wide && g.H) ok = ok && encode_tmap_3d(&m.H, g.H, g.in_kind, f, T, 1, f * 2, 0, 32, 32, 64);
-  if (a.wide && g.out) ok = ok && encode_tmap_3d(&m.GU, g.out, g.in_kind, f, T, 2, 4 * f, 2 * f, 32, 32, 64);
+  if (a.wide && g.H) ok = ok && encode_tmap_3d(&m.H, g.H, g.in_kind, f, T, 1, f * 2, 0, 64, 32, 128);
+  if (a.wide && g.out) ok = ok && encode_tmap_3d(&m.GU, g.out, g.in_kind, f, T, 2, 4 * f, 2 * f, 64, 32, 128);
   if (!ok) return cudaErrorInvalidValue;
   return pt::pair_launch<P>(m, a, g.num_sms, g.stream);
 }

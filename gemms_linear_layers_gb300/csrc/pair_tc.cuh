@@ -6,20 +6,25 @@
 // P::STAGES), rank 0 issues the MMAs, each CTA's epilogue takes its 128 rows of
 // one of two accumulators while the MMAs of the next unit fill the other.
 // Roles of a CTA (10 warps): 0 producer (TMA), 1 MMA issuer (rank 0 of the
-// pair), 2-9 epilogue: two warps a lane quadrant, each with half of the columns.
+// pair), 2-9 epilogue: two warps a lane quadrant, which take the two halves of the
+// same 64 columns, so that rows of 128 bytes leave together.  (With 32 columns a
+// warp and rows of 64 bytes the epilogues of short reductions took twice as long:
+// TMA moves about a row a time, and the main loop's loads wait behind the stores.)
 // Every wait is bounded; the epilogue's wait for an accumulator lasts as long as a
 // reduction, so its bound grows with the blocks of one.
 //
 // P has: Maps, Args (with units, idesc, timeout_ns, status), Unit (with kb, the
-// blocks of its reduction; nmma, its columns), STAGES, EPI_WARP (bytes of shared
-// memory a warp), A_MN, B_MN, and
+// blocks of its reduction; nmma, its columns), PARTS (1, or 2: operands in two 16-bit
+// parts, a stage holds both of both, and a block is the products hi lo, lo hi and hi
+// hi), STAGES, EPI_BLOCKS (64-column blocks of shared memory a quadrant), and
+//   a_mn(args, unit, kb), b_mn     is the operand of this block MN-major
 //   prefetch(maps, args)           the maps of its operands
 //   unit(args, u, &unit)           false: nothing to do
 //   load(maps, args, unit, kb, rank, a_dst, b_dst, bar)   one block's copies
 //   bytes(args, unit)              that they complete on the barrier, a CTA
-//   epilogue(maps, args, unit, warp, rank, taddr, slot, wait, release)
-// `taddr`: the warp's lanes, first column of the accumulator.  The epilogue calls
-// wait() before it reads the accumulator (false: give up) and release() once it has.
+//   epilogue(maps, args, unit, at, wait, release)
+// The epilogue calls wait() before it reads the accumulator (false: give up; both
+// warps of a quadrant get the same answer) and release() once it has.
 #pragma once
 #include <cuda.h>
 
@@ -35,11 +40,12 @@ constexpr int BK = 64;
 constexpr int A_BYTES = 128 * BK * 2;  // one CTA's operand halves of a stage
 constexpr int B_BYTES = 128 * BK * 2;
 constexpr int BAR_BYTES = 256;
-constexpr unsigned long long BLOCK_NS = 8000;  // most that a block of a reduction may take (0.2 to 0.3 us measured)
+constexpr unsigned long long BLOCK_NS = 24000;  // most that a block of a reduction may take (0.2 to 1 us measured)
 
+constexpr int BLOCK = 32 * 128;  // 32 rows x 64 columns of 16 bits
 template <class P>
 constexpr int smem_bytes() {
-  return 1024 + P::STAGES * (A_BYTES + B_BYTES) + EPI_WARPS * P::EPI_WARP + BAR_BYTES;
+  return 1024 + P::STAGES * P::PARTS * (A_BYTES + B_BYTES) + 4 * P::EPI_BLOCKS * BLOCK + BAR_BYTES;
 }
 
 // An arrival on rank 0's barrier: it publishes nothing of its own (the copies'
@@ -48,6 +54,28 @@ __device__ __forceinline__ void arrive_expect_tx_cluster(uint32_t cluster_addr, 
   asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
                "r"(bytes)
                : "memory");
+}
+
+// Where an epilogue warp stands.
+struct EpiWarp {
+  int q, h;        // lane quadrant; half of the quadrant's 64 columns
+  int rank;        // CTA of the pair
+  uint32_t taddr;  // tensor memory: the warp's lanes, first column of the accumulator
+  uint8_t* blocks; // the quadrant's shared memory
+};
+// The 64 threads of a quadrant's two warps.
+__device__ __forceinline__ void quadrant_sync(int q) { asm volatile("bar.sync %0, 64;" ::"r"(q + 1) : "memory"); }
+__device__ __forceinline__ bool quadrant_all(int q, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, o;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred o, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, o;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u), "r"(q + 1)
+      : "memory");
+  return r != 0;
 }
 
 __device__ __forceinline__ int pair_index() { return static_cast<int>(blockIdx.x >> 1); }
@@ -63,9 +91,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sA = smem;
-  uint8_t* sB = sA + S * A_BYTES;
-  uint8_t* sE = sB + S * B_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sE + EPI_WARPS * P::EPI_WARP);
+  constexpr int A_STAGE = P::PARTS * A_BYTES, B_STAGE = P::PARTS * B_BYTES;
+  uint8_t* sB = sA + S * A_STAGE;
+  uint8_t* sE = sB + S * B_STAGE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sE + 4 * P::EPI_BLOCKS * BLOCK);
   uint64_t* empty = full + S;
   uint64_t* tfull = empty + S;
   uint64_t* tempty = tfull + 2;
@@ -124,8 +153,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
           arrive_expect_tx_cluster(bar, bytes);
-          P::load(maps, args, c, kb, static_cast<int>(rank), smem_u32(sA + stage * A_BYTES),
-                  smem_u32(sB + stage * B_BYTES), bar);
+          P::load(maps, args, c, kb, static_cast<int>(rank), smem_u32(sA + stage * A_STAGE),
+                  smem_u32(sB + stage * B_STAGE), bar);
           issued[stage] = static_cast<int>(phase);
           if (++stage == S) {
             stage = 0;
@@ -170,15 +199,21 @@ __global__ void __launch_bounds__(THREADS, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t a_base = smem_u32(sA + stage * A_BYTES);
-          const uint32_t b_base = smem_u32(sB + stage * B_BYTES);
+          const uint32_t a_base = smem_u32(sA + stage * A_STAGE);
+          const uint32_t b_base = smem_u32(sB + stage * B_STAGE);
+          const bool a_mn = P::a_mn(args, c, kb), b_mn = P::b_mn(args, c, kb);
+          const uint32_t id = idesc | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+          const uint64_t ad0 = a_mn ? sdesc_sw128(a_base, 8192, 1024) : sdesc_sw128(a_base, 16, 1024);
+          const uint64_t bd0 = b_mn ? sdesc_sw128(b_base, 8192, 1024) : sdesc_sw128(b_base, 16, 1024);
+          // 16 deep, in descriptor units of 16 bytes: 16 rows of an MN-major block, 32 bytes of K-major rows
+          const uint64_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2;
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = P::A_MN ? sdesc_sw128(a_base + kk * 2048, 8192, 1024)
-                                        : sdesc_sw128(a_base + kk * 32, 16, 1024);
-            const uint64_t bd = P::B_MN ? sdesc_sw128(b_base + kk * 2048, 8192, 1024)
-                                        : sdesc_sw128(b_base + kk * 32, 16, 1024);
-            umma_f16_pair(d_tmem, ad, bd, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+          for (int p = P::PARTS == 2 ? 0 : 2; p < 3; ++p) {
+            const uint64_t ad = ad0 + (p == 1 ? A_BYTES >> 4 : 0), bd = bd0 + (p == 0 ? B_BYTES >> 4 : 0);
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk)
+              umma_f16_pair(d_tmem, ad + kk * a_step, bd + kk * b_step, id,
+                            (kb > 0 || kk > 0 || (P::PARTS == 2 && p > 0)) ? 1u : 0u);
           }
           umma_commit_pair(smem_u32(&empty[stage]), 0x3);
           if (++stage == S) {
@@ -199,19 +234,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else {
     // ------------------------------------------------- epilogue (both CTAs)
-    const int ew = warp - 2;
+    EpiWarp at;
+    at.q = warp & 3;
+    at.h = (warp - 2) >> 2;
+    at.rank = static_cast<int>(rank);
+    at.blocks = sE + at.q * P::EPI_BLOCKS * BLOCK;
     const uint32_t tempty_cl = mapa_shared(smem_u32(&tempty[0]), 0);
     int acc = 0;
     uint32_t acc_phase = 0;
     typename P::Unit c;
     for (int u = pair_index(); u < args.units; u += pair_count()) {
       if (!P::unit(args, u, c)) continue;
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(acc * 256);
+      at.taddr = tmem_base + (static_cast<uint32_t>(at.q * 32) << 16) + static_cast<uint32_t>(acc * 256);
       bool ok = true;
       auto wait = [&] {
         if (c.kb == 0) return true;
         ok = mbar_wait<true>(smem_u32(&tfull[acc]), acc_phase, tmo + c.kb * BLOCK_NS, abort_flag, args.status, P::SITE + 6);
-        ok = __all_sync(~0u, ok);
+        ok = quadrant_all(at.q, ok);
         tc_fence_after();
         return ok;
       };
@@ -221,7 +260,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(tempty_cl + static_cast<uint32_t>(acc * 8));
       };
-      P::epilogue(maps, args, c, ew, static_cast<int>(rank), taddr, sE + ew * P::EPI_WARP, wait, release);
+      P::epilogue(maps, args, c, at, wait, release);
       if (!ok) break;
       if (c.kb > 0 && ++acc == 2) {
         acc = 0;
@@ -270,16 +309,12 @@ cudaError_t pair_launch(const typename P::Maps& maps, const typename P::Args& ar
   return cudaLaunchKernelEx(&cfg, kern, maps, args);
 }
 
-// ------------------------------------------------- 32 x 32 blocks of 16 bits
-// A warp's block in shared memory: rows of 64 bytes, 16-byte word j of row r at
-// word j ^ (r / 2 % 4) (TMA's 64-byte swizzle; 512-byte aligned).  Rows are read
-// and written by their lane without bank conflicts.
-constexpr int BLOCK = 32 * 64;
+// ------------------------------------------------- 32 x 64 blocks of 16 bits
+// A quadrant's block in shared memory: rows of 128 bytes, 16-byte word j of row r at
+// word j ^ (r % 8) (TMA's 128-byte swizzle; 1,024-byte aligned).  A lane reads and
+// writes its row of its warp's half without bank conflicts.
 __device__ __forceinline__ uint8_t* block_word(uint8_t* block, int row, int j) {
-  return block + row * 64 + ((j ^ ((row >> 1) & 3)) << 4);
-}
-__device__ __forceinline__ uint16_t* block_elem(uint8_t* block, int row, int col) {
-  return reinterpret_cast<uint16_t*>(block_word(block, row, col >> 3)) + (col & 7);
+  return block + row * 128 + ((j ^ (row & 7)) << 4);
 }
 
 template <bool F16>
@@ -292,25 +327,25 @@ __device__ __forceinline__ float2 unpack16(uint32_t v) {
   else return __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(v));
 }
 
-// A lane's row of 32 values, rounded, into its row of the block.
+// A lane's 32 values, rounded, into half h of its row of the block.
 template <bool F16>
-__device__ __forceinline__ void put_row(uint8_t* block, int lane, const float* v) {
+__device__ __forceinline__ void put_row(uint8_t* block, int lane, int h, const float* v) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    *reinterpret_cast<uint4*>(block_word(block, lane, j)) =
+    *reinterpret_cast<uint4*>(block_word(block, lane, 4 * h + j)) =
         make_uint4(pack16<F16>(v[8 * j], v[8 * j + 1]), pack16<F16>(v[8 * j + 2], v[8 * j + 3]),
                    pack16<F16>(v[8 * j + 4], v[8 * j + 5]), pack16<F16>(v[8 * j + 6], v[8 * j + 7]));
 }
 
-// A block of a matrix in global memory, in registers: word i of lane l is word
-// l % 4 of row 8 i + l / 4 (whole 64-byte rows travel together).
-struct BlockRegs {
+// Half a block (32 x 32) of a matrix in global memory, in registers: word i of lane l
+// is word l % 4 of row 8 i + l / 4.
+struct HalfRegs {
   uint4 w[4];
 };
 // `rows`, `cols` of it are inside; `wide`: rows start at multiples of 16 bytes and
 // cols is a multiple of 8.  What is outside reads as zero.
-__device__ __forceinline__ void block_fetch(BlockRegs& r, const uint16_t* p, long long pitch, int rows, int cols, int lane,
-                                            bool wide) {
+__device__ __forceinline__ void half_fetch(HalfRegs& r, const uint16_t* p, long long pitch, int rows, int cols, int lane,
+                                           bool wide) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = 8 * i + (lane >> 2), c = (lane & 3) * 8;
@@ -331,16 +366,31 @@ __device__ __forceinline__ void block_fetch(BlockRegs& r, const uint16_t* p, lon
     }
   }
 }
-__device__ __forceinline__ void block_put(const BlockRegs& r, uint8_t* block, int lane) {
+__device__ __forceinline__ void half_put(const HalfRegs& r, uint8_t* block, int h, int lane) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(block_word(block, 8 * i + (lane >> 2), lane & 3)) = r.w[i];
+  for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(block_word(block, 8 * i + (lane >> 2), 4 * h + (lane & 3))) = r.w[i];
 }
-// The block to global memory element by element, lanes along its rows: for rows
-// that TMA cannot take.
-__device__ __forceinline__ void block_store(uint8_t* block, uint16_t* p, long long pitch, int rows, int cols, int lane) {
+// Half h of the block to global memory element by element, lanes along its rows: for
+// rows that TMA cannot take.
+__device__ __forceinline__ void half_store(uint8_t* block, int h, uint16_t* p, long long pitch, int rows, int cols, int lane) {
+  __syncwarp();
 #pragma unroll 4
   for (int i = 0; i < 32; ++i)
-    if (i < rows && lane < cols) p[i * pitch + lane] = *block_elem(block, i, lane);
+    if (i < rows && lane < cols)
+      p[i * pitch + lane] = reinterpret_cast<const uint16_t*>(block_word(block, i, 4 * h + (lane >> 3)))[lane & 7];
+  __syncwarp();
+}
+
+// Before a quadrant's warps write its blocks: what was stored from them has been read.
+__device__ __forceinline__ void blocks_free(const EpiWarp& at, int lane) {
+  if (at.h == 0 && lane == 0) bulk_wait_read<0>();
+  quadrant_sync(at.q);
+}
+// Both have written; true in the thread that stores.
+__device__ __forceinline__ bool blocks_full(const EpiWarp& at, int lane) {
+  fence_async_smem();
+  quadrant_sync(at.q);
+  return at.h == 0 && lane == 0;
 }
 
 }  // namespace pt

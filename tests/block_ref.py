@@ -94,22 +94,31 @@ def gated_bwd(dY, W_down, GU, kind):
     return {"dGU": torch.cat((dG, dU), 1), "H": A * Up}, {"dGU": torch.cat((edG, edU), 1), "H": (ACT + U) * (A * Up).abs()}
 
 
-def orthogonalize(G, coeffs, scale, eps):
-    """(O, bound on |O' - O| in the Frobenius norm before O' is rounded) of one matrix.
+def orthogonalize(G, coeffs, scale, eps, out):
+    """(O, bound on |O' - O| in the Frobenius norm before O' is rounded to `out`) of one matrix.
 
     X and what is made of it are held to 2^-17, each product has two such factors.  For a step of X with largest
     singular value s that is at most 2^-17 |X| (a + 3 b s^2 + 9 c s^4) (A: 2 factors and itself; A A: 2 of 3 and
-    itself, and 2 more in Q X); later steps enlarge it by at most max |p'| and |p(s) / s| of theirs on [0, s]."""
+    itself, and 2 more in Q X); later steps enlarge it by at most max |p'| and |p(s) / s| of theirs on [0, s].
+    The last step of a bf16 result has X, D = A - I and E in one fp16 part in its products, u = 2^-11: with
+    e = 2 u s |X| + u |D| in D, it is s ((|b + 2 c| + 2 |c| |D|_2) e + u |E|) + |E|_2 u |X|."""
     X = G.double()
     X = X / (torch.linalg.vector_norm(X) + eps)
     noise = torch.zeros((), dtype=torch.float64, device=X.device)
-    for a, b, c in coeffs:
-        s = torch.linalg.matrix_norm(X, 2)
+    two, fro = (lambda M: torch.linalg.matrix_norm(M, 2)), torch.linalg.vector_norm
+    for i, (a, b, c) in enumerate(coeffs):
+        s = two(X)
         grid = torch.linspace(0, 1, 401, dtype=torch.float64, device=X.device) * s
         steep = torch.maximum((a + 3 * b * grid ** 2 + 5 * c * grid ** 4).abs().max(), (a + b * grid ** 2 + c * grid ** 4).abs().max())
-        here = 2.0 ** -17 * torch.linalg.vector_norm(X) * (abs(a) + 3 * abs(b) * s ** 2 + 9 * abs(c) * s ** 4)
-        noise = noise * steep + here
+        here = 2.0 ** -17 * fro(X) * (abs(a) + 3 * abs(b) * s ** 2 + 9 * abs(c) * s ** 4)
         A = X @ X.T if X.shape[0] <= X.shape[1] else X.T @ X
-        Q = a * torch.eye(A.shape[0], dtype=torch.float64, device=X.device) + b * A + c * A @ A
+        eye = torch.eye(A.shape[0], dtype=torch.float64, device=X.device)
+        if out == torch.bfloat16 and i > 0 and i + 1 == len(coeffs) and abs(b + 2 * c) + abs(c) <= 3:
+            u, D = 2.0 ** -11, A - eye
+            E = (b + 2 * c) * D + c * D @ D
+            e = 2 * u * s * fro(X) + u * fro(D)
+            here = here + s * ((abs(b + 2 * c) + 2 * abs(c) * two(D)) * e + u * fro(E)) + two(E) * u * fro(X)
+        noise = noise * steep + here
+        Q = a * eye + b * A + c * A @ A
         X = Q @ X if X.shape[0] <= X.shape[1] else X @ Q
     return scale * X, abs(scale) * float(noise)
