@@ -513,6 +513,25 @@ cudaError_t prepare(const OrthCall& g, const Places& l, double* sums, uint16_t* 
                   static_cast<int>(base && g.cols % 8 == 0));
 }
 
+// Whether the last step may take one fp16 part (see orth_launch): its coefficients, and
+// X's entries inside fp16's range by then: the steps before enlarge small singular values
+// (entries start at 1 / sqrt(rows cols) in the mean square) and take none above 8.
+bool light_last(const OrthCall& g) {
+  const double* last = g.coeffs + 3 * (g.steps - 1);
+  if (g.steps < 2 || fabs(last[1] + 2 * last[2]) + fabs(last[2]) > 3. || g.rows * g.cols > int64_t(1) << 30) return false;
+  double slope = 1., top = 1.;
+  for (int64_t i = 0; i + 1 < g.steps; ++i) {
+    const double *k = g.coeffs + 3 * i, from = top;
+    slope *= fabs(k[0]);
+    top = 0.;
+    for (int j = 1; j <= 64; ++j) {
+      const double s = from * j / 64, v = fabs(s * (k[0] + s * s * (k[1] + s * s * k[2])));
+      if (v > top) top = v;
+    }
+  }
+  return slope >= 2. && top <= 8.;
+}
+
 }  // namespace
 
 size_t orth_ws_bytes(int64_t batch, int64_t rows, int64_t cols) {
@@ -539,8 +558,7 @@ cudaError_t orth_launch(const OrthCall& g) {
   // would be 7 and more), and the first term takes X in two parts.  Emulated in 64 bits it
   // leaves 2e-4 to 4e-4 of a result's size beside the 1.7e-3 of rounding to bf16 (1e-3
   // where X has directions of 1e-5), for a third of the products.
-  const double* last = g.coeffs + 3 * (g.steps - 1);
-  const bool light = g.out_kind == EK_BF16 && g.steps > 1 && fabs(last[1] + 2 * last[2]) + fabs(last[2]) <= 3.;
+  const bool light = g.out_kind == EK_BF16 && light_last(g);
   for (int64_t i = 0; i < g.steps && e == cudaSuccess; ++i) {
     const Matrix &x = X[i & 1], &y = X[(i + 1) & 1];
     const double *k = g.coeffs + 3 * i, s = g.scale;
