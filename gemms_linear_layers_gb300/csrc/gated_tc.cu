@@ -69,6 +69,7 @@ struct GatedFwd {
   using Maps = GatedMaps;
   using Args = GatedArgs;
   using Unit = GatedUnit;
+  using State = pt::NoState;
   static constexpr int PARTS = 1, STAGES = 5, EPI_BLOCKS = 3;
   static constexpr unsigned SITE = 0x50;
   static __device__ __forceinline__ bool a_mn(const Args&, const Unit&, int) { return false; }
@@ -87,8 +88,8 @@ struct GatedFwd {
     tma_load_3d_pair(b_dst, &m.B, bar, kb * pt::BK, c.f0, rank);  // rank 0: gate rows, rank 1: up rows
   }
   template <class Wait, class Release>
-  static __device__ __forceinline__ void epilogue(const Maps& m, const Args& a, const Unit& c, const pt::EpiWarp& at,
-                                                  Wait wait, Release release) {
+  static __device__ __forceinline__ void epilogue(const Maps& m, const Args& a, const Unit& c, const Unit*,
+                                                  const pt::EpiWarp& at, pt::NoState&, Wait wait, Release release) {
     const int lane = threadIdx.x & 31;
     const int row0 = c.m0 + at.rank * 128 + at.q * 32;
     const int rows = static_cast<int>(min(32ll, a.T - row0));
@@ -139,12 +140,20 @@ struct GatedFwd {
   }
 };
 
+// The backward's blocks of G and U are copied into shared memory one 64-column step
+// ahead, across units too, by cp.async: loads into registers would hold lines of L1,
+// of which little is left beside this much shared memory, and came late (4,096 rows,
+// 2,304 -> 5,760: 83 us).  dG and dU take their places; H leaves from registers.
 template <bool F16>
 struct GatedBwd {
   using Maps = GatedMaps;
   using Args = GatedArgs;
   using Unit = GatedUnit;
-  static constexpr int PARTS = 1, STAGES = 5, EPI_BLOCKS = 3;
+  struct State {
+    int slot;      // blocks of the step at work: 2 slot, 2 slot + 1
+    bool fetched;  // its copies have been requested
+  };
+  static constexpr int PARTS = 1, STAGES = 5, EPI_BLOCKS = 4;
   static constexpr unsigned SITE = 0x58;
   static __device__ __forceinline__ bool a_mn(const Args&, const Unit&, int) { return false; }
   static __device__ __forceinline__ bool b_mn(const Args&, const Unit&, int) { return true; }
@@ -161,32 +170,42 @@ struct GatedBwd {
     for (int j = 0; j < chunks64(a); ++j) tma_load_3d_pair(b_dst + j * 8192, &m.B, bar, n + 64 * j, kb * pt::BK, 0);
   }
   template <class Wait, class Release>
-  static __device__ __forceinline__ void epilogue(const Maps& m, const Args& a, const Unit& c, const pt::EpiWarp& at,
-                                                  Wait wait, Release release) {
+  static __device__ __forceinline__ void epilogue(const Maps& m, const Args& a, const Unit& c, const Unit* next,
+                                                  const pt::EpiWarp& at, State& st, Wait wait, Release release) {
     const int lane = threadIdx.x & 31;
-    const int row0 = c.m0 + at.rank * 128 + at.q * 32;
+    const int row_in = at.rank * 128 + at.q * 32;
+    const int row0 = c.m0 + row_in;
     const int rows = static_cast<int>(min(32ll, a.T - row0));
-    uint8_t *bg = at.blocks, *bu = bg + pt::BLOCK, *bh = bu + pt::BLOCK;
-    pt::HalfRegs g, u;
-    auto fetch = [&](int col) {
-      const int f = c.f0 + col + 32 * at.h, cols = static_cast<int>(min(32ll, a.f - f));
-      const uint16_t* p = a.gu_in + static_cast<long long>(row0) * 2 * a.f + f;
-      pt::half_fetch(g, p, 2 * a.f, rows, cols, lane, a.wide);
-      pt::half_fetch(u, p + a.f, 2 * a.f, rows, cols, lane, a.wide);
+    // this warp's half of the G and U of columns col.. of a unit, into slot s
+    auto fetch = [&](const Unit& u, int col, int s) {
+      const int f = u.f0 + col + 32 * at.h, r0 = u.m0 + row_in;
+      const int n = static_cast<int>(min(32ll, a.T - r0)), cols = static_cast<int>(min(32ll, a.f - f));
+      uint8_t *bg = at.blocks + 2 * s * pt::BLOCK, *bu = bg + pt::BLOCK;
+      const bool any = n > 0 && cols > 0;
+      const uint16_t* p = any ? a.gu_in + static_cast<long long>(r0) * 2 * a.f + f : a.gu_in;
+      if (a.wide) {
+        pt::half_copy(bg, at.h, p, 2 * a.f, any ? n : 0, cols, lane);
+        pt::half_copy(bu, at.h, any ? p + a.f : p, 2 * a.f, any ? n : 0, cols, lane);
+      } else {
+        pt::HalfRegs r;
+        pt::half_fetch(r, p, 2 * a.f, any ? n : 0, cols, lane, false);
+        pt::half_put(r, bg, at.h, lane);
+        pt::half_fetch(r, p + a.f, 2 * a.f, any ? n : 0, cols, lane, false);
+        pt::half_put(r, bu, at.h, lane);
+      }
+      pt::copies_commit();
     };
-    fetch(0);
+    if (!st.fetched) fetch(c, 0, st.slot);  // the first unit's
     if (!wait()) return;
 #pragma unroll 1
     for (int col = 0; col < a.width; col += 64) {
       const int mine = col + 32 * at.h;
-      const bool live = rows > 0 && c.f0 + col < a.f;
-      if (live) {
-        pt::blocks_free(at, lane);
-        pt::half_put(g, bg, at.h, lane);
-        pt::half_put(u, bu, at.h, lane);
-        __syncwarp();
-      }
-      if (col + 64 < a.width) fetch(col + 64);
+      uint8_t *bg = at.blocks + 2 * st.slot * pt::BLOCK, *bu = bg + pt::BLOCK;
+      pt::copies_wait();
+      // the other slot's results have been read: the next step's G and U may come there
+      pt::blocks_free(at, lane);
+      if (col + 64 < a.width) fetch(c, col + 64, st.slot ^ 1);
+      else if (next) fetch(*next, 0, st.slot ^ 1);
       float dh[32];
       if (c.kb > 0) {
         tmem_ld_32x32b_x32(at.taddr + mine, reinterpret_cast<uint32_t*>(dh));
@@ -196,7 +215,10 @@ struct GatedBwd {
         for (int j = 0; j < 32; ++j) dh[j] = 0.f;
       }
       if (col + 64 >= a.width) release();
-      if (!live) continue;
+      st.slot ^= 1;
+      if (rows <= 0 || c.f0 + col >= a.f) continue;
+      const int f = c.f0 + mine, cols = static_cast<int>(min(32ll, a.f - f));
+      uint16_t* hrow = a.h + static_cast<long long>(row0 + lane) * a.f + f;
       // eight elements at a time, from the lane's rows of G and U into the same places
       with_act(a.act, [&](auto kind) {
 #pragma unroll
@@ -219,24 +241,29 @@ struct GatedBwd {
           }
           *pg = make_uint4(og[0], og[1], og[2], og[3]);
           *pu = make_uint4(ou[0], ou[1], ou[2], ou[3]);
-          if (a.h)
-            *reinterpret_cast<uint4*>(pt::block_word(bh, lane, 4 * at.h + j)) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+          if (a.h && lane < rows) {
+            if (a.wide) {
+              if (8 * j < cols) *reinterpret_cast<uint4*>(hrow + 8 * j) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if (8 * j + k < cols) hrow[8 * j + k] = static_cast<uint16_t>(oh[k / 2] >> (k & 1 ? 16 : 0));
+            }
+          }
         }
       });
       if (a.wide) {
         if (pt::blocks_full(at, lane)) {
           tma_store_3d(&m.GU, smem_u32(bg), c.f0 + col, row0, 0);
           tma_store_3d(&m.GU, smem_u32(bu), c.f0 + col, row0, 1);
-          if (a.h) tma_store_3d(&m.H, smem_u32(bh), c.f0 + col, row0, 0);
           bulk_commit();
         }
       } else {
-        const int f = c.f0 + mine, cols = static_cast<int>(min(32ll, a.f - f));
         gated_put(bg, at.h, a.gu, 2 * a.f, f, row0, rows, cols, lane);
         gated_put(bu, at.h, a.gu + a.f, 2 * a.f, f, row0, rows, cols, lane);
-        if (a.h) gated_put(bh, at.h, a.h, a.f, f, row0, rows, cols, lane);
       }
     }
+    st.fetched = next != nullptr;
   }
 };
 

@@ -90,6 +90,7 @@ struct OrthProduct {
   using Maps = OrthMaps;
   using Args = OrthArgs;
   using Unit = OrthUnit;
+  using State = pt::NoState;
   static constexpr int A_KIND = A_OP, B_KIND = B_OP, EP_KIND = EP;
   static constexpr bool SYM = EP == EP_A || EP == EP_Q || EP == EP_D || EP == EP_E;
   static constexpr bool RESULT = EP == EP_OUT || EP == EP_LAST;
@@ -169,8 +170,8 @@ struct OrthProduct {
     }
   }
   template <class Wait, class Release>
-  static __device__ __forceinline__ void epilogue(const Maps& m, const Args& a, const Unit& c, const pt::EpiWarp& at,
-                                                  Wait wait, Release release) {
+  static __device__ __forceinline__ void epilogue(const Maps& m, const Args& a, const Unit& c, const Unit*,
+                                                  const pt::EpiWarp& at, pt::NoState&, Wait wait, Release release) {
     constexpr bool IN = EP == EP_Q || EP == EP_E || EP == EP_LAST, IN2 = IN && EP != EP_E;  // reads a matrix, of two parts
     constexpr bool IN16 = EP == EP_E || EP == EP_LAST;                                      // in fp16
     const int lane = threadIdx.x & 31;

@@ -16,13 +16,14 @@
 // P has: Maps, Args (with units, idesc, timeout_ns, status), Unit (with kb, the
 // blocks of its reduction; nmma, its columns), PARTS (1, or 2: operands in two 16-bit
 // parts, a stage holds both of both, and a block is the products hi lo, lo hi and hi
-// hi), STAGES, EPI_BLOCKS (64-column blocks of shared memory a quadrant), and
+// hi), STAGES, EPI_BLOCKS (64-column blocks of shared memory a quadrant), State (what
+// an epilogue warp keeps from unit to unit), and
 //   a_mn(args, unit, kb), b_mn     is the operand of this block MN-major
 //   prefetch(maps, args)           the maps of its operands
 //   unit(args, u, &unit)           false: nothing to do
 //   load(maps, args, unit, kb, rank, a_dst, b_dst, bar)   one block's copies
 //   bytes(args, unit)              that they complete on the barrier, a CTA
-//   epilogue(maps, args, unit, at, wait, release)
+//   epilogue(maps, args, unit, next, at, state, wait, release)   next: the unit after, or null
 // The epilogue calls wait() before it reads the accumulator (false: give up; both
 // warps of a quadrant get the same answer) and release() once it has.
 #pragma once
@@ -63,6 +64,7 @@ struct EpiWarp {
   uint32_t taddr;  // tensor memory: the warp's lanes, first column of the accumulator
   uint8_t* blocks; // the quadrant's shared memory
 };
+struct NoState {};
 // The 64 threads of a quadrant's two warps.
 __device__ __forceinline__ void quadrant_sync(int q) { asm volatile("bar.sync %0, 64;" ::"r"(q + 1) : "memory"); }
 __device__ __forceinline__ bool quadrant_all(int q, bool ok) {
@@ -242,9 +244,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tempty_cl = mapa_shared(smem_u32(&tempty[0]), 0);
     int acc = 0;
     uint32_t acc_phase = 0;
-    typename P::Unit c;
+    typename P::State state = {};
+    typename P::Unit c, next;
     for (int u = pair_index(); u < args.units; u += pair_count()) {
       if (!P::unit(args, u, c)) continue;
+      const bool more = u + pair_count() < args.units && P::unit(args, u + pair_count(), next);
       at.taddr = tmem_base + (static_cast<uint32_t>(at.q * 32) << 16) + static_cast<uint32_t>(acc * 256);
       bool ok = true;
       auto wait = [&] {
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(tempty_cl + static_cast<uint32_t>(acc * 8));
       };
-      P::epilogue(maps, args, c, at, wait, release);
+      P::epilogue(maps, args, c, more ? &next : nullptr, at, state, wait, release);
       if (!ok) break;
       if (c.kb > 0 && ++acc == 2) {
         acc = 0;
@@ -365,6 +369,24 @@ __device__ __forceinline__ void half_fetch(HalfRegs& r, const uint16_t* p, long 
       }
     }
   }
+}
+// The same straight into the block, asynchronously (words 16 bytes each; outside: zeros).
+__device__ __forceinline__ void half_copy(uint8_t* block, int h, const uint16_t* p, long long pitch, int rows, int cols,
+                                          int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 8 * i + (lane >> 2), c = (lane & 3) * 8;
+    const bool in = row < rows && c < cols;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(block_word(block, row, 4 * h + (lane & 3)))),
+                 "l"(in ? p + row * pitch + c : p), "r"(in ? 16 : 0)
+                 : "memory");
+  }
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// The warp's copies have landed, for all its lanes.
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncwarp();
 }
 __device__ __forceinline__ void half_put(const HalfRegs& r, uint8_t* block, int h, int lane) {
 #pragma unroll
