@@ -906,11 +906,12 @@ ORTH_QUINTIC = (3.4445, -4.7750, 2.0315)
 @functools.lru_cache(maxsize=64)
 def _orth_coeffs(coeffs, steps):
     """(host array, steps) of one triple for all steps or of a triple for each."""
-    flat = [float(x) for c in coeffs for x in (c if isinstance(c, tuple) else (c,))]
-    one = not isinstance(coeffs[0], tuple)
+    one = bool(coeffs) and not any(isinstance(c, tuple) for c in coeffs)
     n = (5 if one else len(coeffs)) if steps is None else steps
-    if len(flat) != 3 * (1 if one else n):
+    triples = (coeffs,) if one else coeffs
+    if len(triples) != (1 if one else n) or not triples or any(not isinstance(c, tuple) or len(c) != 3 for c in triples):
         raise ValueError("coeffs must be (a, b, c), or such a triple for each step")
+    flat = [float(x) for c in triples for x in c]
     flat = flat * n if one else flat
     return (ctypes.c_double * len(flat))(*flat), n
 
