@@ -2079,6 +2079,7 @@ tg_status tg_orthogonalize(const void* G, void* O, int64_t batch, int64_t rows, 
   if (batch < 0 || rows < 0 || cols < 0 || !orth_sizes_ok(batch, rows, cols)) return TG_ERR_INVALID_ARG;
   if (steps < 1 || steps > 64 || coeffs == nullptr || !std::isfinite(scale) || !std::isfinite(eps) || eps < 0.f)
     return TG_ERR_INVALID_ARG;
+  if (!orth_fits(batch, rows, cols, steps)) return TG_ERR_INVALID_ARG;
   for (int64_t i = 0; i < 3 * steps; ++i)
     if (!std::isfinite(static_cast<float>(coeffs[i]))) return TG_ERR_INVALID_ARG;
   const int64_t n = batch * rows * cols;

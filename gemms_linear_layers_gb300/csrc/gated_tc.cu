@@ -72,6 +72,10 @@ struct GatedFwd {
   using State = pt::NoState;
   static constexpr int PARTS = 1, STAGES = 5, EPI_BLOCKS = 3;
   static constexpr unsigned SITE = 0x50;
+  static constexpr bool COOPERATIVE = false;
+  static __device__ __forceinline__ int parts(const Args&, const Unit&) { return 1; }
+  static __device__ __forceinline__ uint32_t idesc(const Args& a, const Unit&) { return a.idesc; }
+  static __device__ __forceinline__ bool ready(const Args&, const Unit&, volatile int*) { return true; }
   static __device__ __forceinline__ bool a_mn(const Args&, const Unit&, int) { return false; }
   static __device__ __forceinline__ bool b_mn(const Args&, const Unit&, int) { return false; }
   static __device__ __forceinline__ void prefetch(const Maps& m, const Args& a) {
@@ -155,6 +159,10 @@ struct GatedBwd {
   };
   static constexpr int PARTS = 1, STAGES = 5, EPI_BLOCKS = 4;
   static constexpr unsigned SITE = 0x58;
+  static constexpr bool COOPERATIVE = false;
+  static __device__ __forceinline__ int parts(const Args&, const Unit&) { return 1; }
+  static __device__ __forceinline__ uint32_t idesc(const Args& a, const Unit&) { return a.idesc; }
+  static __device__ __forceinline__ bool ready(const Args&, const Unit&, volatile int*) { return true; }
   static __device__ __forceinline__ bool a_mn(const Args&, const Unit&, int) { return false; }
   static __device__ __forceinline__ bool b_mn(const Args&, const Unit&, int) { return true; }
   static __device__ __forceinline__ void prefetch(const Maps& m, const Args& a) { GatedFwd<F16>::prefetch(m, a); }

@@ -19,6 +19,8 @@ struct OrthCall {
   cudaStream_t stream;
 };
 
+// Whether the tiles of a call can be counted (2^30 in all, 2^27 of a matrix).
+bool orth_fits(int64_t batch, int64_t rows, int64_t cols, int64_t steps);
 size_t orth_ws_bytes(int64_t batch, int64_t rows, int64_t cols);
 cudaError_t orth_launch(const OrthCall& g);
 

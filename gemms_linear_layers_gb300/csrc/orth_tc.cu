@@ -32,11 +32,12 @@ namespace {
 enum {
   EP_A = 0,     // A                                    two bf16 parts, symmetric
   EP_Q = 1,     // Q = a I + b A + c sum                two bf16 parts, symmetric
-  EP_X = 2,     // X                                    two parts, bf16 or fp16
+  EP_X = 2,     // X                                    two bf16 parts
   EP_OUT = 3,   // scale X                              the result
   EP_D = 4,     // D = sum - I                          one fp16 part, symmetric
   EP_E = 5,     // E = (b + 2 c) D + c sum              one fp16 part, symmetric
-  EP_LAST = 6   // scale ((a + b + c) X + sum)          the result; X two fp16 parts
+  EP_LAST = 6,  // scale ((a + b + c) X + sum)          the result; X two fp16 parts
+  EP_X16 = 7    // X for EP_D and EP_LAST               two fp16 parts
 };
 
 // How an operand lies in memory.  OP_SYM: a symmetric matrix stored in part.  Row
@@ -47,26 +48,44 @@ enum {
 // are narrow in N and not mostly empty in M.
 enum { OP_K = 0, OP_MN = 1, OP_SYM = 2 };
 
+// All products of a call are one launch.  A unit is a tile of a product of a matrix; the
+// units go product by product and, within one, matrix by matrix, dealt to the pairs in
+// turn.  A matrix's next product begins when every tile of its last one has been stored
+// (a counter of each matrix, in the workspace), whatever the other matrices are at, so
+// only a batch of one waits at a product's end.  (With a launch a product, 24 matrices of
+// 576 x 576 took 345 us.)  A unit waits for units before it only, and the launch is
+// cooperative, so every wait ends.
 struct OrthMaps {
-  CUtensorMap A[2], B[2], C;  // operands: K-major boxes, MN-major boxes
+  // X (two buffers), A or D, Q or E, as loaded: K-major boxes of 128 rows, of half a tile's rows, MN-major boxes
+  CUtensorMap k[4], kb[4], mn[4];
+  CUtensorMap store[5];  // as stored, and the result
 };
+enum { BUF_S = 2, BUF_Q = 3, BUF_O = 4 };  // 0, 1: X
+
+constexpr int MAX_STEPS = 64;
 struct OrthArgs {
-  const uint16_t* in;  // EP_Q: A; EP_E: D; EP_LAST: X
-  uint16_t* o;         // EP_OUT, EP_LAST
-  long long in_pitch, in_part, in_matrix;  // elements from row to row, part to part, matrix to matrix
-  int M, N;            // rows and columns of a result
-  int batch, kbs, units, per, m_tiles, n_tiles, width;
-  int strip;           // OP_SYM operands
-  int main_units, out_strip;  // symmetric results: units before the strip's, first column of it
-  float a, b, c;       // EP_Q: coefficients; EP_E: b, c; results: the factors of the sum (c) and of X (a)
+  const uint16_t* buf[4];
+  int* done;           // [batch] blocks of 32 rows of tiles that have been stored: 8 a unit
+  uint16_t* o;
+  long long x_pitch, x_part, s_pitch, s_part;  // elements from row to row, part to part
+  int rows, cols, m;   // of X; min(rows, cols)
+  int batch, steps, units;
+  int light;           // the last step on one fp16 part
+  int sym_units, x_units;  // of a matrix: of a symmetric product, of the product with X
+  int sym_main, sym_tiles_n, x_tiles_m, x_tiles_n, width;
+  int strip;
+  int kb_gram, kb_m;   // blocks of the reductions
   int wide, out_f16;
-  uint32_t idesc;
+  float scale;
   unsigned long long timeout_ns;
   unsigned int* status;
+  float coeffs[MAX_STEPS][3];
 };
 struct OrthUnit {
+  int step, kind;  // kind 0: A, 1: Q, 2: X
   int z, m0, n0, kb, nmma;
-  int cols;  // that are stored (from n0 on, before clipping)
+  int cols;        // that are stored (from n0 on)
+  bool last;       // step
 };
 
 __device__ __forceinline__ void split2(float v, float* hi, float* lo) {
@@ -77,6 +96,11 @@ __device__ __forceinline__ void split2h(float v, float* hi, float* lo) {
   *hi = __half2float(__float2half_rn(v));
   *lo = v - *hi;
 }
+__device__ __forceinline__ int count_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 
 // Column tiles of a symmetric result's row tile i.
 __host__ __device__ inline int sym_tiles(int i, int n_tiles, int width) {
@@ -85,179 +109,259 @@ __host__ __device__ inline int sym_tiles(int i, int n_tiles, int width) {
 }
 __host__ __device__ inline int up64(int n) { return (n + 63) / 64 * 64; }
 
-template <int A_OP, int B_OP, int EP, bool X16 = false>
-struct OrthProduct {
+template <bool TALL>
+struct OrthChain {
   using Maps = OrthMaps;
   using Args = OrthArgs;
   using Unit = OrthUnit;
   using State = pt::NoState;
-  static constexpr int A_KIND = A_OP, B_KIND = B_OP, EP_KIND = EP;
-  static constexpr bool SYM = EP == EP_A || EP == EP_Q || EP == EP_D || EP == EP_E;
-  static constexpr bool RESULT = EP == EP_OUT || EP == EP_LAST;
-  static constexpr int PARTS = EP >= EP_D ? 1 : 2;
-  static constexpr int OUT_PARTS = RESULT || PARTS == 1 ? 1 : 2;
-  static constexpr int STAGES = PARTS == 2 ? 3 : 6, EPI_BLOCKS = 2;
+  static constexpr bool COOPERATIVE = true;
+  static constexpr int PARTS = 2, STAGES = 3, EPI_BLOCKS = 2;
   static constexpr unsigned SITE = 0x60;
+
+  static __device__ __forceinline__ bool light(const Args& a, const Unit& c) { return a.light && c.last; }
+  static __device__ __forceinline__ int parts(const Args& a, const Unit& c) { return light(a, c) ? 1 : 2; }
+  static __device__ __forceinline__ uint32_t idesc(const Args& a, const Unit& c) {
+    return idesc_f16(!light(a, c), false, false, 256, 0);
+  }
+  // How the operands of a product lie, and the buffers they are in.
+  static __device__ __forceinline__ int a_op(const Unit& c) { return c.kind == 0 ? (TALL ? OP_MN : OP_K) : c.kind == 1 ? OP_SYM : TALL ? OP_K : OP_SYM; }
+  static __device__ __forceinline__ int b_op(const Unit& c) { return c.kind == 0 ? (TALL ? OP_MN : OP_K) : c.kind == 1 ? OP_SYM : TALL ? OP_SYM : OP_MN; }
+  static __device__ __forceinline__ int a_buf(const Unit& c) { return c.kind == 0 ? c.step & 1 : c.kind == 1 ? BUF_S : TALL ? c.step & 1 : BUF_Q; }
+  static __device__ __forceinline__ int b_buf(const Unit& c) { return c.kind == 0 ? c.step & 1 : c.kind == 1 ? BUF_S : TALL ? BUF_Q : c.step & 1; }
+  static __device__ __forceinline__ int c_buf(const Unit& c) { return c.kind == 0 ? BUF_S : c.kind == 1 ? BUF_Q : c.last ? BUF_O : (c.step + 1) & 1; }
+
   static __device__ __forceinline__ bool mn(const Args& a, int op, int row, int k0) {
     if (op != OP_SYM) return op == OP_MN;
     if (row >= a.strip) return k0 < a.strip;
     return k0 < a.strip && k0 >= ((row >> 8) + 1) << 8;
   }
-  static __device__ __forceinline__ bool a_mn(const Args& a, const Unit& c, int kb) { return mn(a, A_OP, c.m0, kb * pt::BK); }
-  static __device__ __forceinline__ bool b_mn(const Args& a, const Unit& c, int kb) { return mn(a, B_OP, c.n0, kb * pt::BK); }
+  static __device__ __forceinline__ bool a_mn(const Args& a, const Unit& c, int kb) { return mn(a, a_op(c), c.m0, kb * pt::BK); }
+  static __device__ __forceinline__ bool b_mn(const Args& a, const Unit& c, int kb) { return mn(a, b_op(c), c.n0, kb * pt::BK); }
   static __device__ __forceinline__ void prefetch(const Maps& m, const Args&) {
-    prefetch_tmap(&m.A[A_OP == OP_MN]);
-    prefetch_tmap(&m.B[B_OP == OP_MN]);
+    prefetch_tmap(TALL ? &m.mn[0] : &m.k[0]);
+    prefetch_tmap(TALL ? &m.mn[0] : &m.kb[0]);
   }
   static __device__ __forceinline__ bool unit(const Args& a, int u, Unit& c) {
-    c.kb = a.kbs;
-    if (SYM && u >= a.main_units) {  // the strip: a tile of every row tile
-      u -= a.main_units;
-      c.z = u / a.m_tiles;
-      c.m0 = (u - c.z * a.m_tiles) * 256;
-      c.n0 = a.out_strip;
-      c.cols = a.N - a.out_strip;
-      c.nmma = up64(c.cols);
-      return true;
-    }
-    c.z = u / a.per;
-    int r = u - c.z * a.per;
-    if (SYM) {
+    const int sym = a.sym_units * a.batch, step = 2 * sym + a.x_units * a.batch;
+    c.step = u / step;
+    int r = u - c.step * step;
+    c.kind = r < sym ? 0 : r < 2 * sym ? 1 : 2;
+    r -= c.kind * sym;
+    c.last = c.step + 1 == a.steps;
+    const int per = c.kind < 2 ? a.sym_units : a.x_units;
+    c.z = r / per;
+    r -= c.z * per;
+    c.kb = c.kind == 0 ? a.kb_gram : a.kb_m;
+    if (c.kind < 2) {
+      if (r >= a.sym_main) {  // the strip: a tile of every row tile
+        c.m0 = (r - a.sym_main) * 256;
+        c.n0 = a.strip;
+        c.cols = a.m - a.strip;
+        c.nmma = up64(c.cols);
+        return true;
+      }
       int i = 0;
-      for (int n; r >= (n = sym_tiles(i, a.n_tiles, a.width)); ++i) r -= n;
+      for (int n; r >= (n = sym_tiles(i, a.sym_tiles_n, a.width)); ++i) r -= n;
       c.m0 = i * 256;
       c.n0 = r * a.width;
-      c.cols = min(a.width, c.m0 + 256 - c.n0);
+      c.cols = min(min(a.width, c.m0 + 256 - c.n0), a.m - c.n0);
+      c.nmma = up64(min(a.width, a.m - c.n0));
     } else {
-      const int j = r / a.m_tiles;
-      c.m0 = (r - j * a.m_tiles) * 256;
+      const int N = TALL ? a.m : a.cols, j = r / a.x_tiles_m;
+      c.m0 = (r - j * a.x_tiles_m) * 256;
       c.n0 = j * a.width;
-      c.cols = a.width;
+      c.cols = min(a.width, N - c.n0);
+      c.nmma = up64(c.cols);
     }
-    c.cols = min(c.cols, a.N - c.n0);
-    c.nmma = up64(min(a.width, a.N - c.n0));
+    return true;
+  }
+  // Units of this matrix that come before the product, times 8.
+  static __device__ __forceinline__ int target(const Args& a, const Unit& c) {
+    return 8 * (c.step * (2 * a.sym_units + a.x_units) + c.kind * a.sym_units);
+  }
+  static __device__ __forceinline__ bool ready(const Args& a, const Unit& c, volatile int* abort_flag) {
+    const int want = target(a, c);
+    if (want == 0) return true;
+    const int* p = a.done + c.z;
+    if (count_acquire(p) < want) {
+      const uint64_t t0 = globaltimer_ns();
+      for (uint32_t it = 1; count_acquire(p) < want; ++it) {
+        if ((it & 31u) == 0u) {
+          if (*abort_flag) return false;
+          __nanosleep(20);
+          if (globaltimer_ns() - t0 > a.timeout_ns) {
+            *abort_flag = 1;
+            atomicOr(a.status, TG_DEVSTAT_TIMEOUT | (SITE & TG_DEVSTAT_SITE_MASK));
+            return false;
+          }
+        }
+      }
+    }
+    asm volatile("fence.proxy.async;" ::: "memory");  // the copies that follow see what the counter stands for
     return true;
   }
   // Boxes of a K-major B hold half a whole tile's rows.  One that may be either way comes
   // in whole 64 x 64 boxes, so that its bytes are the same.
-  static __host__ __device__ __forceinline__ int b_rows(const Args& a) {
-    return B_OP == OP_K ? a.width / 2 : up64(a.width / 2);
-  }
-  static __device__ __forceinline__ uint32_t bytes(const Args& a, const Unit&) {
-    return PARTS * (pt::A_BYTES + b_rows(a) * pt::BK * 2);
+  static __device__ __forceinline__ int b_rows(const Args& a, int op) { return op == OP_K ? a.width / 2 : up64(a.width / 2); }
+  static __device__ __forceinline__ uint32_t bytes(const Args& a, const Unit& c) {
+    return parts(a, c) * (pt::A_BYTES + b_rows(a, b_op(c)) * pt::BK * 2);
   }
   static __device__ __forceinline__ void load(const Maps& m, const Args& a, const Unit& c, int kb, int rank,
                                               uint32_t a_dst, uint32_t b_dst, uint32_t bar) {
     const int k0 = kb * pt::BK;
     const int mrow = c.m0 + rank * 128, n = c.n0 + rank * (c.nmma / 2);
-    const bool am = mn(a, A_OP, c.m0, k0), bm = mn(a, B_OP, c.n0, k0);
-#pragma unroll
-    for (int p = 0; p < PARTS; ++p) {
+    const bool am = a_mn(a, c, kb), bm = b_mn(a, c, kb);
+    const int ab = a_buf(c), bb = b_buf(c), op = b_op(c), rows = b_rows(a, op), np = parts(a, c);
+    for (int p = 0; p < np; ++p) {
       const int z = c.z + p * a.batch;
       if (am) {
-        tma_load_3d_pair(a_dst, &m.A[1], bar, mrow, k0, z);
-        tma_load_3d_pair(a_dst + 8192, &m.A[1], bar, mrow + 64, k0, z);
+        tma_load_3d_pair(a_dst, &m.mn[ab], bar, mrow, k0, z);
+        tma_load_3d_pair(a_dst + 8192, &m.mn[ab], bar, mrow + 64, k0, z);
       } else {
-        tma_load_3d_pair(a_dst, &m.A[0], bar, k0, mrow, z);
+        tma_load_3d_pair(a_dst, &m.k[ab], bar, k0, mrow, z);
       }
       if (bm) {
-        for (int j = 0; j < b_rows(a); j += 64) tma_load_3d_pair(b_dst + j * 128, &m.B[1], bar, n + j, k0, z);
+        for (int j = 0; j < rows; j += 64) tma_load_3d_pair(b_dst + j * 128, &m.mn[bb], bar, n + j, k0, z);
       } else {
-        tma_load_3d_pair(b_dst, &m.B[0], bar, k0, n, z);
+        tma_load_3d_pair(b_dst, &m.kb[bb], bar, k0, n, z);
       }
       a_dst += pt::A_BYTES;
       b_dst += pt::B_BYTES;
     }
   }
+
+  // What EP makes of the accumulator's 64 columns from `col` on, into the quadrant's blocks.
+  template <int EP>
+  static __device__ __forceinline__ void finish(const Args& a, const Unit& c, const pt::EpiWarp& at, int col, int row0,
+                                                int rows, int lane, float* v) {
+    constexpr bool IN = EP == EP_Q || EP == EP_E || EP == EP_LAST, IN2 = IN && EP != EP_E;  // reads a matrix, of two parts
+    constexpr bool IN16 = EP == EP_E || EP == EP_LAST;                                      // in fp16
+    uint8_t *b0 = at.blocks, *b1 = b0 + pt::BLOCK;
+    const int n = c.n0 + col + 32 * at.h;
+    const int diagonal = row0 + lane - n;
+    const float *k = a.coeffs[c.step];
+    if constexpr (IN) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 h = *reinterpret_cast<uint4*>(pt::block_word(b0, lane, 4 * at.h + j));
+        uint4 l = make_uint4(0, 0, 0, 0);
+        if (IN2) l = *reinterpret_cast<uint4*>(pt::block_word(b1, lane, 4 * at.h + j));
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          float2 x = pt::unpack16<IN16>(reinterpret_cast<const uint32_t*>(&h)[w]);
+          if (IN2) {
+            const float2 y = pt::unpack16<IN16>(reinterpret_cast<const uint32_t*>(&l)[w]);
+            x.x += y.x;
+            x.y += y.y;
+          }
+          const int e = 8 * j + 2 * w;
+          if constexpr (EP == EP_Q) {
+            v[e] = fmaf(k[2], v[e], fmaf(k[1], x.x, e == diagonal ? k[0] : 0.f));
+            v[e + 1] = fmaf(k[2], v[e + 1], fmaf(k[1], x.y, e + 1 == diagonal ? k[0] : 0.f));
+          } else {  // the last step's coefficients are (a + b + c, b + 2 c, c)
+            const float of_sum = EP == EP_E ? k[2] : a.scale, of_in = EP == EP_E ? k[1] : a.scale * k[0];
+            v[e] = fmaf(of_sum, v[e], of_in * x.x);
+            v[e + 1] = fmaf(of_sum, v[e + 1], of_in * x.y);
+          }
+        }
+      }
+    } else if constexpr (EP == EP_D) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] -= j == diagonal ? 1.f : 0.f;
+    } else if constexpr (EP == EP_OUT) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] *= a.scale;
+    }
+    if constexpr (EP == EP_OUT || EP == EP_LAST) {
+      if (a.out_f16) pt::put_row<true>(b0, lane, at.h, v);
+      else pt::put_row<false>(b0, lane, at.h, v);
+      if (!a.wide)
+        pt::half_store(b0, at.h, a.o + (static_cast<long long>(c.z) * a.rows + row0) * a.cols + n, a.cols, rows,
+                       min(32, a.cols - n), lane);
+    } else if constexpr (EP == EP_D || EP == EP_E) {
+      pt::put_row<true>(b0, lane, at.h, v);
+    } else {
+      float lo[32];
+      constexpr bool X16 = EP == EP_X16;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if constexpr (X16) split2h(v[j], &v[j], &lo[j]);
+        else split2(v[j], &v[j], &lo[j]);
+      pt::put_row<X16>(b0, lane, at.h, v);
+      pt::put_row<X16>(b1, lane, at.h, lo);
+    }
+  }
   template <class Wait, class Release>
   static __device__ __forceinline__ void epilogue(const Maps& m, const Args& a, const Unit& c, const Unit*,
                                                   const pt::EpiWarp& at, pt::NoState&, Wait wait, Release release) {
-    constexpr bool IN = EP == EP_Q || EP == EP_E || EP == EP_LAST, IN2 = IN && EP != EP_E;  // reads a matrix, of two parts
-    constexpr bool IN16 = EP == EP_E || EP == EP_LAST;                                      // in fp16
     const int lane = threadIdx.x & 31;
+    const bool thin = light(a, c);
+    const int ep = c.kind == 0 ? (thin ? EP_D : EP_A) : c.kind == 1 ? (thin ? EP_E : EP_Q)
+                   : thin ? EP_LAST : c.last ? EP_OUT : a.light && c.step + 2 == a.steps ? EP_X16 : EP_X;
+    const bool in = ep == EP_Q || ep == EP_E || ep == EP_LAST, in2 = in && ep != EP_E;
+    const bool result = c.kind == 2 && c.last;
+    const bool two = !thin && !result;
+    const int M = c.kind == 2 && TALL ? a.rows : a.m;
     const int row0 = c.m0 + at.rank * 128 + at.q * 32;
-    const int rows = min(32, a.M - row0);
+    const int rows = min(32, M - row0);
     const int cols = rows > 0 ? c.cols : 0;
     uint8_t *b0 = at.blocks, *b1 = b0 + pt::BLOCK;
     pt::HalfRegs in0, in1;
+    // what the polynomial and the last step add: A or D, or X
+    const bool of_x = c.kind == 2;
+    const uint16_t* from = a.buf[of_x ? c.step & 1 : BUF_S];
+    const long long pitch = of_x ? a.x_pitch : a.s_pitch, part = of_x ? a.x_part : a.s_part;
+    const int N = of_x ? a.cols : a.m;
     auto fetch = [&](int col) {
       const int n = c.n0 + col + 32 * at.h;
-      const int left = (a.N - n + 7) & ~7;  // rows are whole words; what lies past the columns is not stored
-      const uint16_t* p = a.in + c.z * a.in_matrix + row0 * a.in_pitch + n;
-      pt::half_fetch(in0, p, a.in_pitch, rows, left, lane, true);
-      if (IN2) pt::half_fetch(in1, p + a.in_part, a.in_pitch, rows, left, lane, true);
+      const int left = (N - n + 7) & ~7;  // rows are whole words; what lies past the columns is not stored
+      const uint16_t* p = from + (static_cast<long long>(c.z) * (of_x ? a.rows : a.m) + row0) * pitch + n;
+      pt::half_fetch(in0, p, pitch, rows, left, lane, true);
+      if (in2) pt::half_fetch(in1, p + part, pitch, rows, left, lane, true);
     };
-    if (IN && cols > 0) fetch(0);
     if (!wait()) return;
+    // what this unit's copies waited for has been stored; its lines are taken past L1
+    if (in && cols > 0) {
+      count_acquire(a.done + c.z);
+      fetch(0);
+    }
     if (cols <= 0) release();
 #pragma unroll 1
     for (int col = 0; col < cols; col += 64) {
-      const int mine = col + 32 * at.h, n = c.n0 + mine;
       float v[32];
-      tmem_ld_32x32b_x32(at.taddr + mine, reinterpret_cast<uint32_t*>(v));
+      tmem_ld_32x32b_x32(at.taddr + col + 32 * at.h, reinterpret_cast<uint32_t*>(v));
       tmem_ld_wait();
       if (col + 64 >= cols) release();
       pt::blocks_free(at, lane);
-      const int diagonal = row0 + lane - n;
-      if constexpr (IN) {
+      if (in) {
         pt::half_put(in0, b0, at.h, lane);
-        if (IN2) pt::half_put(in1, b1, at.h, lane);
+        if (in2) pt::half_put(in1, b1, at.h, lane);
         __syncwarp();
         if (col + 64 < cols) fetch(col + 64);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 h = *reinterpret_cast<uint4*>(pt::block_word(b0, lane, 4 * at.h + j));
-          uint4 l = make_uint4(0, 0, 0, 0);
-          if (IN2) l = *reinterpret_cast<uint4*>(pt::block_word(b1, lane, 4 * at.h + j));
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float2 x = pt::unpack16<IN16>(reinterpret_cast<const uint32_t*>(&h)[k]);
-            if (IN2) {
-              const float2 y = pt::unpack16<IN16>(reinterpret_cast<const uint32_t*>(&l)[k]);
-              x.x += y.x;
-              x.y += y.y;
-            }
-            const int e = 8 * j + 2 * k;
-            if constexpr (EP == EP_Q) {
-              v[e] = fmaf(a.c, v[e], fmaf(a.b, x.x, e == diagonal ? a.a : 0.f));
-              v[e + 1] = fmaf(a.c, v[e + 1], fmaf(a.b, x.y, e + 1 == diagonal ? a.a : 0.f));
-            } else {
-              const float by = EP == EP_E ? a.b : a.a;
-              v[e] = fmaf(a.c, v[e], by * x.x);
-              v[e + 1] = fmaf(a.c, v[e + 1], by * x.y);
-            }
-          }
-        }
-      } else if constexpr (EP == EP_D) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] -= j == diagonal ? 1.f : 0.f;
-      } else if constexpr (EP == EP_OUT) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] *= a.c;
       }
-      if constexpr (RESULT) {
-        if (a.out_f16) pt::put_row<true>(b0, lane, at.h, v);
-        else pt::put_row<false>(b0, lane, at.h, v);
-        if (!a.wide) {
-          pt::half_store(b0, at.h, a.o + (static_cast<long long>(c.z) * a.M + row0) * a.N + n, a.N, rows, min(32, a.N - n), lane);
-          continue;
-        }
-      } else if constexpr (OUT_PARTS == 1) {
-        pt::put_row<true>(b0, lane, at.h, v);
-      } else {
-        float lo[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if constexpr (X16) split2h(v[j], &v[j], &lo[j]);
-          else split2(v[j], &v[j], &lo[j]);
-        pt::put_row<X16>(b0, lane, at.h, v);
-        pt::put_row<X16>(b1, lane, at.h, lo);
+      switch (ep) {
+        case EP_A: finish<EP_A>(a, c, at, col, row0, rows, lane, v); break;  // (EP_X is the same)
+        case EP_X: finish<EP_A>(a, c, at, col, row0, rows, lane, v); break;
+        case EP_Q: finish<EP_Q>(a, c, at, col, row0, rows, lane, v); break;
+        case EP_OUT: finish<EP_OUT>(a, c, at, col, row0, rows, lane, v); break;
+        case EP_D: finish<EP_D>(a, c, at, col, row0, rows, lane, v); break;
+        case EP_E: finish<EP_E>(a, c, at, col, row0, rows, lane, v); break;
+        case EP_X16: finish<EP_X16>(a, c, at, col, row0, rows, lane, v); break;
+        default: finish<EP_LAST>(a, c, at, col, row0, rows, lane, v); break;
       }
+      if (result && !a.wide) continue;
       if (pt::blocks_full(at, lane)) {
-        tma_store_3d(&m.C, smem_u32(b0), c.n0 + col, row0, c.z);
-        if (OUT_PARTS == 2) tma_store_3d(&m.C, smem_u32(b1), c.n0 + col, row0, c.z + a.batch);
+        const CUtensorMap* to = &m.store[c_buf(c)];
+        tma_store_3d(to, smem_u32(b0), c.n0 + col, row0, c.z);
+        if (two) tma_store_3d(to, smem_u32(b1), c.n0 + col, row0, c.z + a.batch);
         bulk_commit();
       }
+    }
+    if (!result && at.h == 0 && lane == 0) {  // the thread that stored this quadrant's rows
+      bulk_wait_all();
+      asm volatile("fence.proxy.async;" ::: "memory");
+      asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(a.done + c.z) : "memory");
     }
   }
 };
@@ -340,11 +444,12 @@ __global__ void __launch_bounds__(NORM_THREADS) orth_norm_kernel(const T* __rest
 template <typename T>
 __global__ void __launch_bounds__(256) orth_split_kernel(const T* G, const double* part, uint16_t* X, long long rows, int cols,
                                                          int pitch, int parts, int blocks, long long part_stride, float eps,
-                                                         int wide) {
+                                                         int wide, int* done) {
   __shared__ float factor[2];
   pdl_wait();
   const long long z = blockIdx.x / blocks;
   const int k = static_cast<int>(blockIdx.x - z * blocks);
+  if (k == 0 && threadIdx.x == 0) done[z] = 0;
   if (threadIdx.x < 32) {
     double sum = 0.;
     for (int i = threadIdx.x; i < parts; i += 32) sum += part[z * parts + i];
@@ -387,7 +492,7 @@ struct Places {
   int64_t m, long_side, pitch_x, pitch_s;
   int64_t x_part, s_part;  // elements of one part of X, of A or Q
   int parts;
-  size_t x[2], s, q, sums, bytes;  // offsets
+  size_t x[2], s, q, sums, done, bytes;  // offsets
 };
 Places places(int64_t batch, int64_t rows, int64_t cols) {
   Places l;
@@ -410,15 +515,10 @@ Places places(int64_t batch, int64_t rows, int64_t cols) {
   l.s = take(4 * l.s_part);
   l.q = take(4 * l.s_part);
   l.sums = take(8 * static_cast<size_t>(batch) * l.parts);
+  l.done = take(4 * static_cast<size_t>(batch));
   l.bytes = at;
   return l;
 }
-
-// One operand or result: two parts of [batch][rows][pitch].
-struct Matrix {
-  void* p;
-  int64_t rows, cols, pitch;
-};
 
 // First column of a symmetric matrix's strip (m when it has none).
 int strip_of(int64_t m) {
@@ -426,79 +526,67 @@ int strip_of(int64_t m) {
   return static_cast<int>(m > 256 && rest > 0 && rest <= 128 ? m - rest : m);
 }
 
-template <class P>
-cudaError_t product(const OrthCall& g, const Matrix& A, const Matrix& B, const Matrix& C, OrthArgs a) {
+template <bool TALL>
+cudaError_t chain(const OrthCall& g, const Places& l, OrthArgs a) {
+  using P = OrthChain<TALL>;
   OrthMaps m = {};
-  a.M = static_cast<int>(C.rows);
-  a.N = static_cast<int>(C.cols);
-  a.batch = static_cast<int>(g.batch);
-  a.m_tiles = (a.M + 255) / 256;
-  const int64_t K = P::A_KIND == OP_MN ? A.rows : A.cols;
-  a.kbs = static_cast<int>((K + pt::BK - 1) / pt::BK);
-  constexpr bool strips = P::SYM || P::A_KIND == OP_SYM || P::B_KIND == OP_SYM;
-  a.strip = strip_of(P::SYM ? a.N : P::A_KIND == OP_SYM ? A.rows : B.rows);
-  a.out_strip = a.strip;
-  const bool split = strips && a.strip % 256 == 0 && a.strip < (P::SYM ? a.N : P::A_KIND == OP_SYM ? A.rows : B.rows);
-  const int main_cols = P::SYM ? a.strip : a.N, main_rows = P::SYM && split ? a.strip / 256 : a.m_tiles;
+  const int pairs = g.num_sms / 2, mt = (a.m + 255) / 256;
+  a.strip = strip_of(a.m);
+  const bool split = a.strip < a.m;
+  const int main_rows = split ? a.strip / 256 : mt, rest = up64(a.m - a.strip);
+  a.x_tiles_m = TALL ? (a.rows + 255) / 256 : mt;
   auto fit = [&](int w) {
     a.width = w;
-    a.n_tiles = (main_cols + w - 1) / w;
-    a.per = 0;
-    if (P::SYM)
-      for (int i = 0; i < main_rows; ++i) a.per += sym_tiles(i, a.n_tiles, w);
-    else
-      a.per = a.m_tiles * a.n_tiles;
-    a.main_units = a.per * a.batch;
-    a.units = a.main_units + (P::SYM && split ? a.m_tiles * a.batch : 0);
+    a.sym_tiles_n = (a.strip + w - 1) / w;
+    a.sym_main = 0;
+    for (int i = 0; i < main_rows; ++i) a.sym_main += sym_tiles(i, a.sym_tiles_n, w);
+    a.sym_units = a.sym_main + (split ? mt : 0);
+    a.x_tiles_n = ((TALL ? a.m : a.cols) + w - 1) / w;
+    a.x_units = a.x_tiles_m * a.x_tiles_n;
   };
-  // The width with which the busiest pair has least to do: a unit costs its columns and
-  // UNIT_COST more.  Where a symmetric operand or result has a strip, tiles must not
-  // straddle its first column.
-  const int pairs = g.num_sms / 2, rest = up64(a.N - a.strip);
+  // The width with which a step takes least: a unit costs its columns and UNIT_COST more,
+  // rounds of units end together in a batch of one and run into each other in a large one.
+  // Tiles must not straddle a strip's first column, and hold its columns.
   int best = 0;
-  int64_t least = 0;
-  for (int w = 64; w <= 256; w += 64) {
-    if (split && (256 % w != 0 || (P::SYM && w < rest))) continue;
+  double least = 0.;
+  for (int w = 64; w <= 256; w *= 2) {
+    if (split && w < rest) continue;
     fit(w);
-    int64_t most = 0;
-    for (int p = 0; p < pairs && p < a.units; ++p) {
-      const int64_t mine = (a.units - p + pairs - 1) / pairs;
-      const int64_t main = p < a.main_units ? (a.main_units - p + pairs - 1) / pairs : 0;
-      const int64_t cost = main * (w + UNIT_COST) + (mine - main) * (rest + UNIT_COST);
-      if (cost > most) most = cost;
-    }
-    if (best == 0 || most <= least) best = w, least = most;
+    auto rounds = [&](double units) { return units * g.batch > 4. * pairs ? units * g.batch / pairs : ceil(units * g.batch / pairs); };
+    const double cost = (2. * a.kb_m + 2. * a.kb_gram) / 2. * rounds(a.sym_main) * (w + UNIT_COST) +
+                        (split ? (a.kb_m + a.kb_gram) * rounds(mt) * (rest + UNIT_COST) : 0.) +
+                        a.kb_m * rounds(a.x_units) * (w + UNIT_COST);
+    if (best == 0 || cost <= least) best = w, least = cost;
   }
   fit(best);
-  constexpr int in_kind = P::PARTS == 2 ? EK_BF16 : EK_F16;
-  a.idesc = idesc_f16(in_kind == EK_BF16, false, false, 256, 0);
-  a.timeout_ns = g.timeout_ns;
-  a.status = g.status;
+  const int64_t units = static_cast<int64_t>(a.steps) * g.batch * (2 * a.sym_units + a.x_units);
+  if (units > (int64_t(1) << 30) || 8 * (units / g.batch) > (int64_t(1) << 30)) return cudaErrorInvalidValue;
+  a.units = static_cast<int>(units);
+  // a wait may last as long as everything before it
+  const int64_t blocks = (units / pairs + 1) * (a.kb_gram > a.kb_m ? a.kb_gram : a.kb_m);
+  a.timeout_ns = g.timeout_ns + static_cast<unsigned long long>(blocks) * 4000ull;
   const uint64_t planes = 2 * static_cast<uint64_t>(g.batch);
-  auto map = [&](CUtensorMap* t, const Matrix& x, int op, int box_rows) {
-    const uint64_t pitch = static_cast<uint64_t>(x.pitch) * 2;
-    for (int mn = 0; mn < 2; ++mn)
-      if ((op == OP_SYM || op == mn) &&
-          !encode_tmap_3d(t + mn, x.p, in_kind, x.cols, x.rows, planes, pitch, x.rows * pitch, 64, mn ? 64 : box_rows, 128))
-        return false;
-    return true;
-  };
-  bool ok = map(m.A, A, P::A_KIND, 128) && map(m.B, B, P::B_KIND, P::b_rows(a));
-  const uint64_t pc = static_cast<uint64_t>(C.pitch) * 2;
-  if (P::RESULT) {
-    a.wide = C.cols % 8 == 0 && reinterpret_cast<uintptr_t>(C.p) % 16 == 0;
-    a.out_f16 = g.out_kind == EK_F16;
-    a.o = static_cast<uint16_t*>(C.p);
-    if (a.wide) ok = ok && encode_tmap_3d(&m.C, C.p, g.out_kind, C.cols, C.rows, g.batch, pc, C.rows * pc, 64, 32, 128);
-  } else {
-    ok = ok && encode_tmap_3d(&m.C, C.p, EK_BF16, C.cols, C.rows, planes, pc, C.rows * pc, 64, 32, 128);
+  bool ok = true;
+  for (int i = 0; i < 4; ++i) {
+    const bool x = i < 2;
+    const uint64_t rows = x ? a.rows : a.m, cols = x ? a.cols : a.m, pitch = (x ? a.x_pitch : a.s_pitch) * 2;
+    auto map = [&](CUtensorMap* t, int box_cols, int box_rows) {
+      ok = ok && encode_tmap_3d(t, a.buf[i], EK_BF16, cols, rows, planes, pitch, rows * pitch, box_cols, box_rows, 128);
+    };
+    map(&m.k[i], 64, 128);
+    map(&m.kb[i], 64, x ? a.width / 2 : up64(a.width / 2));
+    map(&m.mn[i], 64, 64);
+    map(&m.store[i], 64, 32);
   }
+  a.wide = g.cols % 8 == 0 && reinterpret_cast<uintptr_t>(g.O) % 16 == 0;
+  if (a.wide)
+    ok = ok && encode_tmap_3d(&m.store[BUF_O], g.O, g.out_kind, g.cols, g.rows, g.batch, 2 * g.cols, g.rows * 2 * g.cols, 64, 32, 128);
   if (!ok) return cudaErrorInvalidValue;
   return pt::pair_launch<P>(m, a, g.num_sms, g.stream);
 }
 
 template <typename T>
-cudaError_t prepare(const OrthCall& g, const Places& l, double* sums, uint16_t* X) {
+cudaError_t prepare(const OrthCall& g, const Places& l, double* sums, uint16_t* X, int* done) {
   const int64_t n = g.rows * g.cols;
   const T* G = static_cast<const T*>(g.G);
   const bool base = reinterpret_cast<uintptr_t>(G) % 16 == 0;
@@ -511,7 +599,7 @@ cudaError_t prepare(const OrthCall& g, const Places& l, double* sums, uint16_t* 
   return launch_k(orth_split_kernel<T>, dim3(static_cast<unsigned>(g.batch * blocks)), dim3(256), 0, g.stream, G,
                   static_cast<const double*>(sums), X, static_cast<long long>(g.rows), static_cast<int>(g.cols),
                   static_cast<int>(l.pitch_x), l.parts, static_cast<int>(blocks), static_cast<long long>(l.x_part), g.eps,
-                  static_cast<int>(base && g.cols % 8 == 0));
+                  static_cast<int>(base && g.cols % 8 == 0), done);
 }
 
 // Whether the last step may take one fp16 part (see orth_launch): its coefficients, and
@@ -535,6 +623,14 @@ bool light_last(const OrthCall& g) {
 
 }  // namespace
 
+bool orth_fits(int64_t batch, int64_t rows, int64_t cols, int64_t steps) {
+  if (batch <= 0 || rows <= 0 || cols <= 0) return true;
+  const int64_t m = rows < cols ? rows : cols, n = rows < cols ? cols : rows, most = int64_t(1) << 27;
+  auto tiles = [](int64_t a, int64_t b) { return ((a + 255) / 256 + 1) * ((b + 63) / 64); };
+  const int64_t each = 2 * tiles(m, m) + tiles(n, m) + tiles(m, n);
+  return each <= most / steps && each * steps <= 8 * most / batch;
+}
+
 size_t orth_ws_bytes(int64_t batch, int64_t rows, int64_t cols) {
   return batch > 0 && rows > 0 && cols > 0 ? places(batch, rows, cols).bytes : 0;
 }
@@ -542,64 +638,49 @@ size_t orth_ws_bytes(int64_t batch, int64_t rows, int64_t cols) {
 cudaError_t orth_launch(const OrthCall& g) {
   const Places l = places(g.batch, g.rows, g.cols);
   char* ws = static_cast<char*>(g.ws);
-  Matrix X[2] = {{ws + l.x[0], g.rows, g.cols, l.pitch_x}, {ws + l.x[1], g.rows, g.cols, l.pitch_x}};
-  const Matrix S = {ws + l.s, l.m, l.m, l.pitch_s}, Q = {ws + l.q, l.m, l.m, l.pitch_s};
-  const Matrix O = {g.O, g.rows, g.cols, g.cols};
-  double* sums = reinterpret_cast<double*>(ws + l.sums);
-  uint16_t* x0 = static_cast<uint16_t*>(X[0].p);
-  cudaError_t e = g.in_kind == EK_BF16  ? prepare<__nv_bfloat16>(g, l, sums, x0)
-                  : g.in_kind == EK_F16 ? prepare<__half>(g, l, sums, x0)
-                                        : prepare<float>(g, l, sums, x0);
-  const bool tall = g.rows > g.cols;
+  OrthArgs a = {};
+  uint16_t* x0 = reinterpret_cast<uint16_t*>(ws + l.x[0]);
+  const size_t at[4] = {l.x[0], l.x[1], l.s, l.q};
+  for (int i = 0; i < 4; ++i) a.buf[i] = reinterpret_cast<const uint16_t*>(ws + at[i]);
+  a.done = reinterpret_cast<int*>(ws + l.done);
+  a.o = static_cast<uint16_t*>(g.O);
+  a.x_pitch = l.pitch_x;
+  a.x_part = l.x_part;
+  a.s_pitch = l.pitch_s;
+  a.s_part = l.s_part;
+  a.rows = static_cast<int>(g.rows);
+  a.cols = static_cast<int>(g.cols);
+  a.m = static_cast<int>(l.m);
+  a.batch = static_cast<int>(g.batch);
+  a.steps = static_cast<int>(g.steps);
+  a.kb_gram = static_cast<int>((l.long_side + pt::BK - 1) / pt::BK);
+  a.kb_m = static_cast<int>((l.m + pt::BK - 1) / pt::BK);
+  a.out_f16 = g.out_kind == EK_F16;
+  a.scale = g.scale;
+  a.status = g.status;
+  for (int64_t i = 0; i < g.steps; ++i)
+    for (int j = 0; j < 3; ++j) a.coeffs[i][j] = static_cast<float>(g.coeffs[3 * i + j]);
   // The last step of a bf16 result: written around 1, where the singular values are by
-  // then, with D = A - I (X'X = I + D),
+  // then, with D = A - I,
   //   (a + b + c) X + E X,  E = (b + 2 c) D + c D D,
   // D, E and the X of the products may be one fp16 part each: their rounding (2^-11 at most)
   // enters times |b + 2 c| + |c|, 2.7 with the usual coefficients (as a I + b A + c A A it
   // would be 7 and more), and the first term takes X in two parts.  Emulated in 64 bits it
   // leaves 2e-4 to 4e-4 of a result's size beside the 1.7e-3 of rounding to bf16 (1e-3
   // where X has directions of 1e-5), for a third of the products.
-  const bool light = g.out_kind == EK_BF16 && light_last(g);
-  for (int64_t i = 0; i < g.steps && e == cudaSuccess; ++i) {
-    const Matrix &x = X[i & 1], &y = X[(i + 1) & 1];
-    const double *k = g.coeffs + 3 * i, s = g.scale;
-    const bool end = i + 1 == g.steps;
-    OrthArgs sum = {}, poly = {}, out = {};
-    poly.in = static_cast<const uint16_t*>(S.p);
-    poly.in_pitch = l.pitch_s;
-    poly.in_part = l.s_part;
-    poly.in_matrix = l.m * l.pitch_s;
-    poly.c = static_cast<float>(k[2]);
-    if (end && light) {
-      poly.b = static_cast<float>(k[1] + 2 * k[2]);
-      out.in = static_cast<const uint16_t*>(x.p);
-      out.in_pitch = l.pitch_x;
-      out.in_part = l.x_part;
-      out.in_matrix = g.rows * l.pitch_x;
-      out.a = static_cast<float>(s * (k[0] + k[1] + k[2]));
-      out.c = g.scale;
-      e = tall ? product<OrthProduct<OP_MN, OP_MN, EP_D>>(g, x, x, S, sum) : product<OrthProduct<OP_K, OP_K, EP_D>>(g, x, x, S, sum);
-      if (e == cudaSuccess) e = product<OrthProduct<OP_SYM, OP_SYM, EP_E>>(g, S, S, Q, poly);
-      if (e == cudaSuccess)
-        e = tall ? product<OrthProduct<OP_K, OP_SYM, EP_LAST>>(g, x, Q, O, out)
-                 : product<OrthProduct<OP_SYM, OP_MN, EP_LAST>>(g, Q, x, O, out);
-      break;
-    }
-    poly.a = static_cast<float>(k[0]);
-    poly.b = static_cast<float>(k[1]);
-    out.c = g.scale;
-    e = tall ? product<OrthProduct<OP_MN, OP_MN, EP_A>>(g, x, x, S, sum) : product<OrthProduct<OP_K, OP_K, EP_A>>(g, x, x, S, sum);
-    if (e == cudaSuccess) e = product<OrthProduct<OP_SYM, OP_SYM, EP_Q>>(g, S, S, Q, poly);
-    if (e != cudaSuccess) break;
-    if (end)
-      e = tall ? product<OrthProduct<OP_K, OP_SYM, EP_OUT>>(g, x, Q, O, out) : product<OrthProduct<OP_SYM, OP_MN, EP_OUT>>(g, Q, x, O, out);
-    else if (light && i + 2 == g.steps)  // X in fp16 parts for the last step
-      e = tall ? product<OrthProduct<OP_K, OP_SYM, EP_X, true>>(g, x, Q, y, out)
-               : product<OrthProduct<OP_SYM, OP_MN, EP_X, true>>(g, Q, x, y, out);
-    else
-      e = tall ? product<OrthProduct<OP_K, OP_SYM, EP_X>>(g, x, Q, y, out) : product<OrthProduct<OP_SYM, OP_MN, EP_X>>(g, Q, x, y, out);
+  a.light = g.out_kind == EK_BF16 && light_last(g);
+  if (a.light) {
+    const double* k = g.coeffs + 3 * (g.steps - 1);
+    float* c = a.coeffs[g.steps - 1];
+    c[0] = static_cast<float>(k[0] + k[1] + k[2]);
+    c[1] = static_cast<float>(k[1] + 2 * k[2]);
   }
-  return e;
+  double* sums = reinterpret_cast<double*>(ws + l.sums);
+  const cudaError_t e = g.in_kind == EK_BF16  ? prepare<__nv_bfloat16>(g, l, sums, x0, a.done)
+                        : g.in_kind == EK_F16 ? prepare<__half>(g, l, sums, x0, a.done)
+                                              : prepare<float>(g, l, sums, x0, a.done);
+  if (e != cudaSuccess) return e;
+  return g.rows > g.cols ? chain<true>(g, l, a) : chain<false>(g, l, a);
 }
 
 }  // namespace tg

@@ -14,10 +14,14 @@
 // reduction, so its bound grows with the blocks of one.
 //
 // P has: Maps, Args (with units, idesc, timeout_ns, status), Unit (with kb, the
-// blocks of its reduction; nmma, its columns), PARTS (1, or 2: operands in two 16-bit
-// parts, a stage holds both of both, and a block is the products hi lo, lo hi and hi
-// hi), STAGES, EPI_BLOCKS (64-column blocks of shared memory a quadrant), State (what
-// an epilogue warp keeps from unit to unit), and
+// blocks of its reduction; nmma, its columns), PARTS (1, or 2: operands in up to two
+// 16-bit parts, a stage holds both of both, and a block is the products hi lo, lo hi and
+// hi hi), STAGES, EPI_BLOCKS (64-column blocks of shared memory a quadrant), State (what
+// an epilogue warp keeps from unit to unit), COOPERATIVE (its units wait for others'
+// results: every CTA has to be resident), and
+//   parts(args, unit)              of this unit
+//   idesc(args, unit)              without N and the majors
+//   ready(args, unit, abort)       before the unit's copies; false: give up
 //   a_mn(args, unit, kb), b_mn     is the operand of this block MN-major
 //   prefetch(maps, args)           the maps of its operands
 //   unit(args, u, &unit)           false: nothing to do
@@ -28,6 +32,8 @@
 // warps of a quadrant get the same answer) and release() once it has.
 #pragma once
 #include <cuda.h>
+
+#include <atomic>
 
 #include "ptx.cuh"
 #include "smem_attr.h"
@@ -147,6 +153,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       typename P::Unit c;
       for (int u = pair_index(); ok && u < args.units; u += pair_count()) {
         if (!P::unit(args, u, c)) continue;
+        if (!P::ready(args, c, abort_flag)) {
+          ok = false;
+          break;
+        }
         const uint32_t bytes = P::bytes(args, c);
         for (int kb = 0; kb < c.kb; ++kb) {
           if (!mbar_wait<true>(smem_u32(&empty[stage]), phase ^ 1u, tmo, abort_flag, args.status, P::SITE + 1)) {
@@ -194,7 +204,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!mbar_wait<true>(smem_u32(&tempty[acc]), acc_phase ^ 1u, tmo, abort_flag, args.status, P::SITE + 3)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
-        const uint32_t idesc = args.idesc | (static_cast<uint32_t>(c.nmma >> 3) << 17);
+        const uint32_t idesc = P::idesc(args, c) | (static_cast<uint32_t>(c.nmma >> 3) << 17);
+        const int parts = P::PARTS == 2 ? P::parts(args, c) : 1;
         for (int kb = 0; kb < c.kb; ++kb) {
           if (!mbar_wait<true>(smem_u32(&full[stage]), phase, tmo, abort_flag, args.status, P::SITE + 4)) {
             ok = false;
@@ -211,11 +222,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint64_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2;
 #pragma unroll
           for (int p = P::PARTS == 2 ? 0 : 2; p < 3; ++p) {
+            if (P::PARTS == 2 && p < 2 && parts == 1) continue;
             const uint64_t ad = ad0 + (p == 1 ? A_BYTES >> 4 : 0), bd = bd0 + (p == 0 ? B_BYTES >> 4 : 0);
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
               umma_f16_pair(d_tmem, ad + kk * a_step, bd + kk * b_step, id,
-                            (kb > 0 || kk > 0 || (P::PARTS == 2 && p > 0)) ? 1u : 0u);
+                            (kb > 0 || kk > 0 || (p > 0 && parts == 2)) ? 1u : 0u);
           }
           umma_commit_pair(smem_u32(&empty[stage]), 0x3);
           if (++stage == S) {
@@ -289,6 +301,19 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
+// Clusters of two that the current device holds at once, counted once (a cooperative
+// launch of more would be refused).
+template <class Kern>
+int resident_pairs(Kern kern, const cudaLaunchConfig_t& cfg) {
+  static std::atomic<int> known[128];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 0;
+  if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
+  known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 // At most `units` pairs, one a pair of SMs.
 template <class P>
 cudaError_t pair_launch(const typename P::Maps& maps, const typename P::Args& args, int num_sms, cudaStream_t stream) {
@@ -308,8 +333,21 @@ cudaError_t pair_launch(const typename P::Maps& maps, const typename P::Args& ar
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  const int pairs = args.units < num_sms / 2 ? args.units : num_sms / 2;
+  if (P::COOPERATIVE) {
+    attr[1].id = cudaLaunchAttributeCooperative;
+    attr[1].val.cooperative = 1;
+    cfg.numAttrs = 2;
+  }
+  int pairs = args.units < num_sms / 2 ? args.units : num_sms / 2;
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  if (P::COOPERATIVE) {
+    cudaLaunchConfig_t one = cfg;  // the query takes the cluster's shape alone
+    one.numAttrs = 1;
+    const int most = resident_pairs(kern, one);
+    if (most <= 0) return cudaErrorCooperativeLaunchTooLarge;
+    if (pairs > most) pairs = most;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  }
   return cudaLaunchKernelEx(&cfg, kern, maps, args);
 }
 
@@ -357,7 +395,7 @@ __device__ __forceinline__ void half_fetch(HalfRegs& r, const uint16_t* p, long 
     if (row < rows && c < cols) {
       const uint16_t* s = p + row * pitch + c;
       if (wide) {
-        r.w[i] = *reinterpret_cast<const uint4*>(s);
+        r.w[i] = __ldcg(reinterpret_cast<const uint4*>(s));
       } else {
         uint32_t o[4];
 #pragma unroll

@@ -506,7 +506,9 @@ tg_status tg_gated_bwd(const void* dY, const void* W_down, const void* GU, void*
  * numbers with eps = 0), one that holds values that are not finite gives values
  * that are not numbers, in that matrix only.  rows, cols and batch are at most
  * 2^20, a tensor has at most 2^38 elements; 1 <= steps <= 64; scale and coeffs
- * finite, eps finite and >= 0.  Workspace: tg_workspace_size(
+ * finite, eps finite and >= 0; batch . steps . (tiles of 256 x 64 of three
+ * products) at most 2^30.  All products are one cooperative launch, whose
+ * blocks wait for each other's tiles: it takes the SMs as others leave them.  Workspace: tg_workspace_size(
  * TG_OP_ORTHOGONALIZE, batch, rows, cols, 0, in, out), 16-byte aligned; its
  * content does not matter.  Results are bitwise reproducible. */
 tg_status tg_orthogonalize(const void* G, void* O, int64_t batch, int64_t rows, int64_t cols, const double* coeffs,
