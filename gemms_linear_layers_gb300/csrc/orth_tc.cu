@@ -5,7 +5,7 @@
 // which takes every singular value s of X to a s + b s^3 + c s^5 and so all of
 // them towards 1, and O = scale X.
 //
-// Everything between the launches is held as two bf16 parts, v = hi + lo to
+// Everything between the products is held as two bf16 parts, v = hi + lo to
 // within 2^-17 |v|, and a product is the three products hi lo + lo hi + hi hi in
 // one FP32 accumulator.  One 16-bit part would not do: rounding spreads over all
 // directions alike, and a direction that the gradient barely has is multiplied
@@ -30,14 +30,13 @@ namespace {
 // What a product makes of its sum.  EP_D, EP_E and EP_LAST are the last step's (see
 // orth_launch), on one fp16 part each.
 enum {
-  EP_A = 0,     // A                                    two bf16 parts, symmetric
+  EP_A = 0,     // A, X                                 two bf16 parts, A symmetric
   EP_Q = 1,     // Q = a I + b A + c sum                two bf16 parts, symmetric
-  EP_X = 2,     // X                                    two bf16 parts
-  EP_OUT = 3,   // scale X                              the result
-  EP_D = 4,     // D = sum - I                          one fp16 part, symmetric
-  EP_E = 5,     // E = (b + 2 c) D + c sum              one fp16 part, symmetric
-  EP_LAST = 6,  // scale ((a + b + c) X + sum)          the result; X two fp16 parts
-  EP_X16 = 7    // X for EP_D and EP_LAST               two fp16 parts
+  EP_OUT = 2,   // scale X                              the result
+  EP_D = 3,     // D = sum - I                          one fp16 part, symmetric
+  EP_E = 4,     // E = (b + 2 c) D + c sum              one fp16 part, symmetric
+  EP_LAST = 5,  // scale ((a + b + c) X + sum)          the result; X two fp16 parts
+  EP_X16 = 6    // X for EP_D and EP_LAST               two fp16 parts
 };
 
 // How an operand lies in memory.  OP_SYM: a symmetric matrix stored in part.  Row
@@ -52,9 +51,17 @@ enum { OP_K = 0, OP_MN = 1, OP_SYM = 2 };
 // units go product by product and, within one, matrix by matrix, dealt to the pairs in
 // turn.  A matrix's next product begins when every tile of its last one has been stored
 // (a counter of each matrix, in the workspace), whatever the other matrices are at, so
-// only a batch of one waits at a product's end.  (With a launch a product, 24 matrices of
-// 576 x 576 took 345 us.)  A unit waits for units before it only, and the launch is
-// cooperative, so every wait ends.
+// only small batches wait at a product's end.  A unit waits for units before it only, and
+// the launch is cooperative, so every wait ends.  (With a launch a product 24 matrices of
+// 576 x 576 took 345 us, four of 5,760 x 2,304 3,322; one of 576 x 576 took 110, one of
+// 2,304 x 2,304 515.)
+//
+// Measured: 24 of 576 x 576 297 us, of which the products' MMAs are 151; four of 5,760 x
+// 2,304 3.24 ms, 84 % of the MMA rate over the 13 / 15 of three products a step; one of
+// 2,304 x 2,304 535 us; one of 576 x 576 124 us, one of 192 x 576 89 us: fifteen products in
+// a row of 5 to 8 us, a third of it until a tile's stores are seen by others.  An epilogue
+// step of 64 columns takes 3,000 to 4,300 cycles, as its stores wait behind the main loop's
+// copies.  Stores straight from registers were slower still (378 us).
 struct OrthMaps {
   // X (two buffers), A or D, Q or E, as loaded: K-major boxes of 128 rows, of half a tile's rows, MN-major boxes
   CUtensorMap k[4], kb[4], mn[4];
@@ -88,13 +95,12 @@ struct OrthUnit {
   bool last;       // step
 };
 
-__device__ __forceinline__ void split2(float v, float* hi, float* lo) {
-  *hi = __bfloat162float(__float2bfloat16_rn(v));
-  *lo = v - *hi;
-}
-__device__ __forceinline__ void split2h(float v, float* hi, float* lo) {
-  *hi = __half2float(__float2half_rn(v));
-  *lo = v - *hi;
+// Two values as two parts: the first parts packed, the values' rests packed.
+template <bool F16>
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t* hi, uint32_t* lo) {
+  *hi = pt::pack16<F16>(x, y);
+  const float2 h = pt::unpack16<F16>(*hi);
+  *lo = pt::pack16<F16>(x - h.x, y - h.y);
 }
 __device__ __forceinline__ int count_acquire(const int* p) {
   int v;
@@ -282,23 +288,24 @@ struct OrthChain {
     } else if constexpr (EP == EP_D || EP == EP_E) {
       pt::put_row<true>(b0, lane, at.h, v);
     } else {
-      float lo[32];
-      constexpr bool X16 = EP == EP_X16;
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if constexpr (X16) split2h(v[j], &v[j], &lo[j]);
-        else split2(v[j], &v[j], &lo[j]);
-      pt::put_row<X16>(b0, lane, at.h, v);
-      pt::put_row<X16>(b1, lane, at.h, lo);
+      for (int j = 0; j < 4; ++j) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split_pair<EP == EP_X16>(v[8 * j + 2 * e], v[8 * j + 2 * e + 1], &hi[e], &lo[e]);
+        *reinterpret_cast<uint4*>(pt::block_word(b0, lane, 4 * at.h + j)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(pt::block_word(b1, lane, 4 * at.h + j)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
     }
   }
   template <class Wait, class Release>
   static __device__ __forceinline__ void epilogue(const Maps& m, const Args& a, const Unit& c, const Unit*,
                                                   const pt::EpiWarp& at, pt::NoState&, Wait wait, Release release) {
     const int lane = threadIdx.x & 31;
+    volatile int* abort_flag = at.abort_flag;
     const bool thin = light(a, c);
     const int ep = c.kind == 0 ? (thin ? EP_D : EP_A) : c.kind == 1 ? (thin ? EP_E : EP_Q)
-                   : thin ? EP_LAST : c.last ? EP_OUT : a.light && c.step + 2 == a.steps ? EP_X16 : EP_X;
+                   : thin ? EP_LAST : c.last ? EP_OUT : a.light && c.step + 2 == a.steps ? EP_X16 : EP_A;
     const bool in = ep == EP_Q || ep == EP_E || ep == EP_LAST, in2 = in && ep != EP_E;
     const bool result = c.kind == 2 && c.last;
     const bool two = !thin && !result;
@@ -320,12 +327,11 @@ struct OrthChain {
       pt::half_fetch(in0, p, pitch, rows, left, lane, true);
       if (in2) pt::half_fetch(in1, p + part, pitch, rows, left, lane, true);
     };
-    if (!wait()) return;
-    // what this unit's copies waited for has been stored; its lines are taken past L1
+    // what this unit's copies wait for, the epilogue's first loads do too; their lines are taken past L1
     if (in && cols > 0) {
-      count_acquire(a.done + c.z);
-      fetch(0);
+      if (pt::quadrant_all(at.q, lane != 0 || ready(a, c, abort_flag))) fetch(0);
     }
+    if (!wait()) return;
     if (cols <= 0) release();
 #pragma unroll 1
     for (int col = 0; col < cols; col += 64) {
@@ -341,8 +347,7 @@ struct OrthChain {
         if (col + 64 < cols) fetch(col + 64);
       }
       switch (ep) {
-        case EP_A: finish<EP_A>(a, c, at, col, row0, rows, lane, v); break;  // (EP_X is the same)
-        case EP_X: finish<EP_A>(a, c, at, col, row0, rows, lane, v); break;
+        case EP_A: finish<EP_A>(a, c, at, col, row0, rows, lane, v); break;  // X in bf16 parts too
         case EP_Q: finish<EP_Q>(a, c, at, col, row0, rows, lane, v); break;
         case EP_OUT: finish<EP_OUT>(a, c, at, col, row0, rows, lane, v); break;
         case EP_D: finish<EP_D>(a, c, at, col, row0, rows, lane, v); break;
@@ -472,13 +477,7 @@ __global__ void __launch_bounds__(256) orth_split_kernel(const T* G, const doubl
     eight<T>(G + (z * rows + r) * cols, c, cols, wide, v);
     uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float h[2], l[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) split2(v[2 * j + e] * f0 * f1, &h[e], &l[e]);
-      hi[j] = pack_bf16x2(h[0], h[1]);
-      lo[j] = pack_bf16x2(l[0], l[1]);
-    }
+    for (int j = 0; j < 4; ++j) split_pair<false>(v[2 * j] * f0 * f1, v[2 * j + 1] * f0 * f1, &hi[j], &lo[j]);
     uint16_t* at = X + (z * rows + r) * pitch + c;
     *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(at + part_stride) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -549,8 +548,8 @@ cudaError_t chain(const OrthCall& g, const Places& l, OrthArgs a) {
   // Tiles must not straddle a strip's first column, and hold its columns.
   int best = 0;
   double least = 0.;
-  for (int w = 64; w <= 256; w *= 2) {
-    if (split && w < rest) continue;
+  for (int w = 64; w <= 256; w += 64) {
+    if (split && (w < rest || 256 % w != 0)) continue;
     fit(w);
     auto rounds = [&](double units) { return units * g.batch > 4. * pairs ? units * g.batch / pairs : ceil(units * g.batch / pairs); };
     const double cost = (2. * a.kb_m + 2. * a.kb_gram) / 2. * rounds(a.sym_main) * (w + UNIT_COST) +

@@ -69,6 +69,7 @@ struct EpiWarp {
   int rank;        // CTA of the pair
   uint32_t taddr;  // tensor memory: the warp's lanes, first column of the accumulator
   uint8_t* blocks; // the quadrant's shared memory
+  volatile int* abort_flag;
 };
 struct NoState {};
 // The 64 threads of a quadrant's two warps.
@@ -253,6 +254,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     at.h = (warp - 2) >> 2;
     at.rank = static_cast<int>(rank);
     at.blocks = sE + at.q * P::EPI_BLOCKS * BLOCK;
+    at.abort_flag = abort_flag;
     const uint32_t tempty_cl = mapa_shared(smem_u32(&tempty[0]), 0);
     int acc = 0;
     uint32_t acc_phase = 0;
