@@ -105,21 +105,25 @@ def orthogonalize(G, coeffs, scale, eps, out):
     e = 2 u s |X| + u |D| in D, it is s ((|b + 2 c| + 2 |c| |D|_2) e + u |E|) + |E|_2 u |X|."""
     X = G.double()
     X = X / (torch.linalg.vector_norm(X) + eps)
-    noise = torch.zeros((), dtype=torch.float64, device=X.device)
-    two, fro = (lambda M: torch.linalg.matrix_norm(M, 2)), torch.linalg.vector_norm
+    noise = 0.0
+    fro = lambda M: float(torch.linalg.vector_norm(M))  # noqa: E731
     for i, (a, b, c) in enumerate(coeffs):
-        s = two(X)
-        grid = torch.linspace(0, 1, 401, dtype=torch.float64, device=X.device) * s
-        steep = torch.maximum((a + 3 * b * grid ** 2 + 5 * c * grid ** 4).abs().max(), (a + b * grid ** 2 + c * grid ** 4).abs().max())
-        here = 2.0 ** -17 * fro(X) * (abs(a) + 3 * abs(b) * s ** 2 + 9 * abs(c) * s ** 4)
         A = X @ X.T if X.shape[0] <= X.shape[1] else X.T @ X
         eye = torch.eye(A.shape[0], dtype=torch.float64, device=X.device)
+        finite = bool(torch.isfinite(A).all())
+        squares = torch.linalg.eigvalsh(A.cpu()).clamp(min=0) if finite else torch.zeros(1, dtype=torch.float64)
+        s = math.sqrt(float(squares.max()))
+        grid = torch.linspace(0, 1, 401, dtype=torch.float64) * s
+        steep = max(float((a + 3 * b * grid ** 2 + 5 * c * grid ** 4).abs().max()),
+                    float((a + b * grid ** 2 + c * grid ** 4).abs().max()))
+        here = 2.0 ** -17 * fro(X) * (abs(a) + 3 * abs(b) * s ** 2 + 9 * abs(c) * s ** 4)
         if out == torch.bfloat16 and i > 0 and i + 1 == len(coeffs) and abs(b + 2 * c) + abs(c) <= 3:
-            u, D = 2.0 ** -11, A - eye
+            u, D, d = 2.0 ** -11, A - eye, squares - 1
             E = (b + 2 * c) * D + c * D @ D
             e = 2 * u * s * fro(X) + u * fro(D)
-            here = here + s * ((abs(b + 2 * c) + 2 * abs(c) * two(D)) * e + u * fro(E)) + two(E) * u * fro(X)
+            here += (s * ((abs(b + 2 * c) + 2 * abs(c) * float(d.abs().max())) * e + u * fro(E))
+                     + float(((b + 2 * c) * d + c * d ** 2).abs().max()) * u * fro(X))
         noise = noise * steep + here
         Q = a * eye + b * A + c * A @ A
         X = Q @ X if X.shape[0] <= X.shape[1] else X @ Q
-    return scale * X, abs(scale) * float(noise)
+    return scale * X, abs(scale) * noise

@@ -33,7 +33,8 @@ def same(t):
 
 # ----------------------------------------------------------------- layer norm
 LN_SIZES = [(1, 1), (1, 8), (2, 7), (5, 31), (3, 33), (17, 64), (8, 576), (301, 576), (2, 2304), (700, 2304), (1, 2301),
-            (333, 2301), (40, 1003), (64, 4100), (5, 5760), (9, 8191), (7, 8200), (3, 12289), (2, 16384), (400, 10240)]
+            (333, 2301), (40, 1003), (64, 4100), (5, 5760), (9, 8191), (7, 8200), (3, 12289), (2, 16384), (400, 10240),
+            (5001, 576), (5001, 577), (3101, 2304), (3101, 2302), (1231, 5124)]  # teams of several rows: two at a time
 
 
 def ln_inputs(T, d, dtype, place=same):
@@ -93,8 +94,9 @@ def test_layer_norm_far_from_zero(T, d):
     check_all(got, ref, err, f"{T}x{d}")
 
 
-def test_layer_norm_in_place_and_rows_apart():
-    t = ln_inputs(70, 1003, BF)
+@pytest.mark.parametrize("T,d", [(70, 1003), (3333, 2304), (5001, 577)])
+def test_layer_norm_in_place_and_rows_apart(T, d):
+    t = ln_inputs(T, d, BF)
     stat = tg.tg_layer_norm_fwd(t["X"], t["w"], b=t["b"])
     X = t["X"].clone()
     assert torch.equal(tg.tg_layer_norm_fwd(X, t["w"], b=t["b"], outs={"Y": X})["Y"], stat["Y"])
@@ -107,7 +109,7 @@ def test_layer_norm_in_place_and_rows_apart():
     bad = t["X"].clone()
     bad[5, 3], bad[9, 0] = math.inf, math.nan
     got = tg.tg_layer_norm_fwd(bad, t["w"], b=t["b"])["Y"]
-    rows = [i for i in range(70) if i not in (5, 9)]
+    rows = [i for i in range(T) if i not in (5, 9)]
     assert torch.equal(got[rows], stat["Y"][rows]) and got[9].isnan().all()
 
 
