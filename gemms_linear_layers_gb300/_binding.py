@@ -539,6 +539,10 @@ def _scratch(op, dims, din, dout, ws, device, stream, raw):
     n = (_lib or lib()).tg_workspace_size(op, *dims, din, dout)
     if n == 0 or n == SIZE_MAX:  # SIZE_MAX: sizes or types that the call itself will refuse
         return 0, 0, None
+    return _scratch_alloc(n, ws, device, stream, raw)
+
+
+def _scratch_alloc(n, ws, device, stream, raw):
     if ws is not None and ws.numel() * ws.element_size() >= n:
         return ws.data_ptr(), ws.numel() * ws.element_size(), None
     if stream is not None or n > _KEEP_BYTES or torch.cuda.is_current_stream_capturing():
@@ -793,54 +797,97 @@ def tg_grad_clip(grads, max_norm, outs=None, norm=None, ws=None, stream=None):
     return _grads("tg_grad_clip", grads, outs, max_norm, norm, ws, stream)
 
 
+# The operators below take few microseconds on the GPU: their checks are written out, each attribute read once.
+_Tensor = torch.Tensor
+_current_device = torch._C._cuda_getDevice
+
+
 def _on_current(t, name, ndim):
     """A contiguous CUDA tensor on the current device; returns its device and type."""
     _need(t, name, ndim)
     dev = t.device
-    if dev.index != torch._C._cuda_getDevice():
+    if dev.index != _current_device():
         raise ValueError(f"{name} must be on the current device")
     return dev, t.dtype
+
+
+def _at(t, name, shape, dtype, device):
+    """Address of a tensor that must be contiguous with this shape, type and device (as _like)."""
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on {device}")
+
+
+@functools.lru_cache(maxsize=1024)
+def _ws_bytes(device_index, op, d0, d1, d2, din, dout):
+    """tg_workspace_size on the current device, whose index is in the key."""
+    return lib().tg_workspace_size(op, d0, d1, d2, 0, din, dout)
+
+
+def _scratch_of(n, ws, device, stream, raw):
+    """As _scratch, for a workspace of n bytes."""
+    if n == 0 or n == SIZE_MAX:  # SIZE_MAX: sizes or types that the call itself will refuse
+        return 0, 0, None
+    if ws is None and stream is None and n <= _KEEP_BYTES:
+        mine = _kept.__dict__.get((device.index, raw))
+        if mine is not None and mine[1] >= n and not torch._C._cuda_isCurrentStreamCapturing():
+            return mine
+    return _scratch_alloc(n, ws, device, stream, raw)
 
 
 def tg_layer_norm_fwd(X, w, b=None, eps=1e-5, outs=None, stream=None):
     """Y = (X - mean) rstd w + b over the rows of X [T, d], rstd = (variance + eps)^-1/2; w, b [d].
     Returns {"Y", "mean", "rstd"} (outs may give any of them; outs["Y"] may be X)."""
     dev, dt = _on_current(X, "X", 2)
-    T, d = shape = tuple(X.shape)
-    wp = _like(w, "w", (d,), dt, dev)
-    bp = 0 if b is None else _like(b, "b", (d,), dt, dev)
-    res = {}
-    y = _result(res, outs, "Y", shape, dt, dev, stream)
-    m, r = (_result(res, outs, k, (T,), torch.float32, dev, stream) for k in ("mean", "rstd"))
-    status = (_lib or lib()).tg_layer_norm_fwd(X.data_ptr(), wp, bp, y, m, r, T, d, eps, _DT.get(dt, -1),
-                                               _raw_stream(stream, dev))
+    shape = X.shape
+    T, d = shape
+    wp = _at(w, "w", (d,), dt, dev)
+    bp = 0 if b is None else _at(b, "b", (d,), dt, dev)
+    o = outs or {}
+    Y, mean, rstd = o.get("Y"), o.get("mean"), o.get("rstd")
+    if Y is None:
+        Y = _new(shape, dt, dev, stream)
+    if mean is None:
+        mean = _new((T,), torch.float32, dev, stream)
+    if rstd is None:
+        rstd = _new((T,), torch.float32, dev, stream)
+    f32 = torch.float32
+    status = (_lib or lib()).tg_layer_norm_fwd(X.data_ptr(), wp, bp, _at(Y, "Y", shape, dt, dev),
+                                               _at(mean, "mean", (T,), f32, dev), _at(rstd, "rstd", (T,), f32, dev), T, d,
+                                               eps, _DT.get(dt, -1), _raw_stream(stream, dev))
     if status:
         raise TGError(status, "tg_layer_norm_fwd")
-    return res
+    return {"Y": Y, "mean": mean, "rstd": rstd}
 
 
 def tg_layer_norm_bwd(dY, X, w, mean, rstd, dR=None, bias=True, out_dtype=None, outs=None, ws=None, stream=None):
     """Gradients of <dY, Y> for the forward of tg_layer_norm_fwd: {"dX", "dw"} and, with `bias`, "db".  dR [T, d]: a
     gradient to add to dX.  out_dtype (X's dtype or FP32; by default that of those in outs): dw and db."""
     dev, dt = _on_current(X, "X", 2)
-    T, d = shape = tuple(X.shape)
-    dy, wp = _like(dY, "dY", shape, dt, dev), _like(w, "w", (d,), dt, dev)
-    m, r = _like(mean, "mean", (T,), torch.float32, dev), _like(rstd, "rstd", (T,), torch.float32, dev)
-    rp = 0 if dR is None else _like(dR, "dR", shape, dt, dev)
+    shape = X.shape
+    T, d = shape
+    f32 = torch.float32
+    o = outs or {}
+    dX, dw, db = o.get("dX"), o.get("dw"), o.get("db") if bias else None
     ot = out_dtype
     if ot is None:  # that of either output that is given
-        given = [outs[k].dtype for k in ("dw", "db") if outs and outs.get(k) is not None and (bias or k == "dw")]
-        ot = given[0] if given else dt
-    res = {}
-    dx, dw = _result(res, outs, "dX", shape, dt, dev, stream), _result(res, outs, "dw", (d,), ot, dev, stream)
-    db = _result(res, outs, "db", (d,), ot, dev, stream) if bias else 0
+        ot = getattr(dw if dw is not None else db, "dtype", dt)
+    if dX is None:
+        dX = _new(shape, dt, dev, stream)
+    if dw is None:
+        dw = _new((d,), ot, dev, stream)
+    if bias and db is None:
+        db = _new((d,), ot, dev, stream)
     din, dout = _DT.get(dt, -1), _DT.get(ot, -1)
     raw = _raw_stream(stream, dev)
-    wsp, wsn, held = _scratch(TG_OP_LAYER_NORM_BWD, (T, d, 0, 0), din, dout, ws, dev, stream, raw)
-    status = (_lib or lib()).tg_layer_norm_bwd(dy, X.data_ptr(), wp, m, r, rp, dx, dw, db, T, d, din, dout, wsp, wsn, raw)
+    wsp, wsn, held = _scratch_of(_ws_bytes(dev.index, TG_OP_LAYER_NORM_BWD, T, d, 0, din, dout), ws, dev, stream, raw)
+    status = (_lib or lib()).tg_layer_norm_bwd(
+        _at(dY, "dY", shape, dt, dev), X.data_ptr(), _at(w, "w", (d,), dt, dev), _at(mean, "mean", (T,), f32, dev),
+        _at(rstd, "rstd", (T,), f32, dev), 0 if dR is None else _at(dR, "dR", shape, dt, dev), _at(dX, "dX", shape, dt, dev),
+        _at(dw, "dw", (d,), ot, dev), _at(db, "db", (d,), ot, dev) if bias else 0, T, d, din, dout, wsp, wsn, raw)
     if status:
         raise TGError(status, "tg_layer_norm_bwd")
-    return res
+    return {"dX": dX, "dw": dw, "db": db} if bias else {"dX": dX, "dw": dw}
 
 
 def _act(act):
@@ -855,24 +902,28 @@ def tg_gated_fwd(X, W, act="silu", keep=False, outs=None, ws=None, stream=None):
     and, with `keep`, "GU" [T, 2 f], which the backward takes.  act: silu, gelu, gelu_tanh or relu."""
     dev, dt = _on_current(X, "X", 2)
     T, d = X.shape
-    rows = W.shape[0] if isinstance(W, torch.Tensor) and W.dim() == 2 else 0
+    rows = W.shape[0] if isinstance(W, _Tensor) and W.dim() == 2 else 0
     if rows % 2:
         raise ValueError("W must have an even number of rows: the gate's, then the up projection's")
     f = rows // 2
-    wp = _like(W, "W", (rows, d), dt, dev)
+    wp = _at(W, "W", (rows, d), dt, dev)
     a = _act(act)
-    res = {}
-    h = _result(res, outs, "H", (T, f), dt, dev, stream)
-    gu = _result(res, outs, "GU", (T, rows), dt, dev, stream) if keep else 0
+    o = outs or {}
+    H, GU = o.get("H"), o.get("GU") if keep else None
+    if H is None:
+        H = _new((T, f), dt, dev, stream)
+    if keep and GU is None:
+        GU = _new((T, rows), dt, dev, stream)
     din = _DT.get(dt, -1)
     x = X.data_ptr()
     raw = _raw_stream(stream, dev)
-    wsp, wsn, held = _scratch(TG_OP_GATED_UNALIGNED if (x | wp) & 15 else TG_OP_GATED_FWD, (T, f, d, 0), din, din, ws, dev,
-                              stream, raw)
-    status = (_lib or lib()).tg_gated_fwd(x, wp, h, gu, T, f, d, a, din, wsp, wsn, raw)
+    n = _ws_bytes(dev.index, TG_OP_GATED_UNALIGNED if (x | wp) & 15 else TG_OP_GATED_FWD, T, f, d, din, din)
+    wsp, wsn, held = _scratch_of(n, ws, dev, stream, raw)
+    status = (_lib or lib()).tg_gated_fwd(x, wp, _at(H, "H", (T, f), dt, dev), _at(GU, "GU", (T, rows), dt, dev) if keep else 0,
+                                          T, f, d, a, din, wsp, wsn, raw)
     if status:
         raise TGError(status, "tg_gated_fwd")
-    return res
+    return {"H": H, "GU": GU} if keep else {"H": H}
 
 
 def tg_gated_bwd(dY, W_down, GU, act="silu", keep=False, outs=None, ws=None, stream=None):
@@ -881,22 +932,27 @@ def tg_gated_bwd(dY, W_down, GU, act="silu", keep=False, outs=None, ws=None, str
     down projection's weight gradient (outs may give them; outs["dGU"] may be GU)."""
     dev, dt = _on_current(dY, "dY", 2)
     T, d = dY.shape
-    f = W_down.shape[1] if isinstance(W_down, torch.Tensor) and W_down.dim() == 2 else 0
-    wp = _like(W_down, "W_down", (d, f), dt, dev)
-    gp = _like(GU, "GU", (T, 2 * f), dt, dev)
+    f = W_down.shape[1] if isinstance(W_down, _Tensor) and W_down.dim() == 2 else 0
+    wp = _at(W_down, "W_down", (d, f), dt, dev)
+    two = (T, 2 * f)
+    gp = _at(GU, "GU", two, dt, dev)
     a = _act(act)
-    res = {}
-    dgu = _result(res, outs, "dGU", (T, 2 * f), dt, dev, stream)
-    h = _result(res, outs, "H", (T, f), dt, dev, stream) if keep else 0
+    o = outs or {}
+    dGU, H = o.get("dGU"), o.get("H") if keep else None
+    if dGU is None:
+        dGU = _new(two, dt, dev, stream)
+    if keep and H is None:
+        H = _new((T, f), dt, dev, stream)
     din = _DT.get(dt, -1)
     y = dY.data_ptr()
     raw = _raw_stream(stream, dev)
-    wsp, wsn, held = _scratch(TG_OP_GATED_UNALIGNED if (y | wp) & 15 else TG_OP_GATED_BWD, (T, f, d, 0), din, din, ws, dev,
-                              stream, raw)
-    status = (_lib or lib()).tg_gated_bwd(y, wp, gp, dgu, h, T, f, d, a, din, wsp, wsn, raw)
+    n = _ws_bytes(dev.index, TG_OP_GATED_UNALIGNED if (y | wp) & 15 else TG_OP_GATED_BWD, T, f, d, din, din)
+    wsp, wsn, held = _scratch_of(n, ws, dev, stream, raw)
+    status = (_lib or lib()).tg_gated_bwd(y, wp, gp, _at(dGU, "dGU", two, dt, dev), _at(H, "H", (T, f), dt, dev) if keep else 0,
+                                          T, f, d, a, din, wsp, wsn, raw)
     if status:
         raise TGError(status, "tg_gated_bwd")
-    return res
+    return {"dGU": dGU, "H": H} if keep else {"dGU": dGU}
 
 
 # (a, b, c) of s -> a s + b s^3 + c s^5: five of them take every singular value into about [0.7, 1.2]
@@ -933,10 +989,11 @@ def tg_orthogonalize(G, O=None, out_dtype=None, steps=None, coeffs=ORTH_QUINTIC,
         O = _new(shape, ot, dev, stream)
         o = O.data_ptr()
     else:
-        o = _like(O, "O", shape, ot, dev)
+        o = _at(O, "O", shape, ot, dev)
     din, dout = _DT.get(dt, -1), _DT.get(ot, -1)
     raw = _raw_stream(stream, dev)
-    wsp, wsn, held = _scratch(TG_OP_ORTHOGONALIZE, (batch, rows, cols, 0), din, dout, ws, dev, stream, raw)
+    n_ws = _ws_bytes(dev.index, TG_OP_ORTHOGONALIZE, batch, rows, cols, din, dout)
+    wsp, wsn, held = _scratch_of(n_ws, ws, dev, stream, raw)
     status = (_lib or lib()).tg_orthogonalize(G.data_ptr(), o, batch, rows, cols, ctypes.addressof(array), n, scale, eps,
                                               din, dout, wsp, wsn, raw)
     if status:
