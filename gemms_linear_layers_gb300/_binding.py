@@ -967,9 +967,11 @@ def _orth_coeffs(coeffs, steps):
     triples = (coeffs,) if one else coeffs
     if len(triples) != (1 if one else n) or not triples or any(not isinstance(c, tuple) or len(c) != 3 for c in triples):
         raise ValueError("coeffs must be (a, b, c), or such a triple for each step")
-    flat = [float(x) for c in triples for x in c]
-    flat = flat * n if one else flat
-    return (ctypes.c_double * len(flat))(*flat), n
+    if n != int(n) or not 1 <= n <= 64:
+        raise ValueError("steps must be an integer from 1 to 64")
+    flat = [x for c in triples for x in c]
+    flat = flat * int(n) if one else flat
+    return (ctypes.c_double * len(flat))(*flat), int(n)
 
 
 def tg_orthogonalize(G, O=None, out_dtype=None, steps=None, coeffs=ORTH_QUINTIC, scale=1.0, eps=1e-7, ws=None, stream=None):
@@ -982,8 +984,7 @@ def tg_orthogonalize(G, O=None, out_dtype=None, steps=None, coeffs=ORTH_QUINTIC,
     dev, dt = _on_current(G, "G", G.dim())
     shape = tuple(G.shape)
     batch, rows, cols = shape if len(shape) == 3 else (1, *shape)
-    key = tuple(tuple(c) if isinstance(c, (list, tuple)) else c for c in coeffs)
-    array, n = _orth_coeffs(key, steps)
+    array, n = _orth_coeffs(tuple(tuple(map(float, c)) if isinstance(c, (list, tuple)) else float(c) for c in coeffs), steps)
     ot = out_dtype or (O.dtype if O is not None else torch.bfloat16 if dt is torch.float32 else dt)
     if O is None:
         O = _new(shape, ot, dev, stream)

@@ -111,6 +111,12 @@ def test_arguments_that_the_binding_looks_at():
             B._orth_coeffs(bad, steps)
 
 
+@pytest.mark.parametrize("steps", (0, -1, 65, 10 ** 15, 2.5))
+def test_steps_are_looked_at_before_they_are_laid_out(steps):
+    with pytest.raises(ValueError):
+        B._orth_coeffs((1.0, 2.0, 3.0), steps)
+
+
 def test_exported():
     import gemms_linear_layers_gb300 as pkg
     for n in B.SIGNATURES:

@@ -358,3 +358,35 @@ def test_streams_and_graphs_give_the_same_bits():
         for _, outs in graphs:
             assert all(torch.equal(a, b) for a, b in zip(outs, want))
     assert tg.tg_stream_status() == 0
+
+
+# ------------------------------------------------------- more than 2^31 elements
+def test_layer_norm_beyond_32_bits():
+    few = ln_inputs(1500, 576, BF)
+    t = {k: v.repeat(2500, 1) if v.dim() == 2 else v for k, v in few.items()}
+    assert t["X"].numel() > 2 ** 31
+    got = tg.tg_layer_norm_fwd(t["X"], t["w"], b=t["b"])
+    m, r = got["mean"], got["rstd"]
+    check_all({k: v[-1500:] for k, v in got.items()}, *R.layer_norm_fwd(few["X"], few["w"], few["b"], 1e-5), "last rows")
+    dX = tg.tg_layer_norm_bwd(t["dY"], t["X"], t["w"], m, r, dR=t["dR"], outs={"dX": got["Y"]})["dX"]
+    check_all({"dX": dX[-1500:]}, *R.layer_norm_bwd(few["dY"], few["X"], few["w"], m[-1500:], r[-1500:], few["dR"]), "last rows")
+
+
+def test_gated_beyond_32_bits():
+    few = gated_inputs(380, 5760, 72, BF)
+    t = {k: v.repeat(500, 1) if k in ("X", "dY", "GU") else v for k, v in few.items()}
+    assert t["GU"].numel() > 2 ** 31
+    got = tg.tg_gated_fwd(t["X"], t["W"], keep=True)
+    check_all({k: v[-380:] for k, v in got.items()}, *R.gated_fwd(few["X"], few["W"], "silu"), "last rows")
+    got = tg.tg_gated_bwd(t["dY"], t["Wd"], t["GU"], keep=True, outs={"dGU": got["GU"], "H": got["H"]})
+    check_all({k: v[-380:] for k, v in got.items()}, *R.gated_bwd(few["dY"], few["Wd"], few["GU"], "silu"), "last rows")
+
+
+def test_orthogonalize_beyond_32_bits():
+    few = gradient(10, 576, 1000, BF)
+    G = few.repeat(380, 1, 1)
+    assert G.numel() > 2 ** 31
+    want = tg.tg_orthogonalize(few)
+    got = tg.tg_orthogonalize(G, O=G).view(380, 10, 576, 1000)
+    for i in (0, 185, 379):
+        assert torch.equal(got[i], want)
