@@ -9,6 +9,16 @@
 //            projection's weight gradient.  dH never reaches memory.
 // Everything of an element is FP32 until its one rounding.  The blocks of G and U that
 // a backward epilogue needs are asked for before its accumulator is waited for.
+//
+// Measured, 2,304 -> 5,760, 4,096 rows, bf16: forward 121 us (1,790 TFLOP/s; without G and
+// U 114), backward 83 us (1,310 TFLOP/s; without H 77, GELU 88); 576 -> 1,536, 1,001 rows,
+// fp16 GELU 11.5 and 12.2 us (bf16 SiLU 10.3 and 10.7), 4,096 rows 19 and 25 us.
+// Bound by what passes an SM's port, 64 bytes a cycle in and out together: a 64-deep block
+// brings a CTA 32 KB for 512 cycles of MMA, all the port has, so what an epilogue reads
+// and writes comes on top: 96 KB of a forward unit (19,900 cycles a unit, 18,400 of MMA),
+// 320 KB of a backward one (25,500).  Hence the epilogue moves nothing twice; a ring of 4
+// instead of 5 stages cost the backward 6 us, slots for two steps of G and U 7, G and U asked
+// into L2 ahead 11.
 #include "gated.h"
 
 #include <type_traits>

@@ -56,12 +56,14 @@ enum { OP_K = 0, OP_MN = 1, OP_SYM = 2 };
 // 576 x 576 took 345 us, four of 5,760 x 2,304 3,322; one of 576 x 576 took 110, one of
 // 2,304 x 2,304 515.)
 //
-// Measured: 24 of 576 x 576 297 us, of which the products' MMAs are 151; four of 5,760 x
-// 2,304 3.24 ms, 84 % of the MMA rate over the 13 / 15 of three products a step; one of
+// Measured: 24 of 576 x 576 300 us, of which the products' MMAs are 151; four of 5,760 x
+// 2,304 3.27 ms, 84 % of the MMA rate over the 13 / 15 of three products a step; one of
 // 2,304 x 2,304 535 us; one of 576 x 576 124 us, one of 192 x 576 89 us: fifteen products in
 // a row of 5 to 8 us, a third of it until a tile's stores are seen by others.  An epilogue
 // step of 64 columns takes 3,000 to 4,300 cycles, as its stores wait behind the main loop's
-// copies.  Stores straight from registers were slower still (378 us).
+// copies.  Stores straight from registers were slower still (24 of 576 x 576 378 us), stores by
+// the lanes from shared memory, 64 bytes of a row at a time, too (308; 192 x 576 95, 100 of
+// 64 x 64 84 instead of 80).
 struct OrthMaps {
   // X (two buffers), A or D, Q or E, as loaded: K-major boxes of 128 rows, of half a tile's rows, MN-major boxes
   CUtensorMap k[4], kb[4], mn[4];
