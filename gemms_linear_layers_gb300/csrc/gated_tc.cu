@@ -80,7 +80,7 @@ struct GatedFwd {
   using Args = GatedArgs;
   using Unit = GatedUnit;
   using State = pt::NoState;
-  static constexpr int PARTS = 1, STAGES = 5, EPI_BLOCKS = 3;
+  static constexpr int PARTS = 1, STAGES = 5, B_PART = pt::B_BYTES, EPI_BLOCKS = 3;
   static constexpr unsigned SITE = 0x50;
   static constexpr bool COOPERATIVE = false;
   static __device__ __forceinline__ int parts(const Args&, const Unit&) { return 1; }
@@ -167,7 +167,7 @@ struct GatedBwd {
     int slot;      // blocks of the step at work: 2 slot, 2 slot + 1
     bool fetched;  // its copies have been requested
   };
-  static constexpr int PARTS = 1, STAGES = 5, EPI_BLOCKS = 4;
+  static constexpr int PARTS = 1, STAGES = 5, B_PART = pt::B_BYTES, EPI_BLOCKS = 4;
   static constexpr unsigned SITE = 0x58;
   static constexpr bool COOPERATIVE = false;
   static __device__ __forceinline__ int parts(const Args&, const Unit&) { return 1; }

@@ -58,7 +58,7 @@ enum { OP_K = 0, OP_MN = 1, OP_SYM = 2 };
 //
 // Measured: 24 of 576 x 576 300 us, of which the products' MMAs are 151; four of 5,760 x
 // 2,304 3.27 ms, 84 % of the MMA rate over the 13 / 15 of three products a step; one of
-// 2,304 x 2,304 535 us; one of 576 x 576 124 us, one of 192 x 576 89 us: fifteen products in
+// 2,304 x 2,304 535 us; one of 576 x 576 118 us, one of 192 x 576 88 us: fifteen products in
 // a row of 5 to 8 us, a third of it until a tile's stores are seen by others.  An epilogue
 // step of 64 columns takes 3,000 to 4,300 cycles, as its stores wait behind the main loop's
 // copies.  Stores straight from registers were slower still (24 of 576 x 576 378 us), stores by
@@ -117,14 +117,17 @@ __host__ __device__ inline int sym_tiles(int i, int n_tiles, int width) {
 }
 __host__ __device__ inline int up64(int n) { return (n + 63) / 64 * 64; }
 
-template <bool TALL>
+// NARROW: tiles of up to 128 columns, whose part of B needs half the place: a stage more
+// (8 of 1,536 x 576 240 -> 233.6 us, one of 576 x 576 122.6 -> 117.6).  Stages of one part (five,
+// and blocks for two epilogue steps in their stead) cost 8 us and 6 here.
+template <bool TALL, bool NARROW>
 struct OrthChain {
   using Maps = OrthMaps;
   using Args = OrthArgs;
   using Unit = OrthUnit;
   using State = pt::NoState;
   static constexpr bool COOPERATIVE = true;
-  static constexpr int PARTS = 2, STAGES = 3, EPI_BLOCKS = 2;
+  static constexpr int PARTS = 2, STAGES = NARROW ? 4 : 3, B_PART = NARROW ? pt::B_BYTES / 2 : pt::B_BYTES, EPI_BLOCKS = 2;
   static constexpr unsigned SITE = 0x60;
 
   static __device__ __forceinline__ bool light(const Args& a, const Unit& c) { return a.light && c.last; }
@@ -235,7 +238,7 @@ struct OrthChain {
         tma_load_3d_pair(b_dst, &m.kb[bb], bar, k0, n, z);
       }
       a_dst += pt::A_BYTES;
-      b_dst += pt::B_BYTES;
+      b_dst += B_PART;
     }
   }
 
@@ -530,7 +533,6 @@ int strip_of(int64_t m) {
 
 template <bool TALL>
 cudaError_t chain(const OrthCall& g, const Places& l, OrthArgs a) {
-  using P = OrthChain<TALL>;
   OrthMaps m = {};
   const int pairs = g.num_sms / 2, mt = (a.m + 255) / 256;
   a.strip = strip_of(a.m);
@@ -584,7 +586,8 @@ cudaError_t chain(const OrthCall& g, const Places& l, OrthArgs a) {
   if (a.wide)
     ok = ok && encode_tmap_3d(&m.store[BUF_O], g.O, g.out_kind, g.cols, g.rows, g.batch, 2 * g.cols, g.rows * 2 * g.cols, 64, 32, 128);
   if (!ok) return cudaErrorInvalidValue;
-  return pt::pair_launch<P>(m, a, g.num_sms, g.stream);
+  return a.width <= 128 ? pt::pair_launch<OrthChain<TALL, true>>(m, a, g.num_sms, g.stream)
+                        : pt::pair_launch<OrthChain<TALL, false>>(m, a, g.num_sms, g.stream);
 }
 
 template <typename T>

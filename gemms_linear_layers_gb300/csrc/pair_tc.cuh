@@ -16,9 +16,10 @@
 // P has: Maps, Args (with units, idesc, timeout_ns, status), Unit (with kb, the
 // blocks of its reduction; nmma, its columns), PARTS (1, or 2: operands in up to two
 // 16-bit parts, a stage holds both of both, and a block is the products hi lo, lo hi and
-// hi hi), STAGES, EPI_BLOCKS (64-column blocks of shared memory a quadrant), State (what
-// an epilogue warp keeps from unit to unit), COOPERATIVE (its units wait for others'
-// results: every CTA has to be resident), and
+// hi hi), STAGES, B_PART (bytes of a part of B in a stage: a CTA's half of its rows),
+// EPI_BLOCKS (64-column blocks of shared memory a quadrant), State (what an epilogue warp
+// keeps from unit to unit), COOPERATIVE (its units wait for others' results: every CTA has
+// to be resident), and
 //   parts(args, unit)              of this unit
 //   idesc(args, unit)              without N and the majors
 //   ready(args, unit, abort)       before the unit's copies; false: give up
@@ -52,7 +53,7 @@ constexpr unsigned long long BLOCK_NS = 24000;  // most that a block of a reduct
 constexpr int BLOCK = 32 * 128;  // 32 rows x 64 columns of 16 bits
 template <class P>
 constexpr int smem_bytes() {
-  return 1024 + P::STAGES * P::PARTS * (A_BYTES + B_BYTES) + 4 * P::EPI_BLOCKS * BLOCK + BAR_BYTES;
+  return 1024 + P::STAGES * P::PARTS * (A_BYTES + P::B_PART) + 4 * P::EPI_BLOCKS * BLOCK + BAR_BYTES;
 }
 
 // An arrival on rank 0's barrier: it publishes nothing of its own (the copies'
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sA = smem;
-  constexpr int A_STAGE = P::PARTS * A_BYTES, B_STAGE = P::PARTS * B_BYTES;
+  constexpr int A_STAGE = P::PARTS * A_BYTES, B_STAGE = P::PARTS * P::B_PART;
   uint8_t* sB = sA + S * A_STAGE;
   uint8_t* sE = sB + S * B_STAGE;
   uint64_t* full = reinterpret_cast<uint64_t*>(sE + 4 * P::EPI_BLOCKS * BLOCK);
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int p = P::PARTS == 2 ? 0 : 2; p < 3; ++p) {
             if (P::PARTS == 2 && p < 2 && parts == 1) continue;
-            const uint64_t ad = ad0 + (p == 1 ? A_BYTES >> 4 : 0), bd = bd0 + (p == 0 ? B_BYTES >> 4 : 0);
+            const uint64_t ad = ad0 + (p == 1 ? A_BYTES >> 4 : 0), bd = bd0 + (p == 0 ? P::B_PART >> 4 : 0);
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
               umma_f16_pair(d_tmem, ad + kk * a_step, bd + kk * b_step, id,
