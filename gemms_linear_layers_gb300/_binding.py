@@ -805,17 +805,19 @@ _current_device = torch._C._cuda_getDevice
 def _on_current(t, name, ndim):
     """A contiguous CUDA tensor on the current device; returns its device and type."""
     _need(t, name, ndim)
-    dev = t.device
-    if dev.index != _current_device():
+    if t.get_device() != _current_device():
         raise ValueError(f"{name} must be on the current device")
-    return dev, t.dtype
+    return t.device, t.dtype
 
 
-def _at(t, name, shape, dtype, device):
-    """Address of a tensor that must be contiguous with this shape, type and device (as _like)."""
-    if (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
-        return t.data_ptr()
-    raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on {device}")
+def _at(t, name, shape, dtype, index):
+    """Address of a tensor that must be contiguous with this shape, type and CUDA device (as _like)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # not a tensor
+        pass
+    raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on cuda:{index}")
 
 
 @functools.lru_cache(maxsize=1024)
@@ -839,10 +841,11 @@ def tg_layer_norm_fwd(X, w, b=None, eps=1e-5, outs=None, stream=None):
     """Y = (X - mean) rstd w + b over the rows of X [T, d], rstd = (variance + eps)^-1/2; w, b [d].
     Returns {"Y", "mean", "rstd"} (outs may give any of them; outs["Y"] may be X)."""
     dev, dt = _on_current(X, "X", 2)
+    index = dev.index
     shape = X.shape
     T, d = shape
-    wp = _at(w, "w", (d,), dt, dev)
-    bp = 0 if b is None else _at(b, "b", (d,), dt, dev)
+    wp = _at(w, "w", (d,), dt, index)
+    bp = 0 if b is None else _at(b, "b", (d,), dt, index)
     o = outs or {}
     Y, mean, rstd = o.get("Y"), o.get("mean"), o.get("rstd")
     if Y is None:
@@ -852,8 +855,8 @@ def tg_layer_norm_fwd(X, w, b=None, eps=1e-5, outs=None, stream=None):
     if rstd is None:
         rstd = _new((T,), torch.float32, dev, stream)
     f32 = torch.float32
-    status = (_lib or lib()).tg_layer_norm_fwd(X.data_ptr(), wp, bp, _at(Y, "Y", shape, dt, dev),
-                                               _at(mean, "mean", (T,), f32, dev), _at(rstd, "rstd", (T,), f32, dev), T, d,
+    status = (_lib or lib()).tg_layer_norm_fwd(X.data_ptr(), wp, bp, _at(Y, "Y", shape, dt, index),
+                                               _at(mean, "mean", (T,), f32, index), _at(rstd, "rstd", (T,), f32, index), T, d,
                                                eps, _DT.get(dt, -1), _raw_stream(stream, dev))
     if status:
         raise TGError(status, "tg_layer_norm_fwd")
@@ -864,6 +867,7 @@ def tg_layer_norm_bwd(dY, X, w, mean, rstd, dR=None, bias=True, out_dtype=None, 
     """Gradients of <dY, Y> for the forward of tg_layer_norm_fwd: {"dX", "dw"} and, with `bias`, "db".  dR [T, d]: a
     gradient to add to dX.  out_dtype (X's dtype or FP32; by default that of those in outs): dw and db."""
     dev, dt = _on_current(X, "X", 2)
+    index = dev.index
     shape = X.shape
     T, d = shape
     f32 = torch.float32
@@ -880,11 +884,11 @@ def tg_layer_norm_bwd(dY, X, w, mean, rstd, dR=None, bias=True, out_dtype=None, 
         db = _new((d,), ot, dev, stream)
     din, dout = _DT.get(dt, -1), _DT.get(ot, -1)
     raw = _raw_stream(stream, dev)
-    wsp, wsn, held = _scratch_of(_ws_bytes(dev.index, TG_OP_LAYER_NORM_BWD, T, d, 0, din, dout), ws, dev, stream, raw)
+    wsp, wsn, held = _scratch_of(_ws_bytes(index, TG_OP_LAYER_NORM_BWD, T, d, 0, din, dout), ws, dev, stream, raw)
     status = (_lib or lib()).tg_layer_norm_bwd(
-        _at(dY, "dY", shape, dt, dev), X.data_ptr(), _at(w, "w", (d,), dt, dev), _at(mean, "mean", (T,), f32, dev),
-        _at(rstd, "rstd", (T,), f32, dev), 0 if dR is None else _at(dR, "dR", shape, dt, dev), _at(dX, "dX", shape, dt, dev),
-        _at(dw, "dw", (d,), ot, dev), _at(db, "db", (d,), ot, dev) if bias else 0, T, d, din, dout, wsp, wsn, raw)
+        _at(dY, "dY", shape, dt, index), X.data_ptr(), _at(w, "w", (d,), dt, index), _at(mean, "mean", (T,), f32, index),
+        _at(rstd, "rstd", (T,), f32, index), 0 if dR is None else _at(dR, "dR", shape, dt, index), _at(dX, "dX", shape, dt, index),
+        _at(dw, "dw", (d,), ot, index), _at(db, "db", (d,), ot, index) if bias else 0, T, d, din, dout, wsp, wsn, raw)
     if status:
         raise TGError(status, "tg_layer_norm_bwd")
     return {"dX": dX, "dw": dw, "db": db} if bias else {"dX": dX, "dw": dw}
@@ -901,12 +905,13 @@ def tg_gated_fwd(X, W, act="silu", keep=False, outs=None, ws=None, stream=None):
     """[G U] = X W^T and H = act(G) U in one kernel: X [T, d], W [2 f, d] (gate rows, then up rows).  Returns {"H"}
     and, with `keep`, "GU" [T, 2 f], which the backward takes.  act: silu, gelu, gelu_tanh or relu."""
     dev, dt = _on_current(X, "X", 2)
+    index = dev.index
     T, d = X.shape
     rows = W.shape[0] if isinstance(W, _Tensor) and W.dim() == 2 else 0
     if rows % 2:
         raise ValueError("W must have an even number of rows: the gate's, then the up projection's")
     f = rows // 2
-    wp = _at(W, "W", (rows, d), dt, dev)
+    wp = _at(W, "W", (rows, d), dt, index)
     a = _act(act)
     o = outs or {}
     H, GU = o.get("H"), o.get("GU") if keep else None
@@ -917,9 +922,9 @@ def tg_gated_fwd(X, W, act="silu", keep=False, outs=None, ws=None, stream=None):
     din = _DT.get(dt, -1)
     x = X.data_ptr()
     raw = _raw_stream(stream, dev)
-    n = _ws_bytes(dev.index, TG_OP_GATED_UNALIGNED if (x | wp) & 15 else TG_OP_GATED_FWD, T, f, d, din, din)
+    n = _ws_bytes(index, TG_OP_GATED_UNALIGNED if (x | wp) & 15 else TG_OP_GATED_FWD, T, f, d, din, din)
     wsp, wsn, held = _scratch_of(n, ws, dev, stream, raw)
-    status = (_lib or lib()).tg_gated_fwd(x, wp, _at(H, "H", (T, f), dt, dev), _at(GU, "GU", (T, rows), dt, dev) if keep else 0,
+    status = (_lib or lib()).tg_gated_fwd(x, wp, _at(H, "H", (T, f), dt, index), _at(GU, "GU", (T, rows), dt, index) if keep else 0,
                                           T, f, d, a, din, wsp, wsn, raw)
     if status:
         raise TGError(status, "tg_gated_fwd")
@@ -931,11 +936,12 @@ def tg_gated_bwd(dY, W_down, GU, act="silu", keep=False, outs=None, ws=None, str
     dY [T, d], W_down [d, f], GU [T, 2 f] of the forward.  Returns {"dGU"} and, with `keep`, "H" = act(G) U for the
     down projection's weight gradient (outs may give them; outs["dGU"] may be GU)."""
     dev, dt = _on_current(dY, "dY", 2)
+    index = dev.index
     T, d = dY.shape
     f = W_down.shape[1] if isinstance(W_down, _Tensor) and W_down.dim() == 2 else 0
-    wp = _at(W_down, "W_down", (d, f), dt, dev)
+    wp = _at(W_down, "W_down", (d, f), dt, index)
     two = (T, 2 * f)
-    gp = _at(GU, "GU", two, dt, dev)
+    gp = _at(GU, "GU", two, dt, index)
     a = _act(act)
     o = outs or {}
     dGU, H = o.get("dGU"), o.get("H") if keep else None
@@ -946,9 +952,9 @@ def tg_gated_bwd(dY, W_down, GU, act="silu", keep=False, outs=None, ws=None, str
     din = _DT.get(dt, -1)
     y = dY.data_ptr()
     raw = _raw_stream(stream, dev)
-    n = _ws_bytes(dev.index, TG_OP_GATED_UNALIGNED if (y | wp) & 15 else TG_OP_GATED_BWD, T, f, d, din, din)
+    n = _ws_bytes(index, TG_OP_GATED_UNALIGNED if (y | wp) & 15 else TG_OP_GATED_BWD, T, f, d, din, din)
     wsp, wsn, held = _scratch_of(n, ws, dev, stream, raw)
-    status = (_lib or lib()).tg_gated_bwd(y, wp, gp, _at(dGU, "dGU", two, dt, dev), _at(H, "H", (T, f), dt, dev) if keep else 0,
+    status = (_lib or lib()).tg_gated_bwd(y, wp, gp, _at(dGU, "dGU", two, dt, index), _at(H, "H", (T, f), dt, index) if keep else 0,
                                           T, f, d, a, din, wsp, wsn, raw)
     if status:
         raise TGError(status, "tg_gated_bwd")
@@ -982,6 +988,7 @@ def tg_orthogonalize(G, O=None, out_dtype=None, steps=None, coeffs=ORTH_QUINTIC,
     if not isinstance(G, torch.Tensor) or G.dim() not in (2, 3):
         raise ValueError("G must be [rows, cols] or [batch, rows, cols]")
     dev, dt = _on_current(G, "G", G.dim())
+    index = dev.index
     shape = tuple(G.shape)
     batch, rows, cols = shape if len(shape) == 3 else (1, *shape)
     array, n = _orth_coeffs(tuple(tuple(map(float, c)) if isinstance(c, (list, tuple)) else float(c) for c in coeffs), steps)
@@ -990,10 +997,10 @@ def tg_orthogonalize(G, O=None, out_dtype=None, steps=None, coeffs=ORTH_QUINTIC,
         O = _new(shape, ot, dev, stream)
         o = O.data_ptr()
     else:
-        o = _at(O, "O", shape, ot, dev)
+        o = _at(O, "O", shape, ot, index)
     din, dout = _DT.get(dt, -1), _DT.get(ot, -1)
     raw = _raw_stream(stream, dev)
-    n_ws = _ws_bytes(dev.index, TG_OP_ORTHOGONALIZE, batch, rows, cols, din, dout)
+    n_ws = _ws_bytes(index, TG_OP_ORTHOGONALIZE, batch, rows, cols, din, dout)
     wsp, wsn, held = _scratch_of(n_ws, ws, dev, stream, raw)
     status = (_lib or lib()).tg_orthogonalize(G.data_ptr(), o, batch, rows, cols, ctypes.addressof(array), n, scale, eps,
                                               din, dout, wsp, wsn, raw)
