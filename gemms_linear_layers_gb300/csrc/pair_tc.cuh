@@ -304,15 +304,15 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// Clusters of two that the current device holds at once, counted once (a cooperative
-// launch of more would be refused).
-template <class Kern>
-int resident_pairs(Kern kern, const cudaLaunchConfig_t& cfg) {
+// Pairs that the current device holds at once, counted once a device and kernel (a
+// cooperative launch of more would be refused).
+template <class P>
+int resident_pairs(const cudaLaunchConfig_t& cfg) {
   static std::atomic<int> known[128];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 0;
   if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
-  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
+  if (cudaOccupancyMaxActiveClusters(&n, pair_kernel<P>, &cfg) != cudaSuccess) return 0;
   known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
@@ -346,7 +346,7 @@ cudaError_t pair_launch(const typename P::Maps& maps, const typename P::Args& ar
   if (P::COOPERATIVE) {
     cudaLaunchConfig_t one = cfg;  // the query takes the cluster's shape alone
     one.numAttrs = 1;
-    const int most = resident_pairs(kern, one);
+    const int most = resident_pairs<P>(one);
     if (most <= 0) return cudaErrorCooperativeLaunchTooLarge;
     if (pairs > most) pairs = most;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
