@@ -83,7 +83,6 @@ struct GatedFwd {
   static constexpr int PARTS = 1, STAGES = 5, B_PART = pt::B_BYTES, EPI_BLOCKS = 3;
   static constexpr unsigned SITE = 0x50;
   static constexpr bool COOPERATIVE = false;
-  static __device__ __forceinline__ int parts(const Args&, const Unit&) { return 1; }
   static __device__ __forceinline__ uint32_t idesc(const Args& a, const Unit&) { return a.idesc; }
   static __device__ __forceinline__ bool ready(const Args&, const Unit&, volatile int*) { return true; }
   static __device__ __forceinline__ bool a_mn(const Args&, const Unit&, int) { return false; }
@@ -170,7 +169,6 @@ struct GatedBwd {
   static constexpr int PARTS = 1, STAGES = 5, B_PART = pt::B_BYTES, EPI_BLOCKS = 4;
   static constexpr unsigned SITE = 0x58;
   static constexpr bool COOPERATIVE = false;
-  static __device__ __forceinline__ int parts(const Args&, const Unit&) { return 1; }
   static __device__ __forceinline__ uint32_t idesc(const Args& a, const Unit&) { return a.idesc; }
   static __device__ __forceinline__ bool ready(const Args&, const Unit&, volatile int*) { return true; }
   static __device__ __forceinline__ bool a_mn(const Args&, const Unit&, int) { return false; }

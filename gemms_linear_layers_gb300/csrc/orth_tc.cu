@@ -27,16 +27,11 @@
 namespace tg {
 namespace {
 
-// What a product makes of its sum.  EP_D, EP_E and EP_LAST are the last step's (see
-// orth_launch), on one fp16 part each.
+// What a product makes of its sum.
 enum {
-  EP_A = 0,     // A, X                                 two bf16 parts, A symmetric
-  EP_Q = 1,     // Q = a I + b A + c sum                two bf16 parts, symmetric
-  EP_OUT = 2,   // scale X                              the result
-  EP_D = 3,     // D = sum - I                          one fp16 part, symmetric
-  EP_E = 4,     // E = (b + 2 c) D + c sum              one fp16 part, symmetric
-  EP_LAST = 5,  // scale ((a + b + c) X + sum)          the result; X two fp16 parts
-  EP_X16 = 6    // X for EP_D and EP_LAST               two fp16 parts
+  EP_A = 0,   // A, X                     two parts, A symmetric
+  EP_Q = 1,   // Q = a I + b A + c sum    two parts, symmetric
+  EP_OUT = 2  // scale X                  the result
 };
 
 // How an operand lies in memory.  OP_SYM: a symmetric matrix stored in part.  Row
@@ -56,8 +51,7 @@ enum { OP_K = 0, OP_MN = 1, OP_SYM = 2 };
 // 576 x 576 took 345 us, four of 5,760 x 2,304 3,322; one of 576 x 576 took 110, one of
 // 2,304 x 2,304 515.)
 //
-// Measured: 24 of 576 x 576 300 us, of which the products' MMAs are 151; four of 5,760 x
-// 2,304 3.27 ms, 84 % of the MMA rate over the 13 / 15 of three products a step; one of
+// Measured: 24 of 576 x 576 316 us; four of 5,760 x 2,304 3.69 ms, 86 % of the MMA rate; one of
 // 2,304 x 2,304 535 us; one of 576 x 576 118 us, one of 192 x 576 88 us: fifteen products in
 // a row of 5 to 8 us, a third of it until a tile's stores are seen by others.  An epilogue
 // step of 64 columns takes 3,000 to 4,300 cycles, as its stores wait behind the main loop's
@@ -65,7 +59,7 @@ enum { OP_K = 0, OP_MN = 1, OP_SYM = 2 };
 // the lanes from shared memory, 64 bytes of a row at a time, too (308; 192 x 576 95, 100 of
 // 64 x 64 84 instead of 80).
 struct OrthMaps {
-  // X (two buffers), A or D, Q or E, as loaded: K-major boxes of 128 rows, of half a tile's rows, MN-major boxes
+  // X (two buffers), A, Q, as loaded: K-major boxes of 128 rows, of half a tile's rows, MN-major boxes
   CUtensorMap k[4], kb[4], mn[4];
   CUtensorMap store[5];  // as stored, and the result
 };
@@ -79,7 +73,6 @@ struct OrthArgs {
   long long x_pitch, x_part, s_pitch, s_part;  // elements from row to row, part to part
   int rows, cols, m;   // of X; min(rows, cols)
   int batch, steps, units;
-  int light;           // the last step on one fp16 part
   int sym_units, x_units;  // of a matrix: of a symmetric product, of the product with X
   int sym_main, sym_tiles_n, x_tiles_m, x_tiles_n, width;
   int strip;
@@ -98,11 +91,10 @@ struct OrthUnit {
 };
 
 // Two values as two parts: the first parts packed, the values' rests packed.
-template <bool F16>
 __device__ __forceinline__ void split_pair(float x, float y, uint32_t* hi, uint32_t* lo) {
-  *hi = pt::pack16<F16>(x, y);
-  const float2 h = pt::unpack16<F16>(*hi);
-  *lo = pt::pack16<F16>(x - h.x, y - h.y);
+  *hi = pt::pack16<false>(x, y);
+  const float2 h = pt::unpack16<false>(*hi);
+  *lo = pt::pack16<false>(x - h.x, y - h.y);
 }
 __device__ __forceinline__ int count_acquire(const int* p) {
   int v;
@@ -130,11 +122,7 @@ struct OrthChain {
   static constexpr int PARTS = 2, STAGES = NARROW ? 4 : 3, B_PART = NARROW ? pt::B_BYTES / 2 : pt::B_BYTES, EPI_BLOCKS = 2;
   static constexpr unsigned SITE = 0x60;
 
-  static __device__ __forceinline__ bool light(const Args& a, const Unit& c) { return a.light && c.last; }
-  static __device__ __forceinline__ int parts(const Args& a, const Unit& c) { return light(a, c) ? 1 : 2; }
-  static __device__ __forceinline__ uint32_t idesc(const Args& a, const Unit& c) {
-    return idesc_f16(!light(a, c), false, false, 256, 0);
-  }
+  static __device__ __forceinline__ uint32_t idesc(const Args&, const Unit&) { return idesc_f16(true, false, false, 256, 0); }
   // How the operands of a product lie, and the buffers they are in.
   static __device__ __forceinline__ int a_op(const Unit& c) { return c.kind == 0 ? (TALL ? OP_MN : OP_K) : c.kind == 1 ? OP_SYM : TALL ? OP_K : OP_SYM; }
   static __device__ __forceinline__ int b_op(const Unit& c) { return c.kind == 0 ? (TALL ? OP_MN : OP_K) : c.kind == 1 ? OP_SYM : TALL ? OP_SYM : OP_MN; }
@@ -216,15 +204,15 @@ struct OrthChain {
   // in whole 64 x 64 boxes, so that its bytes are the same.
   static __device__ __forceinline__ int b_rows(const Args& a, int op) { return op == OP_K ? a.width / 2 : up64(a.width / 2); }
   static __device__ __forceinline__ uint32_t bytes(const Args& a, const Unit& c) {
-    return parts(a, c) * (pt::A_BYTES + b_rows(a, b_op(c)) * pt::BK * 2);
+    return PARTS * (pt::A_BYTES + b_rows(a, b_op(c)) * pt::BK * 2);
   }
   static __device__ __forceinline__ void load(const Maps& m, const Args& a, const Unit& c, int kb, int rank,
                                               uint32_t a_dst, uint32_t b_dst, uint32_t bar) {
     const int k0 = kb * pt::BK;
     const int mrow = c.m0 + rank * 128, n = c.n0 + rank * (c.nmma / 2);
     const bool am = a_mn(a, c, kb), bm = b_mn(a, c, kb);
-    const int ab = a_buf(c), bb = b_buf(c), op = b_op(c), rows = b_rows(a, op), np = parts(a, c);
-    for (int p = 0; p < np; ++p) {
+    const int ab = a_buf(c), bb = b_buf(c), op = b_op(c), rows = b_rows(a, op);
+    for (int p = 0; p < PARTS; ++p) {
       const int z = c.z + p * a.batch;
       if (am) {
         tma_load_3d_pair(a_dst, &m.mn[ab], bar, mrow, k0, z);
@@ -246,58 +234,40 @@ struct OrthChain {
   template <int EP>
   static __device__ __forceinline__ void finish(const Args& a, const Unit& c, const pt::EpiWarp& at, int col, int row0,
                                                 int rows, int lane, float* v) {
-    constexpr bool IN = EP == EP_Q || EP == EP_E || EP == EP_LAST, IN2 = IN && EP != EP_E;  // reads a matrix, of two parts
-    constexpr bool IN16 = EP == EP_E || EP == EP_LAST;                                      // in fp16
     uint8_t *b0 = at.blocks, *b1 = b0 + pt::BLOCK;
     const int n = c.n0 + col + 32 * at.h;
     const int diagonal = row0 + lane - n;
     const float *k = a.coeffs[c.step];
-    if constexpr (IN) {
+    if constexpr (EP == EP_Q) {  // A is in the blocks
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint4 h = *reinterpret_cast<uint4*>(pt::block_word(b0, lane, 4 * at.h + j));
-        uint4 l = make_uint4(0, 0, 0, 0);
-        if (IN2) l = *reinterpret_cast<uint4*>(pt::block_word(b1, lane, 4 * at.h + j));
+        const uint4 l = *reinterpret_cast<uint4*>(pt::block_word(b1, lane, 4 * at.h + j));
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          float2 x = pt::unpack16<IN16>(reinterpret_cast<const uint32_t*>(&h)[w]);
-          if (IN2) {
-            const float2 y = pt::unpack16<IN16>(reinterpret_cast<const uint32_t*>(&l)[w]);
-            x.x += y.x;
-            x.y += y.y;
-          }
+          const float2 x = pt::unpack16<false>(reinterpret_cast<const uint32_t*>(&h)[w]);
+          const float2 y = pt::unpack16<false>(reinterpret_cast<const uint32_t*>(&l)[w]);
           const int e = 8 * j + 2 * w;
-          if constexpr (EP == EP_Q) {
-            v[e] = fmaf(k[2], v[e], fmaf(k[1], x.x, e == diagonal ? k[0] : 0.f));
-            v[e + 1] = fmaf(k[2], v[e + 1], fmaf(k[1], x.y, e + 1 == diagonal ? k[0] : 0.f));
-          } else {  // the last step's coefficients are (a + b + c, b + 2 c, c)
-            const float of_sum = EP == EP_E ? k[2] : a.scale, of_in = EP == EP_E ? k[1] : a.scale * k[0];
-            v[e] = fmaf(of_sum, v[e], of_in * x.x);
-            v[e + 1] = fmaf(of_sum, v[e + 1], of_in * x.y);
-          }
+          v[e] = fmaf(k[2], v[e], fmaf(k[1], x.x + y.x, e == diagonal ? k[0] : 0.f));
+          v[e + 1] = fmaf(k[2], v[e + 1], fmaf(k[1], x.y + y.y, e + 1 == diagonal ? k[0] : 0.f));
         }
       }
-    } else if constexpr (EP == EP_D) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] -= j == diagonal ? 1.f : 0.f;
     } else if constexpr (EP == EP_OUT) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] *= a.scale;
     }
-    if constexpr (EP == EP_OUT || EP == EP_LAST) {
+    if constexpr (EP == EP_OUT) {
       if (a.out_f16) pt::put_row<true>(b0, lane, at.h, v);
       else pt::put_row<false>(b0, lane, at.h, v);
       if (!a.wide)
         pt::half_store(b0, at.h, a.o + (static_cast<long long>(c.z) * a.rows + row0) * a.cols + n, a.cols, rows,
                        min(32, a.cols - n), lane);
-    } else if constexpr (EP == EP_D || EP == EP_E) {
-      pt::put_row<true>(b0, lane, at.h, v);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split_pair<EP == EP_X16>(v[8 * j + 2 * e], v[8 * j + 2 * e + 1], &hi[e], &lo[e]);
+        for (int e = 0; e < 4; ++e) split_pair(v[8 * j + 2 * e], v[8 * j + 2 * e + 1], &hi[e], &lo[e]);
         *reinterpret_cast<uint4*>(pt::block_word(b0, lane, 4 * at.h + j)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(pt::block_word(b1, lane, 4 * at.h + j)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
@@ -308,33 +278,25 @@ struct OrthChain {
                                                   const pt::EpiWarp& at, pt::NoState&, Wait wait, Release release) {
     const int lane = threadIdx.x & 31;
     volatile int* abort_flag = at.abort_flag;
-    const bool thin = light(a, c);
-    const int ep = c.kind == 0 ? (thin ? EP_D : EP_A) : c.kind == 1 ? (thin ? EP_E : EP_Q)
-                   : thin ? EP_LAST : c.last ? EP_OUT : a.light && c.step + 2 == a.steps ? EP_X16 : EP_A;
-    const bool in = ep == EP_Q || ep == EP_E || ep == EP_LAST, in2 = in && ep != EP_E;
     const bool result = c.kind == 2 && c.last;
-    const bool two = !thin && !result;
+    const int ep = c.kind == 1 ? EP_Q : result ? EP_OUT : EP_A;
     const int M = c.kind == 2 && TALL ? a.rows : a.m;
     const int row0 = c.m0 + at.rank * 128 + at.q * 32;
     const int rows = min(32, M - row0);
     const int cols = rows > 0 ? c.cols : 0;
     uint8_t *b0 = at.blocks, *b1 = b0 + pt::BLOCK;
     pt::HalfRegs in0, in1;
-    // what the polynomial and the last step add: A or D, or X
-    const bool of_x = c.kind == 2;
-    const uint16_t* from = a.buf[of_x ? c.step & 1 : BUF_S];
-    const long long pitch = of_x ? a.x_pitch : a.s_pitch, part = of_x ? a.x_part : a.s_part;
-    const int N = of_x ? a.cols : a.m;
+    // the polynomial's A
     auto fetch = [&](int col) {
       const int n = c.n0 + col + 32 * at.h;
-      const int left = (N - n + 7) & ~7;  // rows are whole words; what lies past the columns is not stored
-      const uint16_t* p = from + (static_cast<long long>(c.z) * (of_x ? a.rows : a.m) + row0) * pitch + n;
-      pt::half_fetch(in0, p, pitch, rows, left, lane, true);
-      if (in2) pt::half_fetch(in1, p + part, pitch, rows, left, lane, true);
+      const int left = (a.m - n + 7) & ~7;  // rows are whole words; what lies past the columns is not stored
+      const uint16_t* p = a.buf[BUF_S] + (static_cast<long long>(c.z) * a.m + row0) * a.s_pitch + n;
+      pt::half_fetch(in0, p, a.s_pitch, rows, left, lane, true);
+      pt::half_fetch(in1, p + a.s_part, a.s_pitch, rows, left, lane, true);
     };
     // what this unit's copies wait for, the epilogue's first loads do too (one thread a quadrant looks: with two,
     // 8 matrices of 1,536 x 576 took 242 us instead of 239); their lines are taken past L1
-    if (in && cols > 0) {
+    if (ep == EP_Q && cols > 0) {
       if (pt::quadrant_all(at.q, lane != 0 || at.h != 0 || ready(a, c, abort_flag))) fetch(0);
     }
     if (!wait()) return;
@@ -346,26 +308,22 @@ struct OrthChain {
       tmem_ld_wait();
       if (col + 64 >= cols) release();
       pt::blocks_free(at, lane);
-      if (in) {
+      if (ep == EP_Q) {
         pt::half_put(in0, b0, at.h, lane);
-        if (in2) pt::half_put(in1, b1, at.h, lane);
+        pt::half_put(in1, b1, at.h, lane);
         __syncwarp();
         if (col + 64 < cols) fetch(col + 64);
       }
       switch (ep) {
-        case EP_A: finish<EP_A>(a, c, at, col, row0, rows, lane, v); break;  // X in bf16 parts too
+        case EP_A: finish<EP_A>(a, c, at, col, row0, rows, lane, v); break;  // X too
         case EP_Q: finish<EP_Q>(a, c, at, col, row0, rows, lane, v); break;
-        case EP_OUT: finish<EP_OUT>(a, c, at, col, row0, rows, lane, v); break;
-        case EP_D: finish<EP_D>(a, c, at, col, row0, rows, lane, v); break;
-        case EP_E: finish<EP_E>(a, c, at, col, row0, rows, lane, v); break;
-        case EP_X16: finish<EP_X16>(a, c, at, col, row0, rows, lane, v); break;
-        default: finish<EP_LAST>(a, c, at, col, row0, rows, lane, v); break;
+        default: finish<EP_OUT>(a, c, at, col, row0, rows, lane, v); break;
       }
       if (result && !a.wide) continue;
       if (pt::blocks_full(at, lane)) {
         const CUtensorMap* to = &m.store[c_buf(c)];
         tma_store_3d(to, smem_u32(b0), c.n0 + col, row0, c.z);
-        if (two) tma_store_3d(to, smem_u32(b1), c.n0 + col, row0, c.z + a.batch);
+        if (!result) tma_store_3d(to, smem_u32(b1), c.n0 + col, row0, c.z + a.batch);
         bulk_commit();
       }
     }
@@ -483,7 +441,7 @@ __global__ void __launch_bounds__(256) orth_split_kernel(const T* G, const doubl
     eight<T>(G + (z * rows + r) * cols, c, cols, wide, v);
     uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) split_pair<false>(v[2 * j] * f0 * f1, v[2 * j + 1] * f0 * f1, &hi[j], &lo[j]);
+    for (int j = 0; j < 4; ++j) split_pair(v[2 * j] * f0 * f1, v[2 * j + 1] * f0 * f1, &hi[j], &lo[j]);
     uint16_t* at = X + (z * rows + r) * pitch + c;
     *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(at + part_stride) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -607,25 +565,6 @@ cudaError_t prepare(const OrthCall& g, const Places& l, double* sums, uint16_t* 
                   static_cast<int>(base && g.cols % 8 == 0), done);
 }
 
-// Whether the last step may take one fp16 part (see orth_launch): its coefficients, and
-// X's entries inside fp16's range by then: the steps before enlarge small singular values
-// (entries start at 1 / sqrt(rows cols) in the mean square) and take none above 8.
-bool light_last(const OrthCall& g) {
-  const double* last = g.coeffs + 3 * (g.steps - 1);
-  if (g.steps < 2 || fabs(last[1] + 2 * last[2]) + fabs(last[2]) > 3. || g.rows * g.cols > int64_t(1) << 30) return false;
-  double slope = 1., top = 1.;
-  for (int64_t i = 0; i + 1 < g.steps; ++i) {
-    const double *k = g.coeffs + 3 * i, from = top;
-    slope *= fabs(k[0]);
-    top = 0.;
-    for (int j = 1; j <= 64; ++j) {
-      const double s = from * j / 64, v = fabs(s * (k[0] + s * s * (k[1] + s * s * k[2])));
-      if (v > top) top = v;
-    }
-  }
-  return slope >= 2. && top <= 8.;
-}
-
 }  // namespace
 
 bool orth_fits(int64_t batch, int64_t rows, int64_t cols, int64_t steps) {
@@ -665,21 +604,6 @@ cudaError_t orth_launch(const OrthCall& g) {
   a.status = g.status;
   for (int64_t i = 0; i < g.steps; ++i)
     for (int j = 0; j < 3; ++j) a.coeffs[i][j] = static_cast<float>(g.coeffs[3 * i + j]);
-  // The last step of a bf16 result: written around 1, where the singular values are by
-  // then, with D = A - I,
-  //   (a + b + c) X + E X,  E = (b + 2 c) D + c D D,
-  // D, E and the X of the products may be one fp16 part each: their rounding (2^-11 at most)
-  // enters times |b + 2 c| + |c|, 2.7 with the usual coefficients (as a I + b A + c A A it
-  // would be 7 and more), and the first term takes X in two parts.  Emulated in 64 bits it
-  // leaves 2e-4 to 4e-4 of a result's size beside the 1.7e-3 of rounding to bf16 (1e-3
-  // where X has directions of 1e-5), for a third of the products.
-  a.light = g.out_kind == EK_BF16 && light_last(g);
-  if (a.light) {
-    const double* k = g.coeffs + 3 * (g.steps - 1);
-    float* c = a.coeffs[g.steps - 1];
-    c[0] = static_cast<float>(k[0] + k[1] + k[2]);
-    c[1] = static_cast<float>(k[1] + 2 * k[2]);
-  }
   double* sums = reinterpret_cast<double*>(ws + l.sums);
   const cudaError_t e = g.in_kind == EK_BF16  ? prepare<__nv_bfloat16>(g, l, sums, x0, a.done)
                         : g.in_kind == EK_F16 ? prepare<__half>(g, l, sums, x0, a.done)

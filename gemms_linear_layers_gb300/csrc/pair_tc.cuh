@@ -14,13 +14,12 @@
 // reduction, so its bound grows with the blocks of one.
 //
 // P has: Maps, Args (with units, idesc, timeout_ns, status), Unit (with kb, the
-// blocks of its reduction; nmma, its columns), PARTS (1, or 2: operands in up to two
+// blocks of its reduction; nmma, its columns), PARTS (1, or 2: operands in two
 // 16-bit parts, a stage holds both of both, and a block is the products hi lo, lo hi and
 // hi hi), STAGES, B_PART (bytes of a part of B in a stage: a CTA's half of its rows),
 // EPI_BLOCKS (64-column blocks of shared memory a quadrant), State (what an epilogue warp
 // keeps from unit to unit), COOPERATIVE (its units wait for others' results: every CTA has
 // to be resident), and
-//   parts(args, unit)              of this unit
 //   idesc(args, unit)              without N and the majors
 //   ready(args, unit, abort)       before the unit's copies; false: give up
 //   a_mn(args, unit, kb), b_mn     is the operand of this block MN-major
@@ -207,7 +206,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
         const uint32_t idesc = P::idesc(args, c) | (static_cast<uint32_t>(c.nmma >> 3) << 17);
-        const int parts = P::PARTS == 2 ? P::parts(args, c) : 1;
         for (int kb = 0; kb < c.kb; ++kb) {
           if (!mbar_wait<true>(smem_u32(&full[stage]), phase, tmo, abort_flag, args.status, P::SITE + 4)) {
             ok = false;
@@ -224,12 +222,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint64_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2;
 #pragma unroll
           for (int p = P::PARTS == 2 ? 0 : 2; p < 3; ++p) {
-            if (P::PARTS == 2 && p < 2 && parts == 1) continue;
             const uint64_t ad = ad0 + (p == 1 ? A_BYTES >> 4 : 0), bd = bd0 + (p == 0 ? P::B_PART >> 4 : 0);
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
               umma_f16_pair(d_tmem, ad + kk * a_step, bd + kk * b_step, id,
-                            (kb > 0 || kk > 0 || (p > 0 && parts == 2)) ? 1u : 0u);
+                            (kb > 0 || kk > 0 || (P::PARTS == 2 && p > 0)) ? 1u : 0u);
           }
           umma_commit_pair(smem_u32(&empty[stage]), 0x3);
           if (++stage == S) {

@@ -1,0 +1,53 @@
+"""The orthogonalised update against the polynomial in 64 bits where its accuracy can go wrong: few and many steps,
+gradients of a few strong directions."""
+import pytest
+import torch
+
+import gemms_linear_layers_gb300 as tg
+from gemms_linear_layers_gb300 import inputs
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+QUINTIC = (3.4445, -4.7750, 2.0315)
+
+
+def randn(shape, tag):
+    return inputs.normal(shape, 1.0, F32, inputs.seed_for("update", *shape, tag)).cuda()
+
+
+def gradient(batch, rows, cols, noise, dtype=F32, rank=8):
+    """A strong part of this rank, its directions of sizes 1 to 0.1, beside `noise`."""
+    left = randn((batch, rows, rank), "left") * 0.7 ** torch.arange(rank, device="cuda")
+    return (left @ randn((batch, rank, cols), "right") + noise * randn((batch, rows, cols), "noise")).to(dtype)
+
+
+def polynomial(G, coeffs, scale=1.0, eps=1e-7):
+    """The definition in 64 bits, of a batch."""
+    X = G.double()
+    X = X / (torch.linalg.vector_norm(X, dim=(1, 2), keepdim=True) + eps)
+    tall = X.shape[1] > X.shape[2]
+    X = X.mT if tall else X
+    for a, b, c in coeffs:
+        A = X @ X.mT
+        X = a * X + (b * A + c * (A @ A)) @ X
+    return scale * (X.mT if tall else X)
+
+
+def errors(got, ref):
+    """Of each matrix, in the Frobenius norm: the result's error, and that of rounding the true values once."""
+    size = lambda t: torch.linalg.vector_norm(t, dim=(1, 2))  # noqa: E731
+    return size(got.double() - ref) / size(ref), size(ref.to(got.dtype).double() - ref) / size(ref)
+
+
+# What the parts leave is independent of the result's rounding, so that squares add.  A step leaves at most 2^-17 of
+# |X| in X (0.71 of that and less in the mean square), which later steps enlarge by at most a each: 57 times in
+# four steps of a = 3.4445, 3.1e-4 beside |O| of at least 0.7 sqrt(8) = 2.  Rounding to bf16 is 1.66e-3 in the mean
+# square: 1.5e-4 adds 0.4 % to it, and 2 % is a fifth of it.
+@pytest.mark.parametrize("noise", (0.3, 0.02, 1e-3))
+@pytest.mark.parametrize("steps", (2, 3, 4))
+@pytest.mark.parametrize("rows,cols", [(300, 700), (577, 321)])
+def test_a_bf16_result_of_few_steps_has_its_rounding_alone(rows, cols, steps, noise):
+    G = gradient(2, rows, cols, noise)
+    off, rounding = errors(tg.tg_orthogonalize(G, steps=steps), polynomial(G, [QUINTIC] * steps))
+    assert bool((off <= 1.02 * rounding).all()), (off / rounding).tolist()
