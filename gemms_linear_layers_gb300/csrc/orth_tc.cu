@@ -5,19 +5,30 @@
 // which takes every singular value s of X to a s + b s^3 + c s^5 and so all of
 // them towards 1, and O = scale X.
 //
-// Everything between the products is held as two bf16 parts, v = hi + lo to
-// within 2^-17 |v|, and a product is the three products hi lo + lo hi + hi hi in
-// one FP32 accumulator.  One 16-bit part would not do: rounding spreads over all
-// directions alike, and a direction that the gradient barely has is multiplied
-// by a^steps (485 for five steps of a = 3.44) on its way to 1, the rounding of the
-// strong directions with it.  Relative to |X| = 1 the parts leave about
-// 2^-18 |x|, or 5e-5 of a result's entries after that, below half a unit of fp16.
+// Everything between the products is held as two fp16 parts, v = hi + lo, and a product is
+// the three products hi lo + lo hi + hi hi in one FP32 accumulator.  One 16-bit part would
+// not do: rounding spreads over all directions alike, and a direction that the gradient
+// barely has is multiplied by a^steps (485 for five steps of a = 3.44) on its way to 1, the
+// rounding of the strong directions with it.  Two bf16 parts (2^-17) fell short too where eight
+// strong directions stand beside others of 1e-3: 7e-4 of a result's size after five steps and
+// 2.3e-3 after six (300 x 700), beside 2.1e-4 of rounding to fp16.  Two fp16 parts hold 22 bits
+// where a value's size lets them, so X, A and Q are stored times powers of two that bring the
+// largest they can be to 2^15 (see Ranges): what is lost is 2^-22 of a value or 2^-40 of that
+// bound, 1.5e-5 and 4e-5 of those results when emulated with exact sums.  The rest is the tensor
+// cores' FP32 sums, which cut off what lies below their last bit.  Measured, of a result's size
+// beside its own rounding, others of 0.3 / 1e-3 after five steps: 300 x 700 1.2e-5 / 8e-5,
+// 576 x 576 1.6e-5 / 1.4e-4, 2,304 x 2,304 2.7e-5 / 6e-4; after six, of 1e-3, 2.6e-4, 4.8e-4 and
+// 1.9e-3.  (FP32 products: 2e-6 / 3e-5, 2e-6 / 4e-5, 3e-6 / 9e-5; 1.0e-4, 1.3e-4, 2.8e-4.  Against
+// bf16 parts fp16 cost 6 % for four of 5,760 x 2,304, power, and 1 % and less below.  The sums of
+// hi hi apart from the others' left no less after five steps; a X added beside the sum instead of
+// a I within it left half, for 10 % of 8 x 1,536 x 576.)
 // A and Q are symmetric: only tiles that reach the diagonal or lie below it are
 // computed and stored; an operand's block above it is loaded from below, where it is
 // the same block MN-major, and the instruction is told so block by block.
 // A tall G needs no transpose: its A is the product of MN-major operands, its
 // X Q takes the symmetric Q as a K-major one.
 #include <cmath>
+#include <type_traits>
 
 #include "orth.h"
 
@@ -33,6 +44,25 @@ enum {
   EP_Q = 1,   // Q = a I + b A + c sum    two parts, symmetric
   EP_OUT = 2  // scale X                  the result
 };
+
+constexpr int MAX_STEPS = 64;
+
+// Powers of two that the parts are scaled with.  X of step i is stored times 2^(bits - e_i), A
+// times 2^(bits - 2 e_i), Q times 2^(bits - q_i), where 2^e_i is not below X's spectral norm
+// (which no entry exceeds) and 2^q_i not below |a + b s^2 + c s^4| for the s that X can have.
+// e_0 is a matrix's own, from |G| / (|G| + eps); e_(i+1) = min(x_(i+1), e_i + q_i), x_i the
+// bound that holds for every matrix.  Coefficients that let X's size move too far from its
+// bound for fp16 (through a zero of the polynomial, or by growing without limit) take bf16
+// parts, unscaled (bits = 0, all exponents 0), of 2^-17.
+struct Ranges {
+  int f16, bits;
+  signed char x[MAX_STEPS + 1], q[MAX_STEPS];
+};
+__host__ __device__ inline int next_range(const Ranges& r, int i, int e) {
+  const int grown = e + r.q[i];
+  return grown < r.x[i + 1] ? grown : r.x[i + 1];
+}
+constexpr int LEAST_RANGE = -100;  // of a matrix that eps leaves next to nothing of
 
 // How an operand lies in memory.  OP_SYM: a symmetric matrix stored in part.  Row
 // tile i (256 rows) of it holds its columns before 256 (i + 1), and the rest is taken
@@ -51,8 +81,8 @@ enum { OP_K = 0, OP_MN = 1, OP_SYM = 2 };
 // 576 x 576 took 345 us, four of 5,760 x 2,304 3,322; one of 576 x 576 took 110, one of
 // 2,304 x 2,304 515.)
 //
-// Measured: 24 of 576 x 576 316 us; four of 5,760 x 2,304 3.69 ms, 86 % of the MMA rate; one of
-// 2,304 x 2,304 535 us; one of 576 x 576 118 us, one of 192 x 576 88 us: fifteen products in
+// Measured: 24 of 576 x 576 308 us; four of 5,760 x 2,304 3.87 ms, 82 % of the MMA rate; one of
+// 2,304 x 2,304 583 us; one of 576 x 576 117 us, one of 192 x 576 88 us: fifteen products in
 // a row of 5 to 8 us, a third of it until a tile's stores are seen by others.  An epilogue
 // step of 64 columns takes 3,000 to 4,300 cycles, as its stores wait behind the main loop's
 // copies.  Stores straight from registers were slower still (24 of 576 x 576 378 us), stores by
@@ -65,10 +95,10 @@ struct OrthMaps {
 };
 enum { BUF_S = 2, BUF_Q = 3, BUF_O = 4 };  // 0, 1: X
 
-constexpr int MAX_STEPS = 64;
 struct OrthArgs {
   const uint16_t* buf[4];
   int* done;           // [batch] blocks of 32 rows of tiles that have been stored: 8 a unit
+  const int* range0;   // [batch] e_0
   uint16_t* o;
   long long x_pitch, x_part, s_pitch, s_part;  // elements from row to row, part to part
   int rows, cols, m;   // of X; min(rows, cols)
@@ -81,7 +111,8 @@ struct OrthArgs {
   float scale;
   unsigned long long timeout_ns;
   unsigned int* status;
-  float coeffs[MAX_STEPS][3];
+  float coeffs[MAX_STEPS][3];  // a, b, c times 2^(bits - q), 2^-q, 2^(-bits - q)
+  Ranges range;
 };
 struct OrthUnit {
   int step, kind;  // kind 0: A, 1: Q, 2: X
@@ -91,11 +122,14 @@ struct OrthUnit {
 };
 
 // Two values as two parts: the first parts packed, the values' rests packed.
+template <bool F16>
 __device__ __forceinline__ void split_pair(float x, float y, uint32_t* hi, uint32_t* lo) {
-  *hi = pt::pack16<false>(x, y);
-  const float2 h = pt::unpack16<false>(*hi);
-  *lo = pt::pack16<false>(x - h.x, y - h.y);
+  *hi = pt::pack16<F16>(x, y);
+  const float2 h = pt::unpack16<F16>(*hi);
+  *lo = pt::pack16<F16>(x - h.x, y - h.y);
 }
+// 2^n, 0 below FP32's normal range
+__device__ __forceinline__ float power_of_two(int n) { return n < -126 ? 0.f : __int_as_float((n + 127) << 23); }
 __device__ __forceinline__ int count_acquire(const int* p) {
   int v;
   asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -122,7 +156,9 @@ struct OrthChain {
   static constexpr int PARTS = 2, STAGES = NARROW ? 4 : 3, B_PART = NARROW ? pt::B_BYTES / 2 : pt::B_BYTES, EPI_BLOCKS = 2;
   static constexpr unsigned SITE = 0x60;
 
-  static __device__ __forceinline__ uint32_t idesc(const Args&, const Unit&) { return idesc_f16(true, false, false, 256, 0); }
+  static __device__ __forceinline__ uint32_t idesc(const Args& a, const Unit&) {
+    return idesc_f16(!a.range.f16, false, false, 256, 0);
+  }
   // How the operands of a product lie, and the buffers they are in.
   static __device__ __forceinline__ int a_op(const Unit& c) { return c.kind == 0 ? (TALL ? OP_MN : OP_K) : c.kind == 1 ? OP_SYM : TALL ? OP_K : OP_SYM; }
   static __device__ __forceinline__ int b_op(const Unit& c) { return c.kind == 0 ? (TALL ? OP_MN : OP_K) : c.kind == 1 ? OP_SYM : TALL ? OP_SYM : OP_MN; }
@@ -231,30 +267,30 @@ struct OrthChain {
   }
 
   // What EP makes of the accumulator's 64 columns from `col` on, into the quadrant's blocks.
-  template <int EP>
+  // k: what the unit matrix, A and the sum are taken times; without a polynomial k.x is the sum's factor.
+  template <int EP, bool F16>
   static __device__ __forceinline__ void finish(const Args& a, const Unit& c, const pt::EpiWarp& at, int col, int row0,
-                                                int rows, int lane, float* v) {
+                                                int rows, int lane, const float3& k, float* v) {
     uint8_t *b0 = at.blocks, *b1 = b0 + pt::BLOCK;
     const int n = c.n0 + col + 32 * at.h;
-    const int diagonal = row0 + lane - n;
-    const float *k = a.coeffs[c.step];
     if constexpr (EP == EP_Q) {  // A is in the blocks
+      const int diagonal = row0 + lane - n;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint4 h = *reinterpret_cast<uint4*>(pt::block_word(b0, lane, 4 * at.h + j));
         const uint4 l = *reinterpret_cast<uint4*>(pt::block_word(b1, lane, 4 * at.h + j));
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const float2 x = pt::unpack16<false>(reinterpret_cast<const uint32_t*>(&h)[w]);
-          const float2 y = pt::unpack16<false>(reinterpret_cast<const uint32_t*>(&l)[w]);
+          const float2 x = pt::unpack16<F16>(reinterpret_cast<const uint32_t*>(&h)[w]);
+          const float2 y = pt::unpack16<F16>(reinterpret_cast<const uint32_t*>(&l)[w]);
           const int e = 8 * j + 2 * w;
-          v[e] = fmaf(k[2], v[e], fmaf(k[1], x.x + y.x, e == diagonal ? k[0] : 0.f));
-          v[e + 1] = fmaf(k[2], v[e + 1], fmaf(k[1], x.y + y.y, e + 1 == diagonal ? k[0] : 0.f));
+          v[e] = fmaf(k.z, v[e], fmaf(k.y, x.x + y.x, e == diagonal ? k.x : 0.f));
+          v[e + 1] = fmaf(k.z, v[e + 1], fmaf(k.y, x.y + y.y, e + 1 == diagonal ? k.x : 0.f));
         }
       }
-    } else if constexpr (EP == EP_OUT) {
+    } else {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] *= a.scale;
+      for (int j = 0; j < 32; ++j) v[j] *= k.x;
     }
     if constexpr (EP == EP_OUT) {
       if (a.out_f16) pt::put_row<true>(b0, lane, at.h, v);
@@ -267,7 +303,7 @@ struct OrthChain {
       for (int j = 0; j < 4; ++j) {
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split_pair(v[8 * j + 2 * e], v[8 * j + 2 * e + 1], &hi[e], &lo[e]);
+        for (int e = 0; e < 4; ++e) split_pair<F16>(v[8 * j + 2 * e], v[8 * j + 2 * e + 1], &hi[e], &lo[e]);
         *reinterpret_cast<uint4*>(pt::block_word(b0, lane, 4 * at.h + j)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(pt::block_word(b1, lane, 4 * at.h + j)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
@@ -280,6 +316,22 @@ struct OrthChain {
     volatile int* abort_flag = at.abort_flag;
     const bool result = c.kind == 2 && c.last;
     const int ep = c.kind == 1 ? EP_Q : result ? EP_OUT : EP_A;
+    // the factors between what is stored: see Ranges
+    const int bits = a.range.bits;
+    float3 k = make_float3(power_of_two(-bits), 0.f, 0.f);
+    if (c.kind > 0) {
+      int e = a.range0[c.z];
+      for (int i = 0; i < c.step; ++i) e = next_range(a.range, i, e);
+      const int q = a.range.q[c.step];
+      if (c.kind == 1) {
+        const float* p = a.coeffs[c.step];
+        k = make_float3(p[0], p[1] * power_of_two(2 * e), p[2] * power_of_two(4 * e));
+      } else if (result) {  // in two factors: the first keeps the second within FP32's range
+        k.x = power_of_two(-2 * bits) * (a.scale * power_of_two(q + e));
+      } else {
+        k.x = power_of_two(e - next_range(a.range, c.step, e) + q - bits);
+      }
+    }
     const int M = c.kind == 2 && TALL ? a.rows : a.m;
     const int row0 = c.m0 + at.rank * 128 + at.q * 32;
     const int rows = min(32, M - row0);
@@ -314,11 +366,14 @@ struct OrthChain {
         __syncwarp();
         if (col + 64 < cols) fetch(col + 64);
       }
-      switch (ep) {
-        case EP_A: finish<EP_A>(a, c, at, col, row0, rows, lane, v); break;  // X too
-        case EP_Q: finish<EP_Q>(a, c, at, col, row0, rows, lane, v); break;
-        default: finish<EP_OUT>(a, c, at, col, row0, rows, lane, v); break;
-      }
+      auto parts = [&](auto f16) {
+        constexpr bool F16 = decltype(f16)::value;
+        if (ep == EP_Q) finish<EP_Q, F16>(a, c, at, col, row0, rows, lane, k, v);
+        else finish<EP_A, F16>(a, c, at, col, row0, rows, lane, k, v);  // X too
+      };
+      if (result) finish<EP_OUT, true>(a, c, at, col, row0, rows, lane, k, v);
+      else if (a.range.f16) parts(std::true_type());
+      else parts(std::false_type());
       if (result && !a.wide) continue;
       if (pt::blocks_full(at, lane)) {
         const CUtensorMap* to = &m.store[c_buf(c)];
@@ -409,22 +464,32 @@ __global__ void __launch_bounds__(NORM_THREADS) orth_norm_kernel(const T* __rest
   }
 }
 
-// X, two parts of [batch][rows][pitch], from G [batch][rows][cols].  `blocks` CTAs a matrix.
+// X, two parts of [batch][rows][pitch], from G [batch][rows][cols], and each matrix's e_0
+// (see Ranges).  `blocks` CTAs a matrix.
 template <typename T>
 __global__ void __launch_bounds__(256) orth_split_kernel(const T* G, const double* part, uint16_t* X, long long rows, int cols,
                                                          int pitch, int parts, int blocks, long long part_stride, float eps,
-                                                         int wide, int* done) {
+                                                         int wide, int* done, int* range0, int f16, int bits) {
   __shared__ float factor[2];
   pdl_wait();
   const long long z = blockIdx.x / blocks;
   const int k = static_cast<int>(blockIdx.x - z * blocks);
-  if (k == 0 && threadIdx.x == 0) done[z] = 0;
   if (threadIdx.x < 32) {
     double sum = 0.;
     for (int i = threadIdx.x; i < parts; i += 32) sum += part[z * parts + i];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    const double inv = 1. / (sqrt(sum) + static_cast<double>(eps));
+    const double norm = sqrt(sum), under = norm + static_cast<double>(eps);
+    int e = 0;
+    if (bits > 0 && norm < under) {  // |X| = norm / under < 1, at most 2^e
+      frexp(norm / under, &e);
+      e = min(0, max(LEAST_RANGE, e));
+    }
+    if (k == 0 && threadIdx.x == 0) {
+      done[z] = 0;
+      range0[z] = e;
+    }
+    const double inv = ldexp(1., bits - e) / under;
     // in two factors, the first a power of two that keeps the second within FP32's range
     const double first = inv < 1e-36 ? 0x1p-64 : inv > 1e36 ? 0x1p64 : 1.;
     factor[0] = static_cast<float>(first);
@@ -441,7 +506,10 @@ __global__ void __launch_bounds__(256) orth_split_kernel(const T* G, const doubl
     eight<T>(G + (z * rows + r) * cols, c, cols, wide, v);
     uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) split_pair(v[2 * j] * f0 * f1, v[2 * j + 1] * f0 * f1, &hi[j], &lo[j]);
+    for (int j = 0; j < 4; ++j) {
+      if (f16) split_pair<true>(v[2 * j] * f0 * f1, v[2 * j + 1] * f0 * f1, &hi[j], &lo[j]);
+      else split_pair<false>(v[2 * j] * f0 * f1, v[2 * j + 1] * f0 * f1, &hi[j], &lo[j]);
+    }
     uint16_t* at = X + (z * rows + r) * pitch + c;
     *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(at + part_stride) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -478,7 +546,7 @@ Places places(int64_t batch, int64_t rows, int64_t cols) {
   l.s = take(4 * l.s_part);
   l.q = take(4 * l.s_part);
   l.sums = take(8 * static_cast<size_t>(batch) * l.parts);
-  l.done = take(4 * static_cast<size_t>(batch));
+  l.done = take(8 * static_cast<size_t>(batch));  // and e_0
   l.bytes = at;
   return l;
 }
@@ -548,8 +616,83 @@ cudaError_t chain(const OrthCall& g, const Places& l, OrthArgs a) {
                         : pt::pair_launch<OrthChain<TALL, false>>(m, a, g.num_sms, g.stream);
 }
 
+// The polynomial of a step where X's singular values s are at most t.
+struct Span {
+  double most;  // |a + b s^2 + c s^4|, at most
+  double next;  // |a s + b s^3 + c s^5|, at most
+  bool zero;    // somewhere
+};
+Span span_of(const double* k, double t) {
+  const double a = k[0], b = k[1], c = k[2], end = t * t;
+  Span r = {0., 0., false};
+  bool above = false, below = false;
+  auto look = [&](double u, bool turns) {
+    if (!(u >= 0. && u <= end)) return;
+    const double v = a + u * (b + u * c), size = fabs(v);
+    above = above || v > 0.;
+    below = below || v < 0.;
+    r.zero = r.zero || v == 0.;
+    if (turns) r.most = fmax(r.most, size);
+    r.next = fmax(r.next, sqrt(u) * size);
+  };
+  look(0., true);
+  look(end, true);
+  if (c != 0.) look(-b / (2. * c), true);
+  // where a s + b s^3 + c s^5 turns: a + 3 b u + 5 c u^2 = 0
+  const double root = 9. * b * b - 20. * a * c;
+  if (root >= 0.) {
+    const double w = -(3. * b + copysign(sqrt(root), b)) / 2.;
+    if (c != 0.) look(w / (5. * c), false);
+    if (w != 0.) look(a / w, false);
+  }
+  r.zero = r.zero || (above && below);
+  return r;
+}
+int exponent_above(double v) {  // 2^this >= v
+  int e = 0;
+  const double m = frexp(v, &e);
+  return m == 0.5 ? e - 1 : e;
+}
+// fp16 parts where what they lose below their range (2^-25 an entry as stored, 2^-39 of the
+// bound that the scale comes from) stays under about 2^-20 of |X| whatever the matrix: X's
+// bound of each step beside what becomes of |X|, followed on singular values of four sizes an
+// octave, for each e_0.
+Ranges ranges_of(const OrthCall& g) {
+  Ranges r = {1, 15, {}, {}};
+  const int steps = static_cast<int>(g.steps);
+  const double entries = sqrt(static_cast<double>(g.rows) * static_cast<double>(g.cols));
+  double t = 1.;
+  for (int i = 0; i < steps; ++i) {
+    const Span s = span_of(g.coeffs + 3 * i, t);
+    t = s.next * (1. + 0x1p-10);  // rounding adds a little
+    if (s.zero || !(t > 0x1p-30 && t < 0x1p30 && s.most > 0x1p-30 && s.most < 0x1p30)) return Ranges{};
+    r.q[i] = static_cast<signed char>(exponent_above(s.most));
+    r.x[i + 1] = static_cast<signed char>(exponent_above(t));
+  }
+  double kept[MAX_STEPS];  // the least |X_i| / |X_0|
+  for (int i = 0; i < steps; ++i) kept[i] = HUGE_VAL;
+  const int smallest = -16;  // below, a alone counts
+  for (int e0 = smallest; e0 <= 0; ++e0) {
+    for (const double part : {1., 0.841, 0.707, 0.595}) {
+      const double from = ldexp(part, e0);
+      double s = from;
+      for (int i = 0; i < steps; ++i) {
+        const double* k = g.coeffs + 3 * i;
+        kept[i] = fmin(kept[i], s / from);
+        s = fabs(s * (k[0] + s * s * (k[1] + s * s * k[2])));
+      }
+    }
+    const int from = e0 == smallest ? -100000 : e0;
+    for (int i = 0, e = from; i < steps; ++i) {  // |X_0| is above 2^(e_0 - 1)
+      if (!(ldexp(entries, e - from) <= 0x1p18 * kept[i])) return Ranges{};
+      e = next_range(r, i, e);
+    }
+  }
+  return r;
+}
+
 template <typename T>
-cudaError_t prepare(const OrthCall& g, const Places& l, double* sums, uint16_t* X, int* done) {
+cudaError_t prepare(const OrthCall& g, const Places& l, double* sums, uint16_t* X, int* done, const Ranges& range) {
   const int64_t n = g.rows * g.cols;
   const T* G = static_cast<const T*>(g.G);
   const bool base = reinterpret_cast<uintptr_t>(G) % 16 == 0;
@@ -562,7 +705,7 @@ cudaError_t prepare(const OrthCall& g, const Places& l, double* sums, uint16_t* 
   return launch_k(orth_split_kernel<T>, dim3(static_cast<unsigned>(g.batch * blocks)), dim3(256), 0, g.stream, G,
                   static_cast<const double*>(sums), X, static_cast<long long>(g.rows), static_cast<int>(g.cols),
                   static_cast<int>(l.pitch_x), l.parts, static_cast<int>(blocks), static_cast<long long>(l.x_part), g.eps,
-                  static_cast<int>(base && g.cols % 8 == 0), done);
+                  static_cast<int>(base && g.cols % 8 == 0), done, done + g.batch, range.f16, range.bits);
 }
 
 }  // namespace
@@ -602,12 +745,15 @@ cudaError_t orth_launch(const OrthCall& g) {
   a.out_f16 = g.out_kind == EK_F16;
   a.scale = g.scale;
   a.status = g.status;
+  a.range0 = a.done + g.batch;
+  a.range = ranges_of(g);
   for (int64_t i = 0; i < g.steps; ++i)
-    for (int j = 0; j < 3; ++j) a.coeffs[i][j] = static_cast<float>(g.coeffs[3 * i + j]);
+    for (int j = 0; j < 3; ++j)
+      a.coeffs[i][j] = static_cast<float>(ldexp(g.coeffs[3 * i + j], (1 - j) * a.range.bits - a.range.q[i]));
   double* sums = reinterpret_cast<double*>(ws + l.sums);
-  const cudaError_t e = g.in_kind == EK_BF16  ? prepare<__nv_bfloat16>(g, l, sums, x0, a.done)
-                        : g.in_kind == EK_F16 ? prepare<__half>(g, l, sums, x0, a.done)
-                                              : prepare<float>(g, l, sums, x0, a.done);
+  const cudaError_t e = g.in_kind == EK_BF16  ? prepare<__nv_bfloat16>(g, l, sums, x0, a.done, a.range)
+                        : g.in_kind == EK_F16 ? prepare<__half>(g, l, sums, x0, a.done, a.range)
+                                              : prepare<float>(g, l, sums, x0, a.done, a.range);
   if (e != cudaSuccess) return e;
   return g.rows > g.cols ? chain<true>(g, l, a) : chain<false>(g, l, a);
 }

@@ -5,6 +5,7 @@ import torch
 
 import gemms_linear_layers_gb300 as tg
 from gemms_linear_layers_gb300 import inputs
+import block_ref as R
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +52,48 @@ def test_a_bf16_result_of_few_steps_has_its_rounding_alone(rows, cols, steps, no
     G = gradient(2, rows, cols, noise)
     off, rounding = errors(tg.tg_orthogonalize(G, steps=steps), polynomial(G, [QUINTIC] * steps))
     assert bool((off <= 1.02 * rounding).all()), (off / rounding).tolist()
+
+
+# Steps of a = 3.4445 enlarge what a step leaves in X by 198 in all over five, 683 over six, beside |O| of at least 2.
+# Values are stored to 2^-22, three of them in a step, and summed in FP32: at these sizes what a step leaves is held to
+# 2^-20 of |X|.
+def left(steps):
+    return sum(3.4445 ** i for i in range(steps)) / 2 * 2.0 ** -20
+
+
+@pytest.mark.parametrize("out", (BF, HF))
+@pytest.mark.parametrize("noise", (0.02, 1e-3, 1e-4))
+@pytest.mark.parametrize("steps", (5, 6))
+@pytest.mark.parametrize("rows,cols", [(300, 700), (577, 321)])
+def test_weak_directions_keep_their_digits(rows, cols, steps, noise, out):
+    G = gradient(2, rows, cols, noise)
+    off, rounding = errors(tg.tg_orthogonalize(G, steps=steps, out_dtype=out), polynomial(G, [QUINTIC] * steps))
+    assert bool((off <= torch.hypot(rounding, torch.full_like(off, left(steps)))).all()), (off.tolist(), rounding.tolist())
+
+
+@pytest.mark.parametrize("steps", (1, 5))
+def test_each_matrix_has_its_own_size_beside_eps(steps):
+    """Gradients far below eps, of eps' size and far above it in one batch: X's norm runs from 1e-20 to 1."""
+    sizes = torch.tensor([1.0, 1e-27, 1e3, 1e-8, 3e-10, 1e-12, 0.0, 1e-18], device="cuda")
+    G = gradient(8, 130, 200, 0.02) * sizes[:, None, None]
+    got = tg.tg_orthogonalize(G, steps=steps)
+    live = sizes > 0
+    off, rounding = errors(got[live], polynomial(G[live], [QUINTIC] * steps))
+    # not by hypot: with what is left far below the rounding, the two's product over the 26,000 entries of a matrix
+    # (2 x 1.7e-3 x 1e-6 / sqrt(26,000) = 2e-11) outweighs its square (1e-12)
+    assert bool((off <= 1.02 * rounding).all()), (off / rounding).tolist()
+    assert not got[6].any()
+    for i in range(8):
+        assert torch.equal(got[i], tg.tg_orthogonalize(G[i], steps=steps))
+
+
+# Coefficients whose polynomial has a zero, or lets X grow: two bf16 parts.
+@pytest.mark.parametrize("coeffs", (((2.0, -3.0, 1.0), (3.0, -3.5, 1.25)), ((6.0, 20.0, 15.0), (1.5, 2.0, 3.0)),
+                                    ((0.0, 1.0, 0.5),), ((0.0, 0.0, 2.0), (1.0, 0.0, 0.0))))
+def test_sizes_that_coefficients_do_not_bound(coeffs):
+    G = gradient(2, 150, 90, 0.3)
+    got = tg.tg_orthogonalize(G, coeffs=coeffs, out_dtype=BF)
+    for g, o in zip(G, got):
+        ref, noise = R.orthogonalize(g, coeffs, 1.0, 1e-7, HF)  # two parts, 2^-17
+        size = torch.linalg.vector_norm(ref)
+        assert torch.linalg.vector_norm(o.double() - ref) <= noise + 2.0 ** -8 * size
