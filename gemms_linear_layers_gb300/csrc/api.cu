@@ -2111,9 +2111,12 @@ tg_status tg_orthogonalize(const void* G, void* O, int64_t batch, int64_t rows, 
   g.status = ctx->status;
   g.timeout_ns = ctx->timeout_ns;
   g.stream = static_cast<cudaStream_t>(stream);
+  OrthForm form = {};
+  g.form = &form;
   const cudaError_t e = orth_launch(g);
   record("orthogonalize tc batch=" + std::to_string(batch) + " rows=" + std::to_string(rows) + " cols=" +
-         std::to_string(cols) + " steps=" + std::to_string(steps) + " " + (e == cudaSuccess ? "ok" : cudaGetErrorString(e)));
+         std::to_string(cols) + " steps=" + std::to_string(steps) + " tiles=256x" + std::to_string(form.width) +
+         (form.f16 ? " fp16 parts " : " bf16 parts ") + (e == cudaSuccess ? "ok" : cudaGetErrorString(e)));
   return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
 }
 

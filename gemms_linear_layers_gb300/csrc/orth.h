@@ -4,6 +4,11 @@
 
 namespace tg {
 
+// How a call was carried out.
+struct OrthForm {
+  int width;  // columns of a tile
+  bool f16;   // parts in fp16
+};
 struct OrthCall {
   const void* G;
   void* O;
@@ -17,6 +22,7 @@ struct OrthCall {
   unsigned int* status;
   unsigned long long timeout_ns;
   cudaStream_t stream;
+  OrthForm* form;  // set
 };
 
 // Whether the tiles of a call can be counted (2^30 in all, 2^27 of a matrix).

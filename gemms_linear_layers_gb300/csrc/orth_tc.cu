@@ -589,6 +589,7 @@ cudaError_t chain(const OrthCall& g, const Places& l, OrthArgs a) {
     if (best == 0 || cost <= least) best = w, least = cost;
   }
   fit(best);
+  *g.form = {best, a.range.f16 != 0};
   const int64_t units = static_cast<int64_t>(a.steps) * g.batch * (2 * a.sym_units + a.x_units);
   if (units > (int64_t(1) << 30) || 8 * (units / g.batch) > (int64_t(1) << 30)) return cudaErrorInvalidValue;
   a.units = static_cast<int>(units);

@@ -520,7 +520,8 @@ tg_status tg_gated_bwd(const void* dY, const void* W_down, const void* GU, void*
  * rounding to `out` (1.7e-3 bf16, 2.1e-4 fp16).
  * Workspace: tg_workspace_size(TG_OP_ORTHOGONALIZE, batch, rows, cols, 0, in,
  * out), 16-byte aligned; its content does not matter.  Results are bitwise
- * reproducible. */
+ * reproducible; a matrix's last bits may differ in a batch of another size, as
+ * tiles are chosen for the batch. */
 tg_status tg_orthogonalize(const void* G, void* O, int64_t batch, int64_t rows, int64_t cols, const double* coeffs,
                            int64_t steps, float scale, float eps, tg_dtype in, tg_dtype out, void* ws, size_t ws_bytes,
                            void* stream);

@@ -97,3 +97,42 @@ def test_sizes_that_coefficients_do_not_bound(coeffs):
         ref, noise = R.orthogonalize(g, coeffs, 1.0, 1e-7, HF)  # two parts, 2^-17
         size = torch.linalg.vector_norm(ref)
         assert torch.linalg.vector_norm(o.double() - ref) <= noise + 2.0 ** -8 * size
+
+
+def check(got, ref, leftover, what):
+    """Each matrix against its true values: in the Frobenius norm as above, and every element within half a step of its
+    own and 2^-8 of the matrix's root mean square (a normal variable stays within 12 times its deviation, and
+    `leftover`, what the parts and sums leave of a result's size, is at most 3e-4 in these tests: 12 x 3e-4 < 2^-8)."""
+    off, rounding = errors(got, ref)
+    assert bool((off <= rounding + leftover).all()), (what, off.tolist(), rounding.tolist())
+    half = R.half_step(torch.maximum(got.double().abs(), ref.abs()), got.dtype)
+    rms = ref.square().mean((1, 2), keepdim=True).sqrt()
+    assert bool(((got.double() - ref).abs() <= half + 2.0 ** -8 * rms).all()), what
+
+
+# The kernel's instances (tiles of up to 128 columns or wider, tall or not) at each width that the rule takes on 152
+# SMs, with and without a strip of a last row tile (a smaller side of a multiple of 256 and at most 128 more), and sizes
+# off the tiles and off 8.  A changed rule has to choose its own sizes here.
+@pytest.mark.parametrize("batch,rows,cols,width", [
+    (1, 130, 200, 64), (1, 200, 130, 64), (1, 313, 331, 64), (1, 331, 313, 64), (3, 137, 333, 64),
+    (24, 252, 264, 128), (24, 264, 252, 128), (1, 374, 398, 128), (1, 398, 374, 128), (2, 1301, 1999, 128),
+    (17, 700, 700, 128), (1, 1700, 2900, 128), (1, 2901, 1699, 128),
+    (40, 130, 137, 192), (40, 191, 130, 192), (1, 2304, 2304, 192), (30, 500, 900, 192), (29, 903, 501, 192),
+    (40, 252, 398, 256), (39, 397, 255, 256), (40, 313, 398, 256), (40, 801, 264, 256), (24, 576, 576, 256),
+    (20, 1100, 513, 256), (3, 1500, 1500, 256), (6, 1401, 1003, 256), (2, 1799, 1801, 256), (16, 449, 448, 256)])
+def test_every_width_of_tiles(batch, rows, cols, width):
+    G = gradient(batch, rows, cols, 0.02)
+    got = tg.tg_orthogonalize(G, steps=3)
+    assert f"tiles=256x{width} fp16 parts" in tg.tg_last_call(), tg.tg_last_call()
+    check(got, polynomial(G, [QUINTIC] * 3), 1e-4, (batch, rows, cols))
+    # the same call gives the same bits.  A matrix alone may not: its tiles may have another width, and tiles of 192
+    # columns take other elements of the symmetric matrices from across the diagonal, where the two cross products
+    # were added in the other order
+    assert torch.equal(tg.tg_orthogonalize(G, steps=3), got)
+
+
+def test_the_large_tall_batch():
+    G = gradient(4, 5760, 2304, 0.02, BF)
+    got = tg.tg_orthogonalize(G, steps=2)
+    assert "tiles=256x256 fp16 parts" in tg.tg_last_call()
+    check(got, polynomial(G, [QUINTIC] * 2), 1e-4, "4 x 5,760 x 2,304")
