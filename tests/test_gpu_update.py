@@ -136,3 +136,27 @@ def test_the_large_tall_batch():
     got = tg.tg_orthogonalize(G, steps=2)
     assert "tiles=256x256 fp16 parts" in tg.tg_last_call()
     check(got, polynomial(G, [QUINTIC] * 2), 1e-4, "4 x 5,760 x 2,304")
+
+
+CUBIC = ((2.0, -1.5, 0.5), (1.875, -1.25, 0.375), (1.5, -0.5, 0.0))
+VARIED = ((4.0, -6.0, 2.8), (3.2, -3.0, 1.0), (2.5, -2.0, 0.6), (2.0, -1.5, 0.5), (1.875, -1.25, 0.375), (1.5, -0.5, 0.0))
+
+
+@pytest.mark.parametrize("out", (BF, HF))
+@pytest.mark.parametrize("coeffs", (CUBIC, VARIED[:2], VARIED[:4], VARIED, VARIED[::-1], (QUINTIC,) * 2 + CUBIC))
+def test_a_triple_for_each_step(coeffs, out):
+    for rows, cols in ((70, 130), (200, 90)):
+        G = gradient(2, rows, cols, 0.1)
+        got = tg.tg_orthogonalize(G, coeffs=coeffs, scale=0.5, out_dtype=out)
+        assert "fp16 parts" in tg.tg_last_call()
+        # no step here has a above 4, and a gradient of noise 0.1 has few directions below 1e-2 of its strongest
+        check(got, polynomial(G, coeffs, 0.5), 1e-4, (rows, cols))
+        assert torch.equal(got, tg.tg_orthogonalize(G, coeffs=[list(k) for k in coeffs], steps=len(coeffs), scale=0.5, out_dtype=out))
+
+
+@pytest.mark.parametrize("out", (BF, HF))
+@pytest.mark.parametrize("steps", (1, 2, 3, 4, 5, 6, 9))
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 9), (31, 33), (257, 256)])
+def test_numbers_of_steps(rows, cols, steps, out):
+    G = gradient(2, rows, cols, 0.3)
+    check(tg.tg_orthogonalize(G, steps=steps, out_dtype=out), polynomial(G, [QUINTIC] * steps), 1e-4, (rows, cols, steps))
