@@ -500,8 +500,8 @@ tg_status tg_gated_bwd(const void* dY, const void* W_down, const void* GU, void*
  * takes all of them into about [0.7, 1.2] in five.  coeffs is a HOST array of
  * 3 steps values, read before the call returns.  G has type `in` (bf16, fp16 or
  * FP32), O type `out`, bf16 or fp16 whatever `in` (not FP32: see the accuracy
- * below).  O may be G when the types agree.  The norm's squares
- * are summed in FP64 beyond groups of 8; a matrix of zeros gives zeros (not
+ * below).  O may be G when the types agree.  The norm's squares are summed in
+ * FP32 in groups of 32 and in FP64 beyond; a matrix of zeros gives zeros (not
  * numbers with eps = 0), one that holds values that are not finite gives values
  * that are not numbers, in that matrix only.  rows, cols and batch are at most
  * 2^20, a tensor has at most 2^38 elements; 1 <= steps <= 64; scale and coeffs
