@@ -383,7 +383,7 @@ cudaError_t gated_launch(const GatedCall& g, size_t* need) {
     const cudaError_t e = launch_k(pitch_copy_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, g.stream, copy[0], copy[1]);
     if (e != cudaSuccess) return e;
   }
-  if (g.T <= GATED_FEW && g.d > 0) {  // both sides measured in gated_few.cu
+  if (g.T <= GATED_FEW && g.d > 0) {
     *g.path = "few rows";
     const GatedFew f = {g.bwd, s.p[0], s.p[1], g.GU, g.H, g.out, g.T, g.f, g.d, s.pitch[0], s.pitch[1], g.act, g.in_kind, g.num_sms,
                         g.status, g.timeout_ns, g.stream};

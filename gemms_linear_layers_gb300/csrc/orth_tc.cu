@@ -77,17 +77,17 @@ enum { OP_K = 0, OP_MN = 1, OP_SYM = 2 };
 // turn.  A matrix's next product begins when every tile of its last one has been stored
 // (a counter of each matrix, in the workspace), whatever the other matrices are at, so
 // only small batches wait at a product's end.  A unit waits for units before it only, and
-// the launch is cooperative, so every wait ends.  (With a launch a product 24 matrices of
-// 576 x 576 took 345 us, four of 5,760 x 2,304 3,322; one of 576 x 576 took 110, one of
-// 2,304 x 2,304 515.)
+// the launch is cooperative, so every wait ends.  (A launch a product made 24 matrices of
+// 576 x 576 15 % slower and four of 5,760 x 2,304 1 %; one of 576 x 576 7 % faster, one of
+// 2,304 x 2,304 4 %.)
 //
-// Measured: 24 of 576 x 576 308 us; four of 5,760 x 2,304 3.87 ms, 82 % of the MMA rate; one of
-// 2,304 x 2,304 583 us; one of 576 x 576 117 us, one of 192 x 576 88 us: fifteen products in
+// Measured: 24 of 576 x 576 314 us; four of 5,760 x 2,304 3.9 ms, 81 % of the MMA rate; one of
+// 2,304 x 2,304 596 us; one of 576 x 576 118 us, one of 192 x 576 87 us: fifteen products in
 // a row of 5 to 8 us, a third of it until a tile's stores are seen by others.  An epilogue
 // step of 64 columns takes 3,000 to 4,300 cycles, as its stores wait behind the main loop's
-// copies.  Stores straight from registers were slower still (24 of 576 x 576 378 us), stores by
-// the lanes from shared memory, 64 bytes of a row at a time, too (308; 192 x 576 95, 100 of
-// 64 x 64 84 instead of 80).
+// copies.  Stores straight from registers were slower still (24 of 576 x 576 26 %), stores by
+// the lanes from shared memory, 64 bytes of a row at a time, too (3 %; 192 x 576 7 %, 100 of
+// 64 x 64 5 %).
 struct OrthMaps {
   // X (two buffers), A, Q, as loaded: K-major boxes of 128 rows, of half a tile's rows, MN-major boxes
   CUtensorMap k[4], kb[4], mn[4];
@@ -144,7 +144,7 @@ __host__ __device__ inline int sym_tiles(int i, int n_tiles, int width) {
 __host__ __device__ inline int up64(int n) { return (n + 63) / 64 * 64; }
 
 // NARROW: tiles of up to 128 columns, whose part of B needs half the place: a stage more
-// (8 of 1,536 x 576 240 -> 233.6 us, one of 576 x 576 122.6 -> 117.6).  Stages of one part (five,
+// (8 of 1,536 x 576 6 us less, now 242; one of 576 x 576 5, now 118).  Stages of one part (five,
 // and blocks for two epilogue steps beside them) cost these 13 us and 10.
 template <bool TALL, bool NARROW>
 struct OrthChain {
@@ -346,8 +346,8 @@ struct OrthChain {
       pt::half_fetch(in0, p, a.s_pitch, rows, left, lane, true);
       pt::half_fetch(in1, p + a.s_part, a.s_pitch, rows, left, lane, true);
     };
-    // what this unit's copies wait for, the epilogue's first loads do too (one thread a quadrant looks: with two,
-    // 8 matrices of 1,536 x 576 took 242 us instead of 239); their lines are taken past L1
+    // what this unit's copies wait for, the epilogue's first loads do too (one thread a quadrant looks: two
+    // cost 8 matrices of 1,536 x 576 3 us); their lines are taken past L1
     if (ep == EP_Q && cols > 0) {
       if (pt::quadrant_all(at.q, lane != 0 || at.h != 0 || ready(a, c, abort_flag))) fetch(0);
     }
