@@ -267,7 +267,7 @@ struct OrthChain {
   }
 
   // What EP makes of the accumulator's 64 columns from `col` on, into the quadrant's blocks.
-  // k: what the unit matrix, A and the sum are taken times; without a polynomial k.x is the sum's factor.
+  // k: what the unit matrix, A and the sum are taken times; without a polynomial the sum's factors.
   template <int EP, bool F16>
   static __device__ __forceinline__ void finish(const Args& a, const Unit& c, const pt::EpiWarp& at, int col, int row0,
                                                 int rows, int lane, const float3& k, float* v) {
@@ -290,7 +290,7 @@ struct OrthChain {
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] *= k.x;
+      for (int j = 0; j < 32; ++j) v[j] = EP == EP_OUT ? v[j] * k.x * k.y * k.z : v[j] * k.x;
     }
     if constexpr (EP == EP_OUT) {
       if (a.out_f16) pt::put_row<true>(b0, lane, at.h, v);
@@ -326,8 +326,8 @@ struct OrthChain {
       if (c.kind == 1) {
         const float* p = a.coeffs[c.step];
         k = make_float3(p[0], p[1] * power_of_two(2 * e), p[2] * power_of_two(4 * e));
-      } else if (result) {  // in two factors: the first keeps the second within FP32's range
-        k.x = power_of_two(-2 * bits) * (a.scale * power_of_two(q + e));
+      } else if (result) {  // X, then its scale: no product of factors may leave FP32's range
+        k = make_float3(power_of_two(-2 * bits), power_of_two(q + e), a.scale);
       } else {
         k.x = power_of_two(e - next_range(a.range, c.step, e) + q - bits);
       }

@@ -88,11 +88,12 @@ def test_each_matrix_has_its_own_size_beside_eps(steps):
 
 
 # Coefficients whose polynomial has a zero, or lets X grow: two bf16 parts.
-@pytest.mark.parametrize("coeffs", (((2.0, -3.0, 1.0), (3.0, -3.5, 1.25)), ((6.0, 20.0, 15.0), (1.5, 2.0, 3.0)),
+@pytest.mark.parametrize("coeffs", (((2.0, -3.0, 1.0), (3.0, -3.5, 1.25)), ((8.0, 30.0, 20.0), (8.0, 30.0, 20.0)),
                                     ((0.0, 1.0, 0.5),), ((0.0, 0.0, 2.0), (1.0, 0.0, 0.0))))
 def test_sizes_that_coefficients_do_not_bound(coeffs):
     G = gradient(2, 150, 90, 0.3)
     got = tg.tg_orthogonalize(G, coeffs=coeffs, out_dtype=BF)
+    assert "bf16 parts" in tg.tg_last_call()
     for g, o in zip(G, got):
         ref, noise = R.orthogonalize(g, coeffs, 1.0, 1e-7, HF)  # two parts, 2^-17
         size = torch.linalg.vector_norm(ref)
@@ -160,3 +161,38 @@ def test_a_triple_for_each_step(coeffs, out):
 def test_numbers_of_steps(rows, cols, steps, out):
     G = gradient(2, rows, cols, 0.3)
     check(tg.tg_orthogonalize(G, steps=steps, out_dtype=out), polynomial(G, [QUINTIC] * steps), 1e-4, (rows, cols, steps))
+
+
+@pytest.mark.parametrize("steps", (1, 5))
+@pytest.mark.parametrize("size,eps,scale", [(1.0, 1e-7, 1e38), (1.0, 1e-7, 1e-36), (1e-30, 1.0, 1.0), (1e-33, 1.0, 1.0), (1e-33, 1.0, -1e30),
+                                            (1e30, 1e-7, 3e37), (0.0, 1.0, 3e38)])
+def test_results_near_the_ends_of_the_range(size, eps, scale, steps):
+    """Of the gradient, of X beside a large eps, and of the result, which is a normal bf16 number here."""
+    G = gradient(2, 60, 90, 0.1) * size
+    got = tg.tg_orthogonalize(G, steps=steps, scale=scale, eps=eps)
+    ref = polynomial(G, [QUINTIC] * steps, scale, eps)
+    if size == 0.0:
+        assert not got.any()
+        return
+    assert bool(got.isfinite().all())
+    by = 1.0 / ref.abs().amax()  # the same in the middle of the range: half steps of the smallest results aside
+    off = torch.linalg.vector_norm((got.double() - ref) * by)
+    assert off <= (2.0 ** -8 + 1e-4) * torch.linalg.vector_norm(ref * by), float(off)
+
+
+@pytest.mark.parametrize("out", (BF, F32))
+@pytest.mark.parametrize("coeffs", (((100.0, 0.0, 0.0),) * 4, ((30.0, 5.0, 2.0), (2.0, 1e-4, 1e-9)), ((1e-3, 0.0, 0.0),) * 3,
+                                    ((-0.02, -0.01, -0.001), (-5.0, 100.0, 1e5), (1.5, -0.5, 0.1)), ((1e8, 1e7, 1e6),)))
+def test_growth_and_decay_that_coefficients_bound(coeffs, out):
+    if out == F32:  # of G, with a result in fp16's range
+        top = 1.0
+        for a, b, c in coeffs:
+            top = abs(a * top + b * top ** 3 + c * top ** 5)
+        G, scale, out = gradient(2, 90, 140, 0.1), 1.0 / top, HF
+    else:
+        G, scale = gradient(2, 90, 140, 0.1, BF), 1.0
+    got = tg.tg_orthogonalize(G, coeffs=coeffs, scale=scale, out_dtype=out)
+    assert "fp16 parts" in tg.tg_last_call(), tg.tg_last_call()
+    ref = polynomial(G, coeffs, scale)
+    off = torch.linalg.vector_norm(got.double() - ref, dim=(1, 2)) / torch.linalg.vector_norm(ref, dim=(1, 2))
+    assert bool((off <= torch.finfo(out).eps / 2 + 1e-4).all()), off.tolist()
